@@ -75,7 +75,8 @@ typedef enum {
                                           CUDA context should not be trusted: end the process */
 } muon_status;
 
-typedef enum { MUON_BF16 = 0, MUON_F32 = 1 } muon_dtype;
+/* MUON_F16 is taken by the stack, norm and AdamW entry points only. */
+typedef enum { MUON_BF16 = 0, MUON_F32 = 1, MUON_F16 = 2 } muon_dtype;
 
 /* Update scale for W in R^{d_out x d_in} (Muon optimizer page, section "缩放因子"). */
 typedef enum {
@@ -182,6 +183,108 @@ MUON_API size_t stiefel_workspace_size(int batch, int n, int k);
 MUON_API muon_status stiefel_cayley_step(float* W, const float* G, int batch, int n, int k, float lr,
                                 void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ stacks of blocks
+ * A stack is `count` equal rows x cols blocks of a parameter: the heads of a fused QKV weight, the
+ * experts of a mixture, the halves of a fused gate/up weight.  Element (b, i, j) of an array is at
+ * p + b * stride + i * ld + j (in elements), so blocks may be strided views.  Any size from 1 x 1
+ * to 32768 x 32768, any alignment that is a multiple of the element's size; bf16, fp16 or fp32.
+ * Input blocks may overlap (a stride of 0 repeats one); blocks that are written may not.
+ *
+ * Arithmetic: the iterates are held as fp16 planes with power-of-two scales derived from the
+ * schedule, products accumulate in fp32 on the tensor cores, and the term a * X takes X with a
+ * second fp16 plane (22 bits), so that small singular directions keep their accuracy: about 1e-3
+ * relative to 64 bits for the fixed 5-step schedule, 2e-4 for a converging one.  The scales are
+ * safe for schedules whose polynomial keeps [0, 1] within [-64, 64]; others are INVALID_ARG, and so
+ * are n_iters = 0, fp32_mode and n_split_iters (ns_orthogonalize has them).  A block with a
+ * non-finite norm comes out as NaN and sets the workspace's device status to NONFINITE; the other
+ * blocks are unaffected.  A block of zeros comes out as zeros.
+ *
+ * These calls keep nothing between calls: the workspace is scratch alone (it may be another one at
+ * every call, or shared by calls that do not overlap in time), nothing is uploaded, and the call
+ * can be captured in a CUDA graph without a call before it.  The first 256 bytes of the workspace
+ * hold the device status. */
+typedef struct {
+    const void* X;             /* input                                                     */
+    void* Y;                   /* output; may be X itself (same view and dtype)             */
+    long long x_stride, y_stride;
+    int x_ld, y_ld;
+    int count, rows, cols;
+    int x_dtype, y_dtype;      /* muon_dtype */
+} ns_stack_desc;
+
+/* Newton-Schulz orthogonalisation of every block of `n` stacks, all in the same launches.  With a
+ * `saved` buffer of ns_stacks_saved_size() bytes (256-byte aligned) the iterates are kept there for
+ * ns_orthogonalize_stacks_backward; NULL (and 0) otherwise.  Size queries return 0 for arguments
+ * that the call would refuse.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE_TOO_SMALL (workspace or saved), CUDA. */
+MUON_API size_t ns_stacks_workspace_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch, int with_saved);
+MUON_API size_t ns_stacks_saved_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch);
+MUON_API muon_status ns_orthogonalize_stacks(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch,
+                                             void* saved, size_t saved_bytes, void* workspace, size_t ws_bytes,
+                                             void* stream);
+
+/* Its gradient: descs[i].X is the gradient of the loss with respect to stack i's output and
+ * descs[i].Y receives the gradient with respect to its input (both with strides and dtypes of their
+ * own); count, rows, cols, their order and the schedule are those of the call that filled `saved`,
+ * which is read and left as it is.  Differentiates the division by (norm + eps) too; for a block of
+ * zeros the norm's derivative is taken as zero.  Workspace: ns_stacks_backward_workspace_size. */
+MUON_API size_t ns_stacks_backward_workspace_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch);
+MUON_API muon_status ns_orthogonalize_stacks_backward(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch,
+                                                      const void* saved, size_t saved_bytes, void* workspace,
+                                                      size_t ws_bytes, void* stream);
+
+typedef struct {
+    void* W;                   /* updated in place                                          */
+    const void* G;
+    float* M;                  /* momentum, fp32, updated in place                          */
+    long long w_stride, g_stride, m_stride;
+    int w_ld, g_ld, m_ld;
+    int count, rows, cols;     /* the shape scale is that of one block                      */
+    int w_dtype, g_dtype;      /* muon_dtype */
+} muon_stack_desc;
+
+/* The Muon step of muon_step_batched on every block of `n` stacks.  The gradient is multiplied by
+ * *grad_scale first (a device float, e.g. the clip factor of grad_norm_batched; NULL: 1).
+ * W, G and M may not overlap. */
+MUON_API size_t muon_stacks_workspace_size(const muon_stack_desc* descs, int n, const muon_hyper* hp);
+MUON_API muon_status muon_step_stacks(const muon_stack_desc* descs, int n, const muon_hyper* hp, const float* grad_scale,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ what Muon does not take
+ * Embeddings, heads, norms and biases go to AdamW, as the Muon optimizer page advises, under one
+ * gradient norm with the matrices.  Tensors are dense, of any length (0 too), aligned to their
+ * element; up to 65536 a call. */
+typedef struct {
+    void* W;                   /* updated in place (grad_norm_batched reads G, n, g_dtype alone) */
+    const void* G;
+    float* m;                  /* first and second moments, fp32, updated in place          */
+    float* v;
+    long long n;               /* elements                                                  */
+    int w_dtype, g_dtype;      /* muon_dtype */
+} adamw_tensor_desc;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    long long step;                /* number of this step, from 1                          */
+    const long long* step_dev;     /* device: the number is read there instead (NULL: step), so that a
+                                      captured call advances with it                       */
+} adamw_hyper;
+
+/* out[0] <- norm of all gradients together, out[1] <- min(1, max_norm / (norm + 1e-6)) (device
+ * floats).  Squares and sums in fp64, in a fixed order: the result does not change from run to run.
+ * A norm that is not finite is reported in the workspace's device status. */
+MUON_API size_t grad_norm_workspace_size(const adamw_tensor_desc* descs, int n);
+MUON_API muon_status grad_norm_batched(const adamw_tensor_desc* descs, int n, float max_norm, float* out,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
+/* AdamW (decoupled weight decay), g = *grad_scale * G (NULL: 1), t the step's number:
+ *   m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2
+ *   W <- (1 - lr wd) W - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, W rounded once.  W, G, m and v may not overlap.  No workspace.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+MUON_API muon_status adamw_step_batched(const adamw_tensor_desc* descs, int n, const adamw_hyper* hp,
+                                        const float* grad_scale, void* stream);
+
 /* Frobenius pre-scaling without a workspace: X_out[i] = X0[i] / (||X0[i]||_F + eps) for a
  * contiguous batch of rows x cols matrices, X0 = bf16(X_in) (fp32 X_in when fp32_mode = 1),
  * written as out_dtype; the same values ns_orthogonalize gives with zero iterations.  If
@@ -253,7 +356,9 @@ typedef enum {
     MUON_KERNEL_TC_F32 = 7,       /* tcgen05 fp32 products from three bf16 planes (Stiefel) */
     MUON_KERNEL_SIMT_GEMM_F64 = 8,  /* fp64 GEMMs (Stiefel LU updates and back substitution),
                                        on the fp64 tensor cores where the layout allows  */
-    MUON_KERNEL_KINDS = 9
+    MUON_KERNEL_GRAD_NORM = 9,    /* global gradient norm                                 */
+    MUON_KERNEL_ADAMW = 10,
+    MUON_KERNEL_KINDS = 11
 } muon_kernel_kind;
 MUON_API muon_status muon_timing_enable(int enable);
 MUON_API muon_status muon_timing_reset(void);

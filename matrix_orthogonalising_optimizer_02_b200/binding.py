@@ -20,11 +20,11 @@ LIB_PATH = os.path.join(HERE, "libmuon_b200.so")
 MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED_SHAPE, MUON_ERR_ALIGNMENT = 0, 1, 2, 3
 MUON_ERR_WORKSPACE_TOO_SMALL, MUON_ERR_CUDA, MUON_ERR_NONFINITE, MUON_ERR_DEVICE_TIMEOUT = 4, 5, 6, 7
 MUON_ERR_DEVICE_UNDRAINED = 8
-MUON_BF16, MUON_F32 = 0, 1
+MUON_BF16, MUON_F32, MUON_F16 = 0, 1, 2
 SCALE_MODES = {"moonlight": 0, "kellerjordan": 1, "mup": 2, "naive": 3}
 MUON_MAX_NS_ITERS = 32
 KERNEL_KINDS = {"momentum": 0, "scale": 1, "ns_gemm": 2, "update": 3, "simt_gemm": 4, "lu": 5, "misc": 6,
-                "tc_f32": 7, "simt_gemm_f64": 8}
+                "tc_f32": 7, "simt_gemm_f64": 8, "grad_norm": 9, "adamw": 10}
 
 #: Exported entry points, as declared in include/muon_b200.h.
 EXPORTED = (
@@ -34,6 +34,10 @@ EXPORTED = (
     "muon_status_string", "muon_build_info", "muon_frobenius_prescale_static",
     "muon_cayley_workspace_size", "muon_cayley_step", "muon_step_host_grad_workspace_size",
     "muon_step_batched_host_grad", "muon_last_error", "muon_selftest_wait_timeout",
+    "ns_stacks_workspace_size", "ns_stacks_saved_size", "ns_orthogonalize_stacks",
+    "ns_stacks_backward_workspace_size", "ns_orthogonalize_stacks_backward",
+    "muon_stacks_workspace_size", "muon_step_stacks",
+    "grad_norm_workspace_size", "grad_norm_batched", "adamw_step_batched",
 )
 
 
@@ -61,6 +65,29 @@ class MatrixDesc(ctypes.Structure):
 class Hyper(ctypes.Structure):
     _fields_ = [("lr", c_float), ("beta", c_float), ("weight_decay", c_float), ("nesterov", c_int),
                 ("scale_mode", c_int), ("ns", NsSchedule)]
+
+
+class NsStackDesc(ctypes.Structure):
+    _fields_ = [("X", c_void_p), ("Y", c_void_p), ("x_stride", c_longlong), ("y_stride", c_longlong),
+                ("x_ld", c_int), ("y_ld", c_int), ("count", c_int), ("rows", c_int), ("cols", c_int),
+                ("x_dtype", c_int), ("y_dtype", c_int)]
+
+
+class MuonStackDesc(ctypes.Structure):
+    _fields_ = [("W", c_void_p), ("G", c_void_p), ("M", c_void_p),
+                ("w_stride", c_longlong), ("g_stride", c_longlong), ("m_stride", c_longlong),
+                ("w_ld", c_int), ("g_ld", c_int), ("m_ld", c_int), ("count", c_int), ("rows", c_int), ("cols", c_int),
+                ("w_dtype", c_int), ("g_dtype", c_int)]
+
+
+class AdamWTensorDesc(ctypes.Structure):
+    _fields_ = [("W", c_void_p), ("G", c_void_p), ("m", c_void_p), ("v", c_void_p), ("n", c_longlong),
+                ("w_dtype", c_int), ("g_dtype", c_int)]
+
+
+class AdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("weight_decay", c_double), ("step", c_longlong), ("step_dev", c_void_p)]
 
 
 _LIB = None
@@ -99,6 +126,20 @@ def _lib():
                                      c_void_p, c_size_t, c_void_p]),
         "muon_frobenius_prescale_static": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                                    c_float, c_void_p, c_void_p]),
+        "ns_stacks_workspace_size": (c_size_t, [POINTER(NsStackDesc), c_int, POINTER(NsSchedule), c_int]),
+        "ns_stacks_saved_size": (c_size_t, [POINTER(NsStackDesc), c_int, POINTER(NsSchedule)]),
+        "ns_orthogonalize_stacks": (c_int, [POINTER(NsStackDesc), c_int, POINTER(NsSchedule), c_void_p, c_size_t,
+                                            c_void_p, c_size_t, c_void_p]),
+        "ns_stacks_backward_workspace_size": (c_size_t, [POINTER(NsStackDesc), c_int, POINTER(NsSchedule)]),
+        "ns_orthogonalize_stacks_backward": (c_int, [POINTER(NsStackDesc), c_int, POINTER(NsSchedule), c_void_p,
+                                                     c_size_t, c_void_p, c_size_t, c_void_p]),
+        "muon_stacks_workspace_size": (c_size_t, [POINTER(MuonStackDesc), c_int, POINTER(Hyper)]),
+        "muon_step_stacks": (c_int, [POINTER(MuonStackDesc), c_int, POINTER(Hyper), c_void_p, c_void_p, c_size_t,
+                                     c_void_p]),
+        "grad_norm_workspace_size": (c_size_t, [POINTER(AdamWTensorDesc), c_int]),
+        "grad_norm_batched": (c_int, [POINTER(AdamWTensorDesc), c_int, c_float, c_void_p, c_void_p, c_size_t,
+                                      c_void_p]),
+        "adamw_step_batched": (c_int, [POINTER(AdamWTensorDesc), c_int, POINTER(AdamWHyper), c_void_p, c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name, None)
@@ -345,3 +386,237 @@ def workspace(nbytes: int, device=None):
     """A caller-owned workspace tensor of at least nbytes (allocated by torch)."""
     import torch
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
+
+
+# ---------------------------------------------------------------------------- stacks of blocks
+@dataclass
+class Stack:
+    """Blocks to orthogonalise: X and Y are [count, rows, cols] (or one [rows, cols]) views with a unit
+    stride in the last dimension, bf16, fp16 or fp32 each.  Y may be X.  For the gradient, X is the
+    gradient of the output and Y receives that of the input."""
+    X: object
+    Y: object
+
+
+@dataclass
+class MuonStack:
+    """Blocks of a Muon parameter: W (updated in place), G and M (fp32, updated in place), each a
+    [count, rows, cols] (or one [rows, cols]) view with a unit stride in the last dimension."""
+    W: object
+    G: object
+    M: object
+
+
+@dataclass
+class AdamWTensor:
+    """A dense tensor of any shape: W (updated in place), G, and the fp32 moments m and v."""
+    W: object
+    G: object
+    m: object
+    v: object
+
+
+def _dtype16(t, name: str) -> int:
+    import torch
+    codes = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32, torch.float16: MUON_F16}
+    if t.dtype not in codes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}: bf16, fp16 or fp32 expected")
+    return codes[t.dtype]
+
+
+def _view3(t, name: str, device):
+    """(shape, row pitch, block stride) of a [count, rows, cols] or [rows, cols] view."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [count, rows, cols] or [rows, cols], got shape {tuple(t.shape)}")
+    shape = tuple(t.shape) if t.dim() == 3 else (1,) + tuple(t.shape)
+    if 0 in shape:
+        raise ValueError(f"{name} has no elements")
+    stride = t.stride() if t.dim() == 3 else (0,) + t.stride()
+    if shape[2] > 1 and stride[2] != 1:
+        raise ValueError(f"{name} must have a unit stride in its last dimension")
+    ld = stride[1] if shape[1] > 1 else shape[2]
+    if ld >= 1 << 31:
+        raise ValueError(f"{name}: row pitch {ld} is too long")
+    return shape, ld, stride[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _stack_descs(stacks: Sequence[Stack]):
+    if not stacks:
+        raise ValueError("no stacks")
+    arr = (NsStackDesc * len(stacks))()
+    device = stacks[0].X.device
+    for i, s in enumerate(stacks):
+        shape, x_ld, x_stride = _view3(s.X, "X", device)
+        yshape, y_ld, y_stride = _view3(s.Y, "Y", device)
+        if yshape != shape:
+            raise ValueError("X and Y must have the same shape")
+        arr[i] = NsStackDesc(s.X.data_ptr(), s.Y.data_ptr(), x_stride, y_stride, x_ld, y_ld, *shape,
+                             _dtype16(s.X, "X"), _dtype16(s.Y, "Y"))
+    return arr, device
+
+
+def _muon_stack_descs(stacks: Sequence[MuonStack]):
+    import torch
+    if not stacks:
+        raise ValueError("no stacks")
+    arr = (MuonStackDesc * len(stacks))()
+    device = stacks[0].W.device
+    for i, s in enumerate(stacks):
+        shape, w_ld, w_stride = _view3(s.W, "W", device)
+        gshape, g_ld, g_stride = _view3(s.G, "G", device)
+        mshape, m_ld, m_stride = _view3(s.M, "M", device)
+        if gshape != shape or mshape != shape:
+            raise ValueError("W, G and M must have the same shape")
+        if s.M.dtype != torch.float32:
+            raise TypeError("the momentum buffer M must be fp32")
+        arr[i] = MuonStackDesc(s.W.data_ptr(), s.G.data_ptr(), s.M.data_ptr(), w_stride, g_stride, m_stride,
+                               w_ld, g_ld, m_ld, *shape, _dtype16(s.W, "W"), _dtype16(s.G, "G"))
+    return arr, device
+
+
+def _bytes(t, name: str, device):
+    _need(t, name, device=device)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _scalar(t, name: str, device, dtype):
+    """Pointer of a one-element device tensor (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{name} must be one {dtype} value on the device")
+    _need(t, name, device=device)
+    return t.data_ptr()
+
+
+class _On:
+    """Makes the tensors' device the current one for a call and gives the stream: the caller's, or
+    torch's current stream of that device."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        import torch
+        self.guard.__enter__()
+        return _stream(self.stream if self.stream is not None else torch.cuda.current_stream(self.device))
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def ns_stacks_workspace_size(stacks: Sequence[Stack], schedule: Schedule, with_saved: bool = False) -> int:
+    return int(_lib().ns_stacks_workspace_size(_stack_descs(stacks)[0], len(stacks), ctypes.byref(schedule.c),
+                                               int(bool(with_saved))))
+
+
+def ns_stacks_saved_size(stacks: Sequence[Stack], schedule: Schedule) -> int:
+    return int(_lib().ns_stacks_saved_size(_stack_descs(stacks)[0], len(stacks), ctypes.byref(schedule.c)))
+
+
+def ns_orthogonalize_stacks(stacks: Sequence[Stack], schedule: Schedule, workspace, saved=None, stream=None):
+    """Newton-Schulz orthogonalisation of every block; `saved` keeps what the gradient needs."""
+    arr, device = _stack_descs(stacks)
+    ws, ws_bytes = _bytes(workspace, "workspace", device)
+    sv, sv_bytes = _bytes(saved, "saved", device) if saved is not None else (None, 0)
+    with _On(device, stream) as st:
+        _check(_lib().ns_orthogonalize_stacks(arr, len(stacks), ctypes.byref(schedule.c), sv, sv_bytes, ws, ws_bytes,
+                                              st), "ns_orthogonalize_stacks")
+
+
+def ns_stacks_backward_workspace_size(grads: Sequence[Stack], schedule: Schedule) -> int:
+    return int(_lib().ns_stacks_backward_workspace_size(_stack_descs(grads)[0], len(grads), ctypes.byref(schedule.c)))
+
+
+def ns_orthogonalize_stacks_backward(grads: Sequence[Stack], schedule: Schedule, saved, workspace, stream=None):
+    """The gradient of ns_orthogonalize_stacks: X of each stack is the gradient of its output, Y
+    receives that of its input; `saved` is the buffer the forward call filled."""
+    arr, device = _stack_descs(grads)
+    ws, ws_bytes = _bytes(workspace, "workspace", device)
+    sv, sv_bytes = _bytes(saved, "saved", device)
+    with _On(device, stream) as st:
+        _check(_lib().ns_orthogonalize_stacks_backward(arr, len(grads), ctypes.byref(schedule.c), sv, sv_bytes, ws,
+                                                       ws_bytes, st), "ns_orthogonalize_stacks_backward")
+
+
+def muon_stacks_workspace_size(stacks: Sequence[MuonStack], hp) -> int:
+    return int(_lib().muon_stacks_workspace_size(_muon_stack_descs(stacks)[0], len(stacks), ctypes.byref(hp[0])))
+
+
+def muon_step_stacks(stacks: Sequence[MuonStack], hp, workspace, grad_scale=None, stream=None):
+    """The Muon step on every block of every stack; G is multiplied by the device scalar
+    `grad_scale` first."""
+    import torch
+    arr, device = _muon_stack_descs(stacks)
+    ws, ws_bytes = _bytes(workspace, "workspace", device)
+    gs = _scalar(grad_scale, "grad_scale", device, torch.float32)
+    with _On(device, stream) as st:
+        _check(_lib().muon_step_stacks(arr, len(stacks), ctypes.byref(hp[0]), gs, ws, ws_bytes, st), "muon_step_stacks")
+
+
+# ---------------------------------------------------------------------------- gradient norm, AdamW
+def _grad_descs(grads):
+    if not grads:
+        raise ValueError("no gradients")
+    arr = (AdamWTensorDesc * len(grads))()
+    device = grads[0].device
+    for i, g in enumerate(grads):
+        _need(g, "G", device=device)
+        arr[i] = AdamWTensorDesc(None, g.data_ptr(), None, None, g.numel(), 0, _dtype16(g, "G"))
+    return arr, device
+
+
+def grad_norm_workspace_size(grads) -> int:
+    return int(_lib().grad_norm_workspace_size(_grad_descs(grads)[0], len(grads)))
+
+
+def grad_norm_batched(grads, max_norm: float, out, workspace, stream=None):
+    """out[0] <- the norm of all gradients together, out[1] <- min(1, max_norm / (norm + 1e-6))."""
+    import torch
+    arr, device = _grad_descs(grads)
+    _need(out, "out", device=device)
+    if out.dtype != torch.float32 or out.numel() != 2:
+        raise ValueError("out must hold two fp32 values")
+    ws, ws_bytes = _bytes(workspace, "workspace", device)
+    with _On(device, stream) as st:
+        _check(_lib().grad_norm_batched(arr, len(grads), float(max_norm), out.data_ptr(), ws, ws_bytes, st),
+               "grad_norm_batched")
+
+
+def adamw_hyper(lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                weight_decay: float = 0.01) -> AdamWHyper:
+    return AdamWHyper(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 0, None)
+
+
+def adamw_step_batched(tensors: Sequence[AdamWTensor], hp: AdamWHyper, step, grad_scale=None, stream=None):
+    """AdamW on every tensor.  `step` is the number of this step, from 1: an int, or a device int64
+    (read when the step runs, so that a captured step can be replayed as it advances)."""
+    import torch
+    if not tensors:
+        raise ValueError("no tensors")
+    arr = (AdamWTensorDesc * len(tensors))()
+    device = tensors[0].W.device
+    for i, t in enumerate(tensors):
+        if tuple(t.G.shape) != tuple(t.W.shape) or tuple(t.m.shape) != tuple(t.W.shape) or \
+                tuple(t.v.shape) != tuple(t.W.shape):
+            raise ValueError("W, G, m and v must have the same shape")
+        if t.m.dtype != torch.float32 or t.v.dtype != torch.float32:
+            raise TypeError("the moments m and v must be fp32")
+        for x, name in ((t.W, "W"), (t.G, "G"), (t.m, "m"), (t.v, "v")):
+            _need(x, name, device=device)
+        arr[i] = AdamWTensorDesc(t.W.data_ptr(), t.G.data_ptr(), t.m.data_ptr(), t.v.data_ptr(), t.W.numel(),
+                                 _dtype16(t.W, "W"), _dtype16(t.G, "G"))
+    h = AdamWHyper(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, 0, None)
+    if isinstance(step, torch.Tensor):
+        h.step_dev = _scalar(step, "step", device, torch.int64)
+    else:
+        h.step = int(step)
+    gs = _scalar(grad_scale, "grad_scale", device, torch.float32)
+    with _On(device, stream) as st:
+        _check(_lib().adamw_step_batched(arr, len(tensors), ctypes.byref(h), gs, st), "adamw_step_batched")

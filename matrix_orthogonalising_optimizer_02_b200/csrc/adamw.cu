@@ -1,0 +1,178 @@
+// The global gradient norm with its clip factor, and AdamW, over any number of tensors.
+//
+// Both are HBM-bound: the norm reads each gradient once; AdamW reads W, G, m, v and writes W, m, v
+// once, all arithmetic in fp32 registers.  Descriptors travel as kernel parameters (up to 256 tensors
+// a launch).  A persistent grid walks chunks of 4096 elements, 8 elements a thread at a time.
+#include <cmath>
+
+#include "../../include/muon_b200.h"
+#include "adamw.cuh"
+#include "typed_io.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int CHUNK = kAdamChunk;
+constexpr int GROUPS = CHUNK / 8 / THREADS;
+static_assert(GROUPS * 8 * THREADS == CHUNK, "a chunk is a whole number of groups per thread");
+
+template <int N>
+struct Params {
+    AdamItem item[N];
+    int n;
+    long long chunks;
+};
+
+template <int N>
+__device__ __forceinline__ int find(const Params<N>& p, long long chunk) {
+    int lo = 0, hi = p.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.item[mid].chunk0 <= chunk) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// partials[blockIdx.x] <- sum of squares of this CTA's chunks, in fp64.
+template <int N>
+__global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Params<N> p, double* partials) {
+    double ss = 0.0;
+    for (long long c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        const AdamItem& it = p.item[find(p, c)];
+        const long long e0 = (c - it.chunk0) * CHUNK;
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q) {
+            const long long e = e0 + (q * THREADS + static_cast<int>(threadIdx.x)) * 8;
+            if (e >= it.n) break;
+            float x[8];
+            load8(it.G, it.g_dtype, e, static_cast<int>(min(8ll, it.n - e)), it.vec & 1, x);
+            // two products of 24 bits each: squares and their sums in fp64
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fma(static_cast<double>(x[j]), static_cast<double>(x[j]), ss);
+        }
+    }
+    ss = block_sum256(ss);
+    if (threadIdx.x == 0) partials[blockIdx.x] = ss;
+}
+
+// out[0] <- norm, out[1] <- min(1, max_norm / (norm + 1e-6)).
+__global__ void __launch_bounds__(THREADS) grad_norm_final_kernel(const double* partials, int n, float max_norm,
+                                                                  float* out, unsigned* status) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += THREADS) s += partials[i];
+    s = block_sum256(s);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(s);
+        const double f = static_cast<double>(max_norm) / (norm + 1e-6);
+        out[0] = static_cast<float>(norm);
+        out[1] = isnan(f) ? static_cast<float>(f) : static_cast<float>(fmin(1.0, f));
+        *status = isfinite(norm) ? 0u : kDevErrNonfinite;
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Params<N> p, const AdamParams h) {
+    __shared__ float corr[2];
+    float c1 = h.c1, c2 = h.c2;
+    if (h.step != nullptr) {   // the step count is on the device
+        if (threadIdx.x == 0) {
+            const double t = static_cast<double>(*h.step);
+            corr[0] = static_cast<float>(1.0 / (1.0 - pow(h.beta1_d, t)));
+            corr[1] = static_cast<float>(1.0 / (1.0 - pow(h.beta2_d, t)));
+        }
+        __syncthreads();
+        c1 = corr[0];
+        c2 = corr[1];
+    }
+    const float gs = h.gscale != nullptr ? __ldg(h.gscale) : 1.f;
+    for (long long c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        const AdamItem& it = p.item[find(p, c)];
+        const long long e0 = (c - it.chunk0) * CHUNK;
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q) {
+            const long long e = e0 + (q * THREADS + static_cast<int>(threadIdx.x)) * 8;
+            if (e >= it.n) break;
+            const int n = static_cast<int>(min(8ll, it.n - e));
+            float g[8], m[8], v[8], w[8];
+            load8(it.G, it.g_dtype, e, n, it.vec & 1, g);
+            load8(it.m, MUON_F32, e, n, it.vec & 2, m);
+            load8(it.v, MUON_F32, e, n, it.vec & 2, v);
+            load8(it.W, it.w_dtype, e, n, it.vec & 4, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = g[j] * gs;
+                m[j] = fmaf(h.beta1, m[j], h.omb1 * x);
+                v[j] = fmaf(h.beta2, v[j], h.omb2 * x * x);
+                const float u = (m[j] * c1) / (sqrtf(v[j] * c2) + h.eps);
+                w[j] = fmaf(-h.lr, u, h.decay * w[j]);
+            }
+            store8(it.m, MUON_F32, e, n, it.vec & 2, m);
+            store8(it.v, MUON_F32, e, n, it.vec & 2, v);
+            store8(it.W, it.w_dtype, e, n, it.vec & 4, w);
+        }
+    }
+}
+
+template <int N>
+void fill(Params<N>& p, const AdamItem* items, int n) {
+    p.n = n;
+    p.chunks = 0;
+    for (int i = 0; i < n; ++i) {
+        p.item[i] = items[i];
+        p.item[i].chunk0 = p.chunks;
+        p.chunks += (items[i].n + CHUNK - 1) / CHUNK;
+    }
+}
+template <int N>
+unsigned grid_of(const Params<N>& p, int num_sms) {
+    const long long most = static_cast<long long>(num_sms) * kAdamCtasPerSm;
+    return static_cast<unsigned>(p.chunks < most ? p.chunks : most);
+}
+
+template <int N>
+cudaError_t norm_part(const AdamItem* items, int n, double* partials, int& used, int num_sms, cudaStream_t stream) {
+    Params<N> p;
+    fill(p, items, n);
+    const unsigned grid = grid_of(p, num_sms);
+    if (grid == 0) return cudaSuccess;
+    grad_norm_kernel<N><<<grid, THREADS, 0, stream>>>(p, partials + used);
+    used += static_cast<int>(grid);
+    return cudaGetLastError();
+}
+template <int N>
+cudaError_t adamw_part(const AdamItem* items, int n, const AdamParams& h, int num_sms, cudaStream_t stream) {
+    Params<N> p;
+    fill(p, items, n);
+    const unsigned grid = grid_of(p, num_sms);
+    if (grid == 0) return cudaSuccess;
+    adamw_kernel<N><<<grid, THREADS, 0, stream>>>(p, h);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t grad_norm_launch(const AdamItem* items, int n, double* partials, float max_norm, float* out,
+                             unsigned* status, int num_sms, cudaStream_t stream) {
+    int used = 0;
+    for (int i = 0; i < n; i += kAdamMaxItems) {
+        const int m = n - i < kAdamMaxItems ? n - i : kAdamMaxItems;
+        const cudaError_t e = m <= 8 ? norm_part<8>(items + i, m, partials, used, num_sms, stream)
+                                     : norm_part<kAdamMaxItems>(items + i, m, partials, used, num_sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    grad_norm_final_kernel<<<1, THREADS, 0, stream>>>(partials, used, max_norm, out, status);
+    return cudaGetLastError();
+}
+
+cudaError_t adamw_launch(const AdamItem* items, int n, const AdamParams& h, int num_sms, cudaStream_t stream) {
+    for (int i = 0; i < n; i += kAdamMaxItems) {
+        const int m = n - i < kAdamMaxItems ? n - i : kAdamMaxItems;
+        const cudaError_t e = m <= 8 ? adamw_part<8>(items + i, m, h, num_sms, stream)
+                                     : adamw_part<kAdamMaxItems>(items + i, m, h, num_sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace muon

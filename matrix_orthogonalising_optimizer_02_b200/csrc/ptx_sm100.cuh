@@ -141,6 +141,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
         : "memory");
 }
 
+// The same for a 3-D map (a stack of matrices).
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* tmap, uint32_t bar_cluster_addr,
+                                                 int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(tmap), "r"(bar_cluster_addr), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_slot, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_slot)),
@@ -242,6 +252,17 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16_f32(int M, int N, int a_
     d |= 1u << 4;                          // C format: F32
     d |= 1u << 7;                          // A format: BF16
     d |= 1u << 10;                         // B format: BF16
+    d |= static_cast<uint32_t>(a_mn_major & 1) << 15;
+    d |= static_cast<uint32_t>(b_mn_major & 1) << 16;
+    d |= static_cast<uint32_t>(N >> 3) << 17;
+    d |= static_cast<uint32_t>(M >> 4) << 24;
+    return d;
+}
+
+// The same with fp16 operands.
+__host__ __device__ __forceinline__ uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
+    uint32_t d = 0;
+    d |= 1u << 4;                          // C format: F32; A and B format 0: F16
     d |= static_cast<uint32_t>(a_mn_major & 1) << 15;
     d |= static_cast<uint32_t>(b_mn_major & 1) << 16;
     d |= static_cast<uint32_t>(N >> 3) << 17;

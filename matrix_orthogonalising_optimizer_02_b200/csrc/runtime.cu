@@ -71,6 +71,31 @@ int device_sm_count() {
     return sms;
 }
 
+namespace {
+const char* const kind_names[MUON_KERNEL_KINDS] = {"momentum", "scale", "ns_gemm", "update", "simt_gemm", "lu",
+                                                   "misc", "tc_f32", "simt_gemm_f64", "grad_norm", "adamw"};
+}  // namespace
+
+cudaError_t launch_timed(int kind, double work, cudaStream_t stream,
+                         const std::function<cudaError_t(cudaStream_t)>& run) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    nvtxRangePushA(kind_names[kind]);
+    cudaError_t e;
+    if (g_timing.enabled) {
+        TimingRec r{kind, work, nullptr, nullptr};
+        cudaEventCreate(&r.e0);
+        cudaEventCreate(&r.e1);
+        cudaEventRecord(r.e0, stream);
+        e = run(stream);
+        cudaEventRecord(r.e1, stream);
+        g_timing.pending.push_back(r);
+    } else {
+        e = run(stream);
+    }
+    nvtxRangePop();
+    return e;
+}
+
 muon_status run_plan(const std::vector<uint8_t>& key_in, void* workspace, size_t table_offset,
                      const std::function<muon_status(Plan&, TableImage&)>& build, cudaStream_t stream,
                      cudaStream_t upload_stream, const std::function<muon_status()>& before_launch) {
@@ -150,9 +175,6 @@ muon_status run_plan(const std::vector<uint8_t>& key_in, void* workspace, size_t
         const muon_status st = before_launch();
         if (st != MUON_OK) return st;
     }
-    static const char* const kind_names[MUON_KERNEL_KINDS] = {"momentum", "scale", "ns_gemm", "update",
-                                                              "simt_gemm", "lu", "misc", "tc_f32",
-                                                              "simt_gemm_f64"};
     // NVTX: one range per launch, named by kernel kind, nested in one range for the call
     // (header-only NVTX 3: free unless a profiler injects its library)
     nvtxRangePushA("muon_b200 plan");

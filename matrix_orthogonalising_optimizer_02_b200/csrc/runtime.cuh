@@ -95,6 +95,10 @@ muon_status run_plan(const std::vector<uint8_t>& key, void* workspace, size_t ta
                      cudaStream_t upload_stream = nullptr,
                      const std::function<muon_status()>& before_launch = nullptr);
 
+// One launch outside a plan, bracketed like a plan's launches (timing, NVTX range).
+cudaError_t launch_timed(int kind, double work, cudaStream_t stream,
+                         const std::function<cudaError_t(cudaStream_t)>& run);
+
 // Tensor map of a row-major bf16 matrix (rows x cols, pitch = cols) with a box of 64 columns
 // x box_rows rows, 128-byte swizzle, zero fill out of bounds.
 bool encode_bf16_tmap(CUtensorMap* out, const void* base, int rows, int cols, int box_rows);
@@ -127,10 +131,23 @@ struct TmapPool {
     }
 };
 
+// Runs `f` at a C entry point: no C++ exception leaves it.
+template <class F>
+muon_status no_throw(F&& f) noexcept;
+
 int device_sm_count();
 muon_status from_cuda(cudaError_t e);
 // Records `where` and the CUDA error as the calling thread's last library error (read with
 // muon_last_error) and returns MUON_ERR_CUDA.
 muon_status cuda_error(cudaError_t e, const char* where);
+
+template <class F>
+muon_status no_throw(F&& f) noexcept {
+    try {
+        return f();
+    } catch (...) {
+        return cuda_error(cudaErrorMemoryAllocation, "host memory of the call");
+    }
+}
 
 }  // namespace muon

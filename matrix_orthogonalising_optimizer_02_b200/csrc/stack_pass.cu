@@ -1,0 +1,223 @@
+// Elementwise passes over stacks of blocks: what comes before and after the products of
+// stack_gemm.cu.  HBM-bound; one CTA takes 8192 elements of one block, 8 a thread at a time.
+//
+// Norms.  A block's sum of squares is formed in fp64 (a gradient's elements, 1e-20 or 1e20, square
+// out of fp32's range), one partial per CTA; the next pass's CTAs each add up their block's partials
+// in one fixed order, so no launch is spent on it and every CTA gets the same number.
+//
+// Scaling.  hi = fp16(U * 2^k) with the power of two that puts the block's rms into [1/2, 1): no
+// element of up to 2^31 can leave fp16's range, a 16-bit input of ordinary spread is held exactly,
+// and 1 / (N + eps) enters in the first products' epilogues as f0 = 1 / ((N + eps) 2^k).
+#include <cmath>
+
+#include "../../include/muon_b200.h"
+#include "stacks.cuh"
+#include "typed_io.cuh"
+
+namespace muon {
+namespace {
+
+template <int N>
+struct PassParams {
+    StackItem item[N];
+    StackPassArgs a;
+    int n;
+};
+
+constexpr int GROUPS = kStackChunk / 8 / kStackThreads;   // 8-element groups per thread
+
+__device__ __forceinline__ float pow2f(int k) {   // 2^k, |k| <= 126
+    return __int_as_float((k + 127) << 23);
+}
+
+template <StackPass PASS, int N>
+__global__ void __launch_bounds__(kStackThreads)
+stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
+    int lo = 0, hi = p.n - 1;
+    const int chunk = static_cast<int>(blockIdx.x);
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.item[mid].chunk0 <= chunk) lo = mid; else hi = mid - 1;
+    }
+    const StackItem& it = p.item[lo];
+    const int b = (chunk - it.chunk0) / it.chunks, c = (chunk - it.chunk0) - b * it.chunks;
+    const int rp = (it.rows + 7) & ~7, cg = (it.cols + 7) >> 3;   // padded rows, 8-column groups a row
+    const int groups = rp * cg;
+    const float gs = p.a.gscale != nullptr ? __ldg(p.a.gscale) : 1.f;
+    const size_t plane = static_cast<size_t>(b) * groups * 8;
+    float* info = it.info != nullptr ? it.info + static_cast<size_t>(b) * kStackInfo : nullptr;
+    double* partials = it.partials != nullptr ? it.partials + static_cast<size_t>(b) * it.chunks : nullptr;
+
+    float up = 1.f;                            // kPack, kPackGrad: factor of the plane
+    float od = 0.f, ox = 0.f;                  // kGradOut: out = od * D + ox * X
+    if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad || PASS == StackPass::kGradOut) {
+        double s = 0.0;
+        for (int i = threadIdx.x; i < it.chunks; i += kStackThreads) s += partials[i];
+        s = block_sum256(s);
+        const double eps = static_cast<double>(p.a.eps);
+        if (PASS == StackPass::kGradOut) {
+            // dU = [D_0 - X_0 <D_0, X_0> (N + eps) / N] / (N + eps), D_0 = (hi + lo) / (2^k step)
+            const float* gi = it.ginfo + static_cast<size_t>(b) * kStackInfo;
+            const double n = info[3], f0 = info[0];
+            const double sd = 1.0 / (static_cast<double>(gi[1]) * it.step);
+            const double corr = n > 0.0 ? s * sd * f0 * (n + eps) / n : (isnan(f0) ? f0 : 0.0);
+            od = static_cast<float>(sd / (n + eps));
+            ox = static_cast<float>(-corr * f0 / (n + eps));
+        } else {
+            const double n = sqrt(s);
+            // hi's rms (kPack) or whole norm (kPackGrad) in [1/2, 1)
+            const double size = PASS == StackPass::kPack ? n / sqrt(static_cast<double>(it.rows) * it.cols) : n;
+            int k = 0;
+            if (isfinite(n) && n > 0.0) k = max(-126, min(126, -(ilogb(size) + 1)));
+            up = pow2f(k);
+            if (c == 0 && threadIdx.x == 0) {
+                const bool fin = isfinite(n);
+                info[0] = !fin ? NAN : n > 0.0 ? static_cast<float>(1.0 / ((n + eps) * static_cast<double>(up))) : 0.f;
+                info[1] = up;
+                info[2] = static_cast<float>(1.0 / (n + eps));
+                info[3] = static_cast<float>(n);
+                if (!fin && p.a.status != nullptr) atomicOr(p.a.status, kDevErrNonfinite);
+            }
+            if (PASS == StackPass::kPackGrad) up *= it.step;
+        }
+    }
+
+    if (PASS == StackPass::kNorm && p.a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.a.status = 0;
+
+    double ss = 0.0;
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+        const int g = c * (kStackChunk / 8) + q * kStackThreads + static_cast<int>(threadIdx.x);
+        if (g >= groups) break;
+        const int i = g / cg, j = (g - i * cg) * 8;
+        const int n = i < it.rows ? min(8, it.cols - j) : 0;     // elements of this group inside the block
+        const long long bi = b;
+        const size_t w8 = plane + static_cast<size_t>(g) * 8;    // the group in the workspace planes
+        if (PASS == StackPass::kNorm) {
+            if (n == 0) continue;
+            float x[8];
+            load8(it.G, it.g_dtype, bi * it.g_stride + static_cast<long long>(i) * it.g_ld + j, n, it.vec & 1, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= gs;
+            if (it.M != nullptr) {
+                float m[8];
+                const long long mo = bi * it.m_stride + static_cast<long long>(i) * it.m_ld + j;
+                load8(it.M, MUON_F32, mo, n, it.vec & 2, m);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    m[e] = fmaf(p.a.beta, m[e], x[e]);
+                    x[e] = p.a.nesterov ? fmaf(p.a.beta, m[e], x[e]) : m[e];
+                }
+                store8(it.M, MUON_F32, mo, n, it.vec & 2, m);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
+        } else if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (n > 0) {
+                if (it.M == nullptr || p.a.nesterov) {
+                    load8(it.G, it.g_dtype, bi * it.g_stride + static_cast<long long>(i) * it.g_ld + j, n, it.vec & 1, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= gs;
+                }
+                if (it.M != nullptr) {   // the momentum pass has updated M
+                    float m[8];
+                    load8(it.M, MUON_F32, bi * it.m_stride + static_cast<long long>(i) * it.m_ld + j, n, it.vec & 2, m);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = p.a.nesterov ? fmaf(p.a.beta, m[e], x[e]) : m[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= up;
+            const uint4 h = pack8(MUON_F16, x);
+            *reinterpret_cast<uint4*>(it.hi + w8) = h;
+            if (it.lo != nullptr) {
+                float y[8];
+                unpack8(h, MUON_F16, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = x[e] - y[e];
+                *reinterpret_cast<uint4*>(it.lo + w8) = pack8(MUON_F16, y);
+            }
+        } else {
+            if (n == 0) continue;
+            float x[8];
+            unpack8(*reinterpret_cast<const uint4*>(it.hi + w8), MUON_F16, x);
+            const long long wo = bi * it.w_stride + static_cast<long long>(i) * it.w_ld + j;
+            if (PASS == StackPass::kOut) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= it.step;
+                store8(it.W, it.w_dtype, wo, n, it.vec & 4, x);
+            } else if (PASS == StackPass::kUpdate) {
+                float w[8];
+                load8(it.W, it.w_dtype, wo, n, it.vec & 4, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = fmaf(it.step, x[e], it.decay * w[e]);
+                store8(it.W, it.w_dtype, wo, n, it.vec & 4, w);
+            } else {
+                float y[8], z[8];
+                unpack8(*reinterpret_cast<const uint4*>(it.lo + w8), MUON_F16, y);
+                unpack8(*reinterpret_cast<const uint4*>(it.hi2 + w8), MUON_F16, z);
+                if (PASS == StackPass::kDot) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        ss = fma(static_cast<double>(x[e]) + static_cast<double>(y[e]), static_cast<double>(z[e]), ss);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(od, x[e] + y[e], ox * z[e]);
+                    store8(it.W, it.w_dtype, wo, n, it.vec & 4, x);
+                }
+            }
+        }
+    }
+    if (PASS == StackPass::kNorm || PASS == StackPass::kDot) {
+        const double t = block_sum256(ss);
+        if (threadIdx.x == 0) partials[c] = t;
+    }
+}
+
+template <StackPass PASS, int N>
+cudaError_t launch(const StackItem* items, int n, const StackPassArgs& a, long long chunks, cudaStream_t stream) {
+    PassParams<N> p;
+    for (int i = 0; i < n; ++i) p.item[i] = items[i];
+    p.a = a;
+    p.n = n;
+    stack_pass_kernel<PASS, N><<<static_cast<unsigned>(chunks), kStackThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <StackPass PASS>
+cudaError_t launch_any(StackItem* items, int n, const StackPassArgs& a, cudaStream_t stream) {
+    for (int i0 = 0; i0 < n; i0 += kStackMaxItems) {
+        const int m = n - i0 < kStackMaxItems ? n - i0 : kStackMaxItems;
+        long long chunks = 0;
+        for (int i = 0; i < m; ++i) {
+            items[i0 + i].chunk0 = static_cast<int>(chunks);
+            chunks += static_cast<long long>(items[i0 + i].chunks) * items[i0 + i].count;
+            if (chunks > INT32_MAX) return cudaErrorInvalidValue;
+        }
+        if (chunks == 0) continue;
+        StackPassArgs b = a;
+        if (PASS == StackPass::kNorm && i0 > 0) b.status = nullptr;   // cleared once
+        const cudaError_t e = m <= 4 ? launch<PASS, 4>(items + i0, m, b, chunks, stream)
+                                     : launch<PASS, kStackMaxItems>(items + i0, m, b, chunks, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const StackPassArgs& a, cudaStream_t stream) {
+    switch (pass) {
+        case StackPass::kNorm: return launch_any<StackPass::kNorm>(items, n, a, stream);
+        case StackPass::kPack: return launch_any<StackPass::kPack>(items, n, a, stream);
+        case StackPass::kPackGrad: return launch_any<StackPass::kPackGrad>(items, n, a, stream);
+        case StackPass::kOut: return launch_any<StackPass::kOut>(items, n, a, stream);
+        case StackPass::kUpdate: return launch_any<StackPass::kUpdate>(items, n, a, stream);
+        case StackPass::kDot: return launch_any<StackPass::kDot>(items, n, a, stream);
+        case StackPass::kGradOut: return launch_any<StackPass::kGradOut>(items, n, a, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace muon

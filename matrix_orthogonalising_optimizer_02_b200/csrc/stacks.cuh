@@ -1,0 +1,105 @@
+// Kernel-level interfaces of the stacked-block operators: Newton-Schulz orthogonalisation of
+// stacks of equal blocks and its gradient, the Muon step on them, global norm and AdamW.
+//
+// Every launch takes its descriptors by value as kernel parameters (up to 32 KB), so a call
+// uploads nothing, keeps nothing between calls and can be captured as it stands.
+#pragma once
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "kernels.cuh"
+
+namespace muon {
+
+// ------------------------------------------------------------------ grouped fp16 GEMM
+// One problem of a launch: `count` products of one shape,
+//   out[b] = f_b * (alpha * sum_seg A_seg[b] x B_seg[b] + beta * (E[0][b] + E[1][b])),
+// f_b = dscale[b]^scale_pow, fp16 operands with fp32 accumulation in TMEM.  The K loop runs
+// over up to two operand pairs (segments) of the same K.  E and out are fp16 planes (value =
+// plane 0 + plane 1, plane 1 optional) with a row pitch and a block stride of their own.
+constexpr uint32_t kStackAMn = 1u;       // A is contiguous along M (else along K)
+constexpr uint32_t kStackBMn = 2u;       // B is contiguous along N (else along K)
+constexpr uint32_t kStackSym = 4u;       // symmetric output: upper tiles computed, stored mirrored
+constexpr uint32_t kStackOutBf16 = 8u;   // plane 0 of the output is bf16
+constexpr uint32_t kStackRowMajor = 16u; // tiles swept along the rows of a block first
+
+struct alignas(64) StackProb {
+    CUtensorMap tmA[2];
+    CUtensorMap tmB[2];
+    const __half* E[2];
+    void* out[2];
+    const float* dscale;
+    long long e_stride, o_stride;    // elements between blocks
+    int e_ld, o_ld;                  // elements between rows
+    int M, N, K;                     // multiples of 8
+    int m_out;                       // rows stored (<= M)
+    int nseg;
+    float alpha, beta;
+    int scale_pow;
+    uint32_t flags;
+    int mbs, nbs;                    // 256 x 256 tiles of a block
+    int tile0, block_tiles;          // first tile of this problem, tiles per block
+};
+constexpr int kStackMaxProbs = 16;
+
+// Tensor map of `count` row-major fp16 matrices (rows x cols, dense): a box of 64 columns x
+// box_rows rows of one matrix, 128-byte swizzle, zero fill out of bounds.
+bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows);
+
+inline int stack_block_tiles(int mbs, int nbs, bool sym) { return sym ? nbs * (nbs + 1) / 2 : mbs * nbs; }
+
+// Fills mbs, nbs, tile0, block_tiles of every problem and launches.
+cudaError_t stack_gemm_launch(StackProb* probs, const int* counts, int n, unsigned* d_status, int num_sms,
+                              cudaStream_t stream);
+
+// ------------------------------------------------------------------ elementwise passes
+// A run of blocks of one stack, as the elementwise kernels see it.  Element (b, i, j) of a
+// caller's array is p[b * stride + i * ld + j]; of a workspace plane, q[b * rp * cp + i * cp + j]
+// with rows and columns padded to multiples of 8 (zero there).
+struct alignas(16) StackItem {
+    const void* G;        // input or gradient
+    float* M;             // momentum (nullable)
+    void* W;              // weights or output
+    __half* hi;           // workspace planes of the first block
+    __half* lo;           // nullable
+    const __half* hi2;    // gradient of the input only: X_0
+    float* info;          // per block: kStackInfo floats
+    const float* ginfo;   // gradient of the input only: info of the gradient planes
+    double* partials;     // per block: `chunks` doubles
+    long long g_stride, m_stride, w_stride;
+    int g_ld, m_ld, w_ld;
+    int rows, cols, count;
+    int chunks;           // chunks of kStackChunk padded elements per block
+    int chunk0;           // first chunk of this item in the launch
+    int g_dtype, w_dtype;
+    int vec;              // bit 0: G, bit 1: M, bit 2: W allow 8-element vector accesses
+    float decay, step;    // W <- decay * W + step * X (step kernels); X * step (output)
+};
+constexpr int kStackMaxItems = 128;
+constexpr int kStackThreads = 256;
+constexpr int kStackChunk = 8192;        // padded elements per chunk: 256 threads x 8 x 4
+// Per block: info[0] = f0 (X_0 = f0 * hi), info[1] = 2^k (hi = U * 2^k), info[2] = 1 / (N + eps),
+// info[3] = N
+constexpr int kStackInfo = 4;
+
+enum class StackPass {
+    kNorm,      // partials <- sum of U^2 (M updated in place where there is one)
+    kPack,      // info <- norms; hi, lo <- U * 2^k
+    kPackGrad,  // info2 <- norms; hi, lo <- G * 2^k * step (G: gradient of the output)
+    kOut,       // W <- hi * step
+    kUpdate,    // W <- decay * W + step * hi
+    kDot,       // partials <- sum of (hi + lo) * hi2
+    kGradOut,   // W <- gradient of the input
+};
+struct StackPassArgs {
+    float beta;             // momentum coefficient
+    int nesterov;
+    float eps;
+    const float* gscale;    // device: factor of G (nullable: 1)
+    unsigned* status;       // kNorm: cleared; kPack, kPackGrad: told of a norm that is not finite
+};
+cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const StackPassArgs& args, cudaStream_t stream);
+
+}  // namespace muon

@@ -1,0 +1,1040 @@
+// C entry points of the stacked-block operators, the global gradient norm and AdamW: argument
+// checks, scales, workspace layout and launches.
+//
+// Blocks of one shape, whatever stack they come from, form a class: their planes lie one behind the
+// other in the workspace and one problem of a launch covers them.  An iteration is three launches
+// for all classes together (Gram, polynomial, apply); tall blocks are not transposed (their Gram
+// matrix is X^T X and the apply step X B).
+//
+// Scales.  With S_t a bound of the singular values of X_t, computed from the schedule (S_0 = 1), the
+// planes hold  X_t * tau_t,  A_t * alpha_t,  B_t * gamma_t  with powers of two such that no element
+// can leave fp16's range (an element is at most the spectral norm) and ordinary ones keep all 11
+// bits: tau ~ sqrt(s) (rows of X_t have norm about 1), alpha ~ r / prod a^2 (A's mean diagonal for a
+// flat spectrum).  In the reverse pass the gradient's bound grows by max |p'| per iteration (the
+// operator norm of the derivative of a matrix function of an odd polynomial p), and delta_t keeps
+// D_t and everything formed from it within range under that bound.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "adamw.cuh"
+#include "runtime.cuh"
+#include "stacks.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kMaxSide = 32768;
+constexpr long long kMaxBlocks = 1 << 20;
+constexpr double kTop = 16384.0;               // no plane's element exceeds this (fp16: 65504)
+constexpr double kMaxSigma = 64.0;
+constexpr int kMaxTensors = 65536;
+// Newton-Schulz planes of one group of blocks; more run group after group in the same space.
+constexpr size_t kGroupBytes = static_cast<size_t>(5) << 30;
+
+bool is_dtype(int d) { return d == MUON_BF16 || d == MUON_F32 || d == MUON_F16; }
+size_t elem_size(int d) { return d == MUON_F32 ? 4 : 2; }
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int up8(int x) { return (x + 7) & ~7; }
+double pow2_floor(double x) { return std::exp2(std::floor(std::log2(x))); }
+
+// ---------------------------------------------------------------- schedule
+struct Bounds {
+    std::vector<double> sigma;    // S_0 .. S_T
+    std::vector<double> growth;   // max |p_t'| on [0, S_t]
+    std::vector<double> bmax;     // max |b l + c l^2| on [0, S_t^2]
+};
+
+// Largest |f| on [0, top] of a function whose interior extrema are among `at`.
+template <class F>
+double largest(F f, double top, const double* at, int n) {
+    double m = std::max(std::fabs(f(0.0)), std::fabs(f(top)));
+    for (int i = 0; i < n; ++i)
+        if (at[i] > 0.0 && at[i] < top) m = std::max(m, std::fabs(f(at[i])));
+    return m;
+}
+
+muon_status check_schedule(const muon_ns_schedule* s, Bounds& out) {
+    if (s == nullptr || s->coeffs == nullptr || s->n_iters < 1 || s->n_iters > MUON_MAX_NS_ITERS)
+        return MUON_ERR_INVALID_ARG;
+    if (s->fp32_mode != 0 || s->n_split_iters != 0) return MUON_ERR_INVALID_ARG;
+    if (!(s->eps > 0.f) || !std::isfinite(s->eps)) return MUON_ERR_INVALID_ARG;
+    out.sigma.assign(1, 1.01);
+    for (int t = 0; t < s->n_iters; ++t) {
+        const double a = s->coeffs[3 * t], b = s->coeffs[3 * t + 1], c = s->coeffs[3 * t + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return MUON_ERR_INVALID_ARG;
+        const double top = out.sigma.back(), lam = top * top;
+        // p' = a + 3b x + 5c x^2 in x = sigma^2: its roots are p's extrema; p'' vanishes at x = -6b / 20c
+        double at[2] = {-1.0, -1.0}, inflect[1] = {-1.0}, vertex[1] = {-1.0};
+        if (c != 0.0) {
+            const double disc = 9 * b * b - 20 * a * c;
+            if (disc >= 0.0) {
+                at[0] = (-3 * b + std::sqrt(disc)) / (10 * c);
+                at[1] = (-3 * b - std::sqrt(disc)) / (10 * c);
+            }
+            inflect[0] = -6 * b / (20 * c);
+            vertex[0] = -b / (2 * c);
+        } else if (b != 0.0) {
+            at[0] = -a / (3 * b);
+        }
+        for (double& x : at) x = x > 0.0 ? std::sqrt(x) : -1.0;
+        inflect[0] = inflect[0] > 0.0 ? std::sqrt(inflect[0]) : -1.0;
+        auto p = [=](double x) { return x * (a + x * x * (b + c * x * x)); };
+        auto dp = [=](double x) { return a + x * x * (3 * b + 5 * c * x * x); };
+        auto q = [=](double l) { return l * (b + c * l); };
+        out.growth.push_back(std::max(0.25, 1.02 * largest(dp, top, inflect, 1)));
+        out.bmax.push_back(std::max(1e-3, largest(q, lam, vertex, 1)));
+        const double next = 1.02 * largest(p, top, at, 2) + 0.01;   // room for rounding
+        if (!(next <= kMaxSigma)) return MUON_ERR_INVALID_ARG;
+        out.sigma.push_back(next);
+    }
+    return MUON_OK;
+}
+
+// ---------------------------------------------------------------- classes of equal blocks
+struct StackClass {
+    int rows = 0, cols = 0, count = 0;
+    int rp = 0, cp = 0, r = 0, s = 0, r8 = 0;   // padded sides; true and padded shorter side
+    bool tall = false;
+    int chunks = 0;
+    std::vector<double> alpha, gamma, tau;       // tau[0] unused: X_0 = f0 * plane
+    std::vector<__half*> X;                      // X_0 .. X_T
+    __half* L[2] = {nullptr, nullptr};           // second plane of X_t in L[t & 1]
+    std::vector<__half*> A, B;
+    float* info = nullptr;
+    double* partials = nullptr;
+    size_t plane() const { return static_cast<size_t>(count) * rp * cp * sizeof(__half); }
+    size_t square() const { return static_cast<size_t>(count) * r8 * r8 * sizeof(__half); }
+};
+
+StackClass make_class(int rows, int cols, const muon_ns_schedule& sch, const Bounds& bd) {
+    StackClass c;
+    c.rows = rows;
+    c.cols = cols;
+    c.rp = up8(rows);
+    c.cp = up8(cols);
+    c.tall = rows > cols;
+    c.r = std::min(rows, cols);
+    c.s = std::max(rows, cols);
+    c.r8 = up8(c.r);
+    c.chunks = static_cast<int>((static_cast<long long>(c.rp) * c.cp + kStackChunk - 1) / kStackChunk);
+    double flat = c.r;   // 1 / (mean diagonal of A_t) for a flat spectrum
+    for (int t = 0; t < sch.n_iters; ++t) {
+        const double lam = bd.sigma[t] * bd.sigma[t];
+        c.alpha.push_back(pow2_floor(std::min(std::max(flat, 1.0), kTop / lam)));
+        c.gamma.push_back(pow2_floor(std::min(c.alpha.back(), kTop / bd.bmax[t])));
+        const double a = sch.coeffs[3 * t];
+        flat = std::min(flat / std::max(a * a, 1e-6), 1e6);
+    }
+    const double root = std::exp2(std::round(0.5 * std::log2(static_cast<double>(c.s))));
+    for (int t = 0; t <= sch.n_iters; ++t) c.tau.push_back(pow2_floor(std::min(root, kTop / bd.sigma[t])));
+    return c;
+}
+
+// A run of blocks of one stack inside a group: the class it belongs to and its place there.
+struct Part {
+    int stack, first, count;   // blocks [first, first + count) of the stack
+    int cls, at;               // blocks [at, at + count) of the class
+};
+struct Group {
+    std::vector<StackClass> classes;
+    std::vector<Part> parts;
+};
+struct Shape {
+    int count, rows, cols;
+};
+
+// Cuts the stacks into groups whose planes fit `budget` bytes and whose classes fit one launch.
+std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_schedule& sch, const Bounds& bd,
+                               size_t budget) {
+    std::vector<Group> groups(1);
+    size_t used = 0;
+    for (size_t i = 0; i < shapes.size(); ++i) {
+        int first = 0;
+        while (first < shapes[i].count) {
+            Group* g = &groups.back();
+            StackClass one = make_class(shapes[i].rows, shapes[i].cols, sch, bd);
+            one.count = 1;
+            const size_t each = 4 * one.plane() + 2 * one.square() + static_cast<size_t>(one.chunks) * sizeof(double) +
+                                kStackInfo * sizeof(float);
+            int cls = -1;
+            for (size_t k = 0; k < g->classes.size(); ++k)
+                if (g->classes[k].rows == one.rows && g->classes[k].cols == one.cols) cls = static_cast<int>(k);
+            const size_t room = budget > used ? (budget - used) / each : 0;
+            int take = static_cast<int>(std::min<size_t>(shapes[i].count - first, room));
+            const bool empty = g->parts.empty();
+            if (take == 0 && empty) take = 1;                    // a single block above the budget
+            if (take == 0 || (cls < 0 && static_cast<int>(g->classes.size()) == kStackMaxProbs)) {
+                groups.emplace_back();
+                used = 0;
+                continue;
+            }
+            if (cls < 0) {
+                one.count = 0;
+                g->classes.push_back(one);
+                cls = static_cast<int>(g->classes.size()) - 1;
+            }
+            StackClass& c = g->classes[cls];
+            g->parts.push_back({static_cast<int>(i), first, take, cls, c.count});
+            c.count += take;
+            used += each * take;
+            first += take;
+        }
+    }
+    return groups;
+}
+
+// Pointers of a group's planes; `sv` takes what the reverse pass reads.  Returns the workspace used.
+size_t layout_forward(Group& g, int T, bool saving, Arena& ws, Arena& sv) {
+    for (StackClass& c : g.classes) {
+        Arena& keep = saving ? sv : ws;
+        auto take = [](Arena& a, size_t bytes) { return static_cast<uint8_t*>(a.at(a.take(bytes))); };
+        c.info = reinterpret_cast<float*>(take(keep, static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
+        c.partials = reinterpret_cast<double*>(take(ws, static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
+        c.X.assign(T + 1, nullptr);
+        c.A.assign(T, nullptr);
+        c.B.assign(T, nullptr);
+        for (int t = 0; t <= T; ++t) {
+            if (saving) c.X[t] = reinterpret_cast<__half*>(take(t < T ? keep : ws, c.plane()));
+            else c.X[t] = t < 2 ? reinterpret_cast<__half*>(take(ws, c.plane())) : c.X[t - 2];
+        }
+        for (int t = 0; t < T; ++t) {
+            c.A[t] = saving || t == 0 ? reinterpret_cast<__half*>(take(keep, c.square())) : c.A[0];
+            c.B[t] = saving || t == 0 ? reinterpret_cast<__half*>(take(keep, c.square())) : c.B[0];
+        }
+        for (auto& l : c.L) l = reinterpret_cast<__half*>(take(ws, c.plane()));
+    }
+    return align_up(ws.used, kAlign);
+}
+
+// ---------------------------------------------------------------- one class's problems
+struct Maps {   // tensor maps of one plane, by box
+    CUtensorMap k, mn;
+};
+bool make_maps(Maps& m, const __half* p, int rows, int cols, int count) {
+    return encode_stack_tmap(&m.k, p, rows, cols, count, 128) && encode_stack_tmap(&m.mn, p, rows, cols, count, 64);
+}
+
+void planes_out(StackProb& P, void* hi, void* lo, int ld, long long stride, int m_out) {
+    P.out[0] = hi;
+    P.out[1] = lo;
+    P.o_ld = ld;
+    P.o_stride = stride;
+    P.m_out = m_out;
+}
+void planes_in(StackProb& P, const __half* hi, const __half* lo, int ld, long long stride) {
+    P.E[0] = hi;
+    P.E[1] = lo;
+    P.e_ld = ld;
+    P.e_stride = stride;
+}
+
+// Sets A x B of one segment: X-like (rows x cols) and symmetric (r x r) factors.
+struct Seg {
+    const Maps* x;
+    const Maps* y;
+};
+// r x r product of two rows x cols planes over the long side: X Y^T (wide) or X^T Y (tall).
+void gram_segs(StackProb& P, const StackClass& c, std::initializer_list<Seg> segs) {
+    P.nseg = 0;
+    for (const Seg& s : segs) {
+        P.tmA[P.nseg] = c.tall ? s.x->mn : s.x->k;
+        P.tmB[P.nseg] = c.tall ? s.y->mn : s.y->k;
+        ++P.nseg;
+    }
+    P.M = P.N = c.r8;
+    P.K = c.tall ? c.rp : c.cp;
+    P.flags = kStackSym | (c.tall ? kStackAMn | kStackBMn : 0u);
+}
+// r x r product of two symmetric matrices (both read along their rows).
+void square_segs(StackProb& P, const StackClass& c, std::initializer_list<Seg> segs) {
+    P.nseg = 0;
+    for (const Seg& s : segs) {
+        P.tmA[P.nseg] = s.x->k;
+        P.tmB[P.nseg] = s.y->k;
+        ++P.nseg;
+    }
+    P.M = P.N = P.K = c.r8;
+    P.flags = kStackSym;
+}
+// Symmetric x plane (wide) or plane x symmetric (tall), rows x cols.  A pair of CTAs sweeps the tiles
+// that share its block of the plane, so the symmetric factor stays in L2.
+void apply_segs(StackProb& P, const StackClass& c, std::initializer_list<Seg> segs) {
+    P.nseg = 0;
+    for (const Seg& s : segs) {   // s.x symmetric, s.y the plane
+        P.tmA[P.nseg] = c.tall ? s.y->k : s.x->k;
+        P.tmB[P.nseg] = c.tall ? s.x->k : s.y->mn;
+        ++P.nseg;
+    }
+    P.M = c.rp;
+    P.N = c.cp;
+    P.K = c.r8;
+    P.flags = c.tall ? kStackRowMajor : kStackBMn;
+}
+
+struct Call {
+    unsigned* status = nullptr;
+    cudaStream_t stream = nullptr;
+    int sms = 148;
+};
+
+muon_status launch_gemm(std::vector<StackProb>& probs, const std::vector<int>& counts, double flops, const Call& call) {
+    const cudaError_t e = launch_timed(MUON_KERNEL_NS_GEMM, flops, call.stream, [&](cudaStream_t st) {
+        return stack_gemm_launch(probs.data(), counts.data(), static_cast<int>(probs.size()), call.status, call.sms, st);
+    });
+    return e == cudaSuccess ? MUON_OK : cuda_error(e, "stack GEMM launch");
+}
+muon_status launch_pass(StackPass pass, std::vector<StackItem>& items, const StackPassArgs& args, int kind, double bytes,
+                        const Call& call) {
+    const cudaError_t e = launch_timed(kind, bytes, call.stream, [&](cudaStream_t st) {
+        return stack_pass_launch(pass, items.data(), static_cast<int>(items.size()), args, st);
+    });
+    return e == cudaSuccess ? MUON_OK : cuda_error(e, "stack pass launch");
+}
+
+// Class order of the launches: the longest sums first, so that the last tiles are short ones.
+std::vector<int> class_order(const Group& g) {
+    std::vector<int> o(g.classes.size());
+    for (size_t i = 0; i < o.size(); ++i) o[i] = static_cast<int>(i);
+    std::stable_sort(o.begin(), o.end(), [&](int x, int y) { return g.classes[x].s > g.classes[y].s; });
+    return o;
+}
+
+// The iterations of a group.  `direct[k]` (if set) receives class k's X_T in bf16 or fp16 instead of
+// its plane.
+struct Direct {
+    void* p = nullptr;
+    int ld = 0, dtype = 0;
+    long long stride = 0;
+};
+muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vector<Direct>& direct, const Call& call) {
+    const int T = sch.n_iters;
+    const std::vector<int> order = class_order(g);
+    std::vector<std::vector<Maps>> mx(g.classes.size()), ma(g.classes.size()), mb(g.classes.size());
+    for (size_t k = 0; k < g.classes.size(); ++k) {
+        StackClass& c = g.classes[k];
+        mx[k].resize(T);
+        ma[k].resize(T);
+        mb[k].resize(T);
+        for (int t = 0; t < T; ++t) {
+            bool ok = true;
+            if (t >= 2 && c.X[t] == c.X[t - 2]) mx[k][t] = mx[k][t - 2];
+            else ok = make_maps(mx[k][t], c.X[t], c.rp, c.cp, c.count);
+            if (t >= 1 && c.A[t] == c.A[0]) {
+                ma[k][t] = ma[k][0];
+                mb[k][t] = mb[k][0];
+            } else {
+                ok = ok && make_maps(ma[k][t], c.A[t], c.r8, c.r8, c.count) &&
+                     make_maps(mb[k][t], c.B[t], c.r8, c.r8, c.count);
+            }
+            if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        }
+    }
+    for (int t = 0; t < T; ++t) {
+        const double a = sch.coeffs[3 * t], b = sch.coeffs[3 * t + 1], cc = sch.coeffs[3 * t + 2];
+        for (int stage = 0; stage < 3; ++stage) {
+            std::vector<StackProb> probs;
+            std::vector<int> counts;
+            double flops = 0.0;
+            for (int k : order) {
+                StackClass& c = g.classes[k];
+                const long long sq = static_cast<long long>(c.r8) * c.r8, pl = static_cast<long long>(c.rp) * c.cp;
+                StackProb P;
+                std::memset(&P, 0, sizeof(P));
+                if (stage == 0) {
+                    gram_segs(P, c, {{&mx[k][t], &mx[k][t]}});
+                    planes_out(P, c.A[t], nullptr, c.r8, sq, c.r8);
+                    P.alpha = static_cast<float>(t == 0 ? c.alpha[0] : c.alpha[t] / (c.tau[t] * c.tau[t]));
+                    if (t == 0) { P.dscale = c.info; P.scale_pow = 2; }
+                    flops += static_cast<double>(c.count) * c.r * c.r * c.s;
+                } else if (stage == 1) {
+                    square_segs(P, c, {{&ma[k][t], &ma[k][t]}});
+                    planes_in(P, c.A[t], nullptr, c.r8, sq);
+                    planes_out(P, c.B[t], nullptr, c.r8, sq, c.r8);
+                    P.alpha = static_cast<float>(cc * c.gamma[t] / (c.alpha[t] * c.alpha[t]));
+                    P.beta = static_cast<float>(b * c.gamma[t] / c.alpha[t]);
+                    flops += static_cast<double>(c.count) * c.r * c.r * c.r;
+                } else {
+                    apply_segs(P, c, {{&mb[k][t], &mx[k][t]}});
+                    planes_in(P, c.X[t], c.L[t & 1], c.cp, pl);
+                    double up = c.tau[t + 1];
+                    if (t + 1 == T && direct[k].p != nullptr) {
+                        planes_out(P, direct[k].p, nullptr, direct[k].ld, direct[k].stride, c.rows);
+                        if (direct[k].dtype == MUON_BF16) P.flags |= kStackOutBf16;
+                        up = 1.0;
+                    } else {
+                        planes_out(P, c.X[t + 1], t + 1 < T ? c.L[(t + 1) & 1] : nullptr, c.cp, pl, c.rp);
+                    }
+                    const double down = t == 0 ? 1.0 : c.tau[t];
+                    P.alpha = static_cast<float>(up / (c.gamma[t] * down));
+                    P.beta = static_cast<float>(a * up / down);
+                    if (t == 0) { P.dscale = c.info; P.scale_pow = 1; }
+                    flops += 2.0 * c.count * c.r * c.r * c.s;
+                }
+                probs.push_back(P);
+                counts.push_back(c.count);
+            }
+            const muon_status st = launch_gemm(probs, counts, flops, call);
+            if (st != MUON_OK) return st;
+        }
+    }
+    return MUON_OK;
+}
+
+// ---------------------------------------------------------------- arguments
+// The arrays that are written: blocks one behind the other, or side by side within a row pitch.
+bool blocks_apart(int count, int rows, int cols, int ld, long long stride) {
+    if (count <= 1) return true;
+    const long long span = static_cast<long long>(rows - 1) * ld + cols;
+    if (stride >= span) return true;
+    return stride >= cols && (static_cast<long long>(count) - 1) * stride + cols <= ld;
+}
+
+muon_status check_view(const void* p, int dtype, int count, int rows, int cols, int ld, long long stride, bool written) {
+    if (p == nullptr || !is_dtype(dtype)) return MUON_ERR_INVALID_ARG;
+    if (count <= 0 || rows <= 0 || cols <= 0 || stride < 0 || ld < 0) return MUON_ERR_INVALID_ARG;
+    if (rows > kMaxSide || cols > kMaxSide || count > kMaxBlocks) return MUON_ERR_UNSUPPORTED_SHAPE;
+    if (rows > 1 && ld < cols) return MUON_ERR_INVALID_ARG;
+    if (written && !blocks_apart(count, rows, cols, rows > 1 ? ld : cols, stride)) return MUON_ERR_INVALID_ARG;
+    if (!aligned_to(p, elem_size(dtype))) return MUON_ERR_ALIGNMENT;
+    return MUON_OK;
+}
+
+// 8-element vector accesses: base, row pitch and block stride are multiples of 16 bytes.
+bool vec_ok(const void* p, int dtype, int ld, long long stride) {
+    const int per16 = 16 / static_cast<int>(elem_size(dtype));
+    return aligned_to(p, 16) && ld % per16 == 0 && stride % per16 == 0;
+}
+
+muon_status check_total(const std::vector<Shape>& shapes) {
+    long long blocks = 0;
+    for (const Shape& s : shapes) blocks += s.count;
+    return blocks > kMaxBlocks ? MUON_ERR_UNSUPPORTED_SHAPE : MUON_OK;
+}
+
+muon_status check_stacks(const ns_stack_desc* d, int n, std::vector<Shape>& shapes) {
+    if (d == nullptr || n <= 0 || n > kMaxBlocks) return MUON_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        muon_status st = check_view(d[i].X, d[i].x_dtype, d[i].count, d[i].rows, d[i].cols, d[i].x_ld, d[i].x_stride, false);
+        if (st == MUON_OK)
+            st = check_view(d[i].Y, d[i].y_dtype, d[i].count, d[i].rows, d[i].cols, d[i].y_ld, d[i].y_stride, true);
+        if (st != MUON_OK) return st;
+        shapes.push_back({d[i].count, d[i].rows, d[i].cols});
+    }
+    return check_total(shapes);
+}
+
+muon_status check_muon(const muon_stack_desc* d, int n, const muon_hyper* hp, std::vector<Shape>& shapes, Bounds& bd) {
+    if (d == nullptr || hp == nullptr || n <= 0 || n > kMaxBlocks) return MUON_ERR_INVALID_ARG;
+    muon_status st = check_schedule(&hp->ns, bd);
+    if (st != MUON_OK) return st;
+    if (!std::isfinite(hp->lr) || !std::isfinite(hp->beta) || !std::isfinite(hp->weight_decay)) return MUON_ERR_INVALID_ARG;
+    if (hp->nesterov != 0 && hp->nesterov != 1) return MUON_ERR_INVALID_ARG;
+    if (hp->scale_mode < MUON_SCALE_MOONLIGHT || hp->scale_mode > MUON_SCALE_NAIVE) return MUON_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        const muon_stack_desc& s = d[i];
+        st = check_view(s.W, s.w_dtype, s.count, s.rows, s.cols, s.w_ld, s.w_stride, true);
+        if (st == MUON_OK) st = check_view(s.G, s.g_dtype, s.count, s.rows, s.cols, s.g_ld, s.g_stride, false);
+        if (st == MUON_OK) st = check_view(s.M, MUON_F32, s.count, s.rows, s.cols, s.m_ld, s.m_stride, true);
+        if (st != MUON_OK) return st;
+        shapes.push_back({s.count, s.rows, s.cols});
+    }
+    return check_total(shapes);
+}
+
+double shape_scale(int rows, int cols, int mode) {
+    const double o = rows, i = cols;
+    switch (mode) {
+        case MUON_SCALE_MOONLIGHT: return 0.2 * std::sqrt(std::max(o, i));
+        case MUON_SCALE_KJ: return std::sqrt(std::max(1.0, o / i));
+        case MUON_SCALE_MUP: return std::sqrt(o / i);
+        default: return 1.0;
+    }
+}
+
+// ---------------------------------------------------------------- layouts
+size_t forward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& sch, const Bounds& bd, bool saving,
+                     size_t* saved) {
+    size_t most = 0, kept = 0;
+    for (Group& g : make_groups(shapes, sch, bd, saving ? SIZE_MAX : kGroupBytes)) {
+        Arena ws, sv;
+        sv.used = kept;
+        most = std::max(most, layout_forward(g, sch.n_iters, saving, ws, sv));
+        kept = align_up(sv.used, kAlign);
+    }
+    if (saved) *saved = kept;
+    return kHeaderBytes + most;
+}
+
+// Planes of the reverse pass of a group.
+struct GradPlanes {
+    __half* D[2][2];     // [ping/pong][plane]
+    __half* S;
+    __half* P;
+    float* info;
+    double* partials;
+};
+std::vector<GradPlanes> layout_backward(const Group& g, Arena& ws) {
+    std::vector<GradPlanes> out;
+    for (const StackClass& c : g.classes) {
+        GradPlanes p;
+        auto take = [&](size_t bytes) { return ws.at(ws.take(bytes)); };
+        p.info = static_cast<float*>(take(static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
+        p.partials = static_cast<double*>(take(static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
+        for (auto& b : p.D)
+            for (auto& x : b) x = static_cast<__half*>(take(c.plane()));
+        p.S = static_cast<__half*>(take(c.square()));
+        p.P = static_cast<__half*>(take(c.square()));
+        out.push_back(p);
+    }
+    return out;
+}
+size_t backward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& sch, const Bounds& bd) {
+    size_t most = 0;
+    for (Group& g : make_groups(shapes, sch, bd, SIZE_MAX)) {
+        Arena ws;
+        layout_backward(g, ws);
+        most = std::max(most, align_up(ws.used, kAlign));
+    }
+    return kHeaderBytes + most;
+}
+
+StackItem base_item(const StackClass& c, const Part& p) {
+    StackItem it;
+    std::memset(&it, 0, sizeof(it));
+    it.rows = c.rows;
+    it.cols = c.cols;
+    it.count = p.count;
+    it.chunks = c.chunks;
+    it.info = c.info + static_cast<size_t>(p.at) * kStackInfo;
+    it.partials = c.partials + static_cast<size_t>(p.at) * c.chunks;
+    return it;
+}
+size_t plane_at(const StackClass& c, const Part& p) { return static_cast<size_t>(p.at) * c.rp * c.cp; }
+
+const uint8_t* bytes_at(const void* p, long long blocks, long long stride, int dtype) {
+    return static_cast<const uint8_t*>(p) + static_cast<size_t>(blocks) * stride * elem_size(dtype);
+}
+
+// ---------------------------------------------------------------- forward
+muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shapes, const muon_ns_schedule& sch,
+                          const Bounds& bd, void* saved, void* workspace, const Call& call) {
+    const bool saving = saved != nullptr;
+    const int T = sch.n_iters;
+    size_t kept = 0;
+    bool first = true;
+    for (Group& g : make_groups(shapes, sch, bd, saving ? SIZE_MAX : kGroupBytes)) {
+        Arena ws, sv;
+        ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+        sv.base = static_cast<uint8_t*>(saved);
+        sv.used = kept;
+        layout_forward(g, T, saving, ws, sv);
+        kept = align_up(sv.used, kAlign);
+        std::vector<Direct> direct(g.classes.size());
+        std::vector<int> parts_of(g.classes.size(), 0);
+        for (const Part& p : g.parts) ++parts_of[p.cls];
+        std::vector<StackItem> in, out;
+        double read = 0.0, written = 0.0;
+        for (const Part& p : g.parts) {
+            const StackClass& c = g.classes[p.cls];
+            const ns_stack_desc& s = d[p.stack];
+            StackItem it = base_item(c, p);
+            const double n = static_cast<double>(p.count) * c.rows * c.cols;
+            it.G = bytes_at(s.X, p.first, s.x_stride, s.x_dtype);
+            it.g_stride = s.x_stride;
+            it.g_ld = s.x_ld;
+            it.g_dtype = s.x_dtype;
+            it.vec = vec_ok(it.G, s.x_dtype, s.x_ld, s.x_stride) ? 1 : 0;
+            it.hi = c.X[0] + plane_at(c, p);
+            it.lo = c.L[0] + plane_at(c, p);
+            in.push_back(it);
+            read += n * elem_size(s.x_dtype);
+            StackItem o = base_item(c, p);
+            o.W = const_cast<uint8_t*>(bytes_at(s.Y, p.first, s.y_stride, s.y_dtype));
+            o.w_stride = s.y_stride;
+            o.w_ld = s.y_ld;
+            o.w_dtype = s.y_dtype;
+            o.vec = vec_ok(o.W, s.y_dtype, s.y_ld, s.y_stride) ? 4 : 0;
+            o.hi = c.X[T] + plane_at(c, p);
+            o.step = static_cast<float>(1.0 / c.tau[T]);
+            // The last product writes a 16-bit result where it belongs, if one stack is the whole class
+            // and its rows are whole 16-byte pieces.
+            if (parts_of[p.cls] == 1 && s.y_dtype != MUON_F32 && c.cols % 8 == 0 && o.vec) {
+                direct[p.cls] = {o.W, s.y_ld, s.y_dtype, s.y_stride};
+            } else {
+                out.push_back(o);
+                written += n * elem_size(s.y_dtype);
+            }
+        }
+        StackPassArgs args = {};
+        args.eps = sch.eps;
+        args.status = first ? call.status : nullptr;
+        muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_SCALE, read, call);
+        if (st != MUON_OK) return st;
+        args.status = call.status;
+        st = launch_pass(StackPass::kPack, in, args, MUON_KERNEL_MOMENTUM, 2 * read, call);
+        if (st != MUON_OK) return st;
+        st = run_iterations(g, sch, direct, call);
+        if (st != MUON_OK) return st;
+        if (!out.empty()) {
+            st = launch_pass(StackPass::kOut, out, args, MUON_KERNEL_MISC, 2 * written, call);
+            if (st != MUON_OK) return st;
+        }
+        first = false;
+    }
+    return MUON_OK;
+}
+
+// ---------------------------------------------------------------- reverse pass
+muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, const muon_ns_schedule& sch,
+                     const Bounds& bd, const void* saved, void* workspace, const Call& call) {
+    const int T = sch.n_iters;
+    size_t kept = 0;
+    bool first = true;
+    for (Group& g : make_groups(shapes, sch, bd, SIZE_MAX)) {
+        Arena ws, sv, fw;
+        ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+        sv.base = static_cast<uint8_t*>(const_cast<void*>(saved));
+        sv.used = kept;
+        layout_forward(g, T, true, fw, sv);   // the saved planes' places
+        kept = align_up(sv.used, kAlign);
+        std::vector<GradPlanes> gp = layout_backward(g, ws);
+        const std::vector<int> order = class_order(g);
+        const size_t nc = g.classes.size();
+
+        // delta[k][t]: D_t's planes hold D_t * 2^k * delta_t
+        std::vector<std::vector<double>> delta(nc, std::vector<double>(T + 1));
+        for (size_t k = 0; k < nc; ++k) {
+            const StackClass& c = g.classes[k];
+            double nu = 1.0;   // bound of |D_t| relative to the incoming gradient
+            for (int t = T; t >= 0; --t) {
+                double most = 1.0;
+                if (t > 0) {
+                    const int u = t - 1;
+                    const double lam = bd.sigma[u] * bd.sigma[u];
+                    const double inv_tau = u == 0 ? 2.0 / std::sqrt(static_cast<double>(c.rows) * c.cols) : 1.0 / c.tau[u];
+                    const double pf = 2.0 * c.gamma[u] * inv_tau * bd.sigma[u] *
+                                      (std::fabs(sch.coeffs[3 * u + 1]) + 2.0 * std::fabs(sch.coeffs[3 * u + 2]) * lam);
+                    most = std::max({1.0, bd.sigma[u], pf});
+                }
+                delta[k][t] = pow2_floor(kTop / (nu * most));
+                if (t > 0) nu *= bd.growth[t - 1];
+            }
+        }
+
+        std::vector<StackItem> in, dot, out;
+        double read = 0.0;
+        for (const Part& p : g.parts) {
+            const StackClass& c = g.classes[p.cls];
+            const GradPlanes& q = gp[p.cls];
+            const ns_stack_desc& s = d[p.stack];
+            StackItem it = base_item(c, p);
+            it.partials = q.partials + static_cast<size_t>(p.at) * c.chunks;
+            StackItem o = it;
+            it.info = q.info + static_cast<size_t>(p.at) * kStackInfo;
+            it.G = bytes_at(s.X, p.first, s.x_stride, s.x_dtype);
+            it.g_stride = s.x_stride;
+            it.g_ld = s.x_ld;
+            it.g_dtype = s.x_dtype;
+            it.vec = vec_ok(it.G, s.x_dtype, s.x_ld, s.x_stride) ? 1 : 0;
+            it.hi = q.D[T & 1][0] + plane_at(c, p);
+            it.lo = q.D[T & 1][1] + plane_at(c, p);
+            it.step = static_cast<float>(delta[p.cls][T]);
+            in.push_back(it);
+            read += static_cast<double>(p.count) * c.rows * c.cols * elem_size(s.x_dtype);
+            o.ginfo = it.info;
+            o.hi = q.D[0][0] + plane_at(c, p);
+            o.lo = q.D[0][1] + plane_at(c, p);
+            o.hi2 = c.X[0] + plane_at(c, p);
+            o.W = const_cast<uint8_t*>(bytes_at(s.Y, p.first, s.y_stride, s.y_dtype));
+            o.w_stride = s.y_stride;
+            o.w_ld = s.y_ld;
+            o.w_dtype = s.y_dtype;
+            o.vec = vec_ok(o.W, s.y_dtype, s.y_ld, s.y_stride) ? 4 : 0;
+            o.step = static_cast<float>(delta[p.cls][0]);
+            out.push_back(o);
+        }
+        StackPassArgs args = {};
+        args.eps = sch.eps;
+        args.status = first ? call.status : nullptr;
+        muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_SCALE, read, call);
+        if (st != MUON_OK) return st;
+        args.status = call.status;
+        st = launch_pass(StackPass::kPackGrad, in, args, MUON_KERNEL_MOMENTUM, 2 * read, call);
+        if (st != MUON_OK) return st;
+
+        std::vector<std::vector<Maps>> mx(nc), ma(nc), mb(nc);
+        std::vector<Maps> md[2] = {std::vector<Maps>(nc), std::vector<Maps>(nc)}, ms(nc), mp(nc);
+        for (size_t k = 0; k < nc; ++k) {
+            const StackClass& c = g.classes[k];
+            mx[k].resize(T);
+            ma[k].resize(T);
+            mb[k].resize(T);
+            bool ok = make_maps(ms[k], gp[k].S, c.r8, c.r8, c.count) && make_maps(mp[k], gp[k].P, c.r8, c.r8, c.count) &&
+                      make_maps(md[0][k], gp[k].D[0][0], c.rp, c.cp, c.count) &&
+                      make_maps(md[1][k], gp[k].D[1][0], c.rp, c.cp, c.count);
+            for (int t = 0; t < T && ok; ++t)
+                ok = make_maps(mx[k][t], c.X[t], c.rp, c.cp, c.count) && make_maps(ma[k][t], c.A[t], c.r8, c.r8, c.count) &&
+                     make_maps(mb[k][t], c.B[t], c.r8, c.r8, c.count);
+            if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        }
+        for (int t = T - 1; t >= 0; --t) {
+            const double a = sch.coeffs[3 * t], b = sch.coeffs[3 * t + 1], cc = sch.coeffs[3 * t + 2];
+            const int cur = (t + 1) & 1, nxt = t & 1;
+            for (int stage = 0; stage < 3; ++stage) {
+                std::vector<StackProb> probs;
+                std::vector<int> counts;
+                double flops = 0.0;
+                for (int k : order) {
+                    const StackClass& c = g.classes[k];
+                    const GradPlanes& q = gp[k];
+                    const long long sq = static_cast<long long>(c.r8) * c.r8, pl = static_cast<long long>(c.rp) * c.cp;
+                    const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t];   // t = 0: f0 comes as dscale
+                    StackProb P;
+                    std::memset(&P, 0, sizeof(P));
+                    if (stage == 0) {          // S = (D X^T + X D^T) / 2
+                        gram_segs(P, c, {{&md[cur][k], &mx[k][t]}, {&mx[k][t], &md[cur][k]}});
+                        planes_out(P, q.S, nullptr, c.r8, sq, c.r8);
+                        P.alpha = static_cast<float>(0.5 * inv_tau);
+                        flops += 2.0 * c.count * c.r * c.r * c.s;
+                    } else if (stage == 1) {   // P * 2 gamma / tau, P = bS + c(SA + AS)
+                        square_segs(P, c, {{&ms[k], &ma[k][t]}, {&ma[k][t], &ms[k]}});
+                        planes_in(P, q.S, nullptr, c.r8, sq);
+                        planes_out(P, q.P, nullptr, c.r8, sq, c.r8);
+                        P.alpha = static_cast<float>(cc * 2.0 * c.gamma[t] * inv_tau / c.alpha[t]);
+                        P.beta = static_cast<float>(b * 2.0 * c.gamma[t] * inv_tau);
+                        flops += 2.0 * c.count * c.r * c.r * c.r;
+                    } else {                   // D' = aD + BD + 2PX
+                        apply_segs(P, c, {{&mb[k][t], &md[cur][k]}, {&mp[k], &mx[k][t]}});
+                        planes_in(P, q.D[cur][0], q.D[cur][1], c.cp, pl);
+                        planes_out(P, q.D[nxt][0], q.D[nxt][1], c.cp, pl, c.rp);
+                        const double kappa = delta[k][t] / delta[k][t + 1];
+                        P.alpha = static_cast<float>(kappa / c.gamma[t]);
+                        P.beta = static_cast<float>(kappa * a);
+                        flops += 4.0 * c.count * c.r * c.r * c.s;
+                    }
+                    if (t == 0 && stage < 2) { P.dscale = c.info; P.scale_pow = 1; }
+                    probs.push_back(P);
+                    counts.push_back(c.count);
+                }
+                st = launch_gemm(probs, counts, flops, call);
+                if (st != MUON_OK) return st;
+            }
+        }
+        dot = out;
+        st = launch_pass(StackPass::kDot, dot, args, MUON_KERNEL_SCALE, 0.0, call);
+        if (st != MUON_OK) return st;
+        st = launch_pass(StackPass::kGradOut, out, args, MUON_KERNEL_MISC, 2 * read, call);
+        if (st != MUON_OK) return st;
+        first = false;
+    }
+    return MUON_OK;
+}
+
+// ---------------------------------------------------------------- Muon step
+muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, const muon_hyper& hp, const Bounds& bd,
+                 const float* grad_scale, void* workspace, const Call& call) {
+    const int T = hp.ns.n_iters;
+    bool first = true;
+    for (Group& g : make_groups(shapes, hp.ns, bd, kGroupBytes)) {
+        Arena ws, sv;
+        ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+        layout_forward(g, T, false, ws, sv);
+        std::vector<StackItem> in, out;
+        double norm_bytes = 0.0, pack_bytes = 0.0, upd_bytes = 0.0;
+        for (const Part& p : g.parts) {
+            const StackClass& c = g.classes[p.cls];
+            const muon_stack_desc& s = d[p.stack];
+            StackItem it = base_item(c, p);
+            it.G = bytes_at(s.G, p.first, s.g_stride, s.g_dtype);
+            it.M = reinterpret_cast<float*>(const_cast<uint8_t*>(bytes_at(s.M, p.first, s.m_stride, MUON_F32)));
+            it.W = const_cast<uint8_t*>(bytes_at(s.W, p.first, s.w_stride, s.w_dtype));
+            it.g_stride = s.g_stride; it.m_stride = s.m_stride; it.w_stride = s.w_stride;
+            it.g_ld = s.g_ld; it.m_ld = s.m_ld; it.w_ld = s.w_ld;
+            it.g_dtype = s.g_dtype; it.w_dtype = s.w_dtype;
+            it.vec = (vec_ok(it.G, s.g_dtype, s.g_ld, s.g_stride) ? 1 : 0) |
+                     (vec_ok(it.M, MUON_F32, s.m_ld, s.m_stride) ? 2 : 0) |
+                     (vec_ok(it.W, s.w_dtype, s.w_ld, s.w_stride) ? 4 : 0);
+            it.hi = c.X[0] + plane_at(c, p);
+            it.lo = c.L[0] + plane_at(c, p);
+            in.push_back(it);
+            it.hi = c.X[T] + plane_at(c, p);
+            it.decay = static_cast<float>(1.0 - static_cast<double>(hp.lr) * hp.weight_decay);
+            it.step = static_cast<float>(-static_cast<double>(hp.lr) * shape_scale(c.rows, c.cols, hp.scale_mode) / c.tau[T]);
+            out.push_back(it);
+            const double n = static_cast<double>(p.count) * c.rows * c.cols;
+            norm_bytes += n * (elem_size(s.g_dtype) + 8.0);
+            pack_bytes += n * ((hp.nesterov ? elem_size(s.g_dtype) : 0.0) + 8.0);
+            upd_bytes += n * (2.0 * elem_size(s.w_dtype) + 2.0);
+        }
+        StackPassArgs args = {};
+        args.eps = hp.ns.eps;
+        args.beta = hp.beta;
+        args.nesterov = hp.nesterov;
+        args.gscale = grad_scale;
+        args.status = first ? call.status : nullptr;
+        muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_MOMENTUM, norm_bytes, call);
+        if (st != MUON_OK) return st;
+        args.status = call.status;
+        st = launch_pass(StackPass::kPack, in, args, MUON_KERNEL_MISC, pack_bytes, call);
+        if (st != MUON_OK) return st;
+        st = run_iterations(g, hp.ns, std::vector<Direct>(g.classes.size()), call);
+        if (st != MUON_OK) return st;
+        st = launch_pass(StackPass::kUpdate, out, args, MUON_KERNEL_UPDATE, upd_bytes, call);
+        if (st != MUON_OK) return st;
+        first = false;
+    }
+    return MUON_OK;
+}
+
+muon_status make_call(Call& call, void* workspace, void* stream) {
+    call.status = static_cast<unsigned*>(workspace);
+    call.stream = static_cast<cudaStream_t>(stream);
+    call.sms = device_sm_count();
+    cudaGetLastError();   // an earlier, unrelated error is not this call's
+    return MUON_OK;
+}
+
+// ---------------------------------------------------------------- norm, AdamW
+muon_status check_tensors(const adamw_tensor_desc* d, int n, bool all) {
+    if (d == nullptr || n <= 0 || n > kMaxTensors) return MUON_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        const adamw_tensor_desc& t = d[i];
+        if (t.n < 0 || !is_dtype(t.g_dtype) || (all && !is_dtype(t.w_dtype))) return MUON_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (t.G == nullptr || (all && (t.W == nullptr || t.m == nullptr || t.v == nullptr))) return MUON_ERR_INVALID_ARG;
+        if (!aligned_to(t.G, elem_size(t.g_dtype))) return MUON_ERR_ALIGNMENT;
+        if (all && (!aligned_to(t.W, elem_size(t.w_dtype)) || !aligned_to(t.m, 4) || !aligned_to(t.v, 4)))
+            return MUON_ERR_ALIGNMENT;
+    }
+    return MUON_OK;
+}
+std::vector<AdamItem> adam_items(const adamw_tensor_desc* d, int n) {
+    std::vector<AdamItem> items;
+    items.reserve(n);
+    for (int i = 0; i < n; ++i) {
+        if (d[i].n == 0) continue;
+        AdamItem it;
+        std::memset(&it, 0, sizeof(it));
+        it.W = d[i].W; it.G = d[i].G; it.m = d[i].m; it.v = d[i].v;
+        it.n = d[i].n;
+        it.w_dtype = d[i].w_dtype; it.g_dtype = d[i].g_dtype;
+        it.vec = (aligned_to(it.G, 16) ? 1 : 0) | (aligned_to(it.m, 16) && aligned_to(it.v, 16) ? 2 : 0) |
+                 (aligned_to(it.W, 16) ? 4 : 0);
+        items.push_back(it);
+    }
+    return items;
+}
+constexpr int kMostSms = 256;   // the norm's partials: room for any device of this architecture
+size_t norm_bytes(int n) {
+    const size_t launches = (static_cast<size_t>(n) + kAdamMaxItems - 1) / kAdamMaxItems;
+    return kHeaderBytes + align_up(launches * kMostSms * kAdamCtasPerSm * sizeof(double), kAlign);
+}
+
+}  // namespace
+
+bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows) {
+    using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    if (fn == nullptr) return false;
+    const cuuint64_t gdim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
+    const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * rows * 2};
+    const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+    const cuuint32_t estride[3] = {1u, 1u, 1u};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t ns_stacks_workspace_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch, int with_saved) {
+    size_t bytes = 0;
+    no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        muon_status st = check_schedule(sch, bd);
+        if (st == MUON_OK) st = check_stacks(descs, n, shapes);
+        if (st == MUON_OK) bytes = forward_bytes(shapes, *sch, bd, with_saved != 0, nullptr);
+        return st;
+    });
+    return bytes;
+}
+
+size_t ns_stacks_saved_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch) {
+    size_t bytes = 0;
+    no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        muon_status st = check_schedule(sch, bd);
+        if (st == MUON_OK) st = check_stacks(descs, n, shapes);
+        if (st == MUON_OK) forward_bytes(shapes, *sch, bd, true, &bytes);
+        return st;
+    });
+    return bytes;
+}
+
+muon_status ns_orthogonalize_stacks(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch, void* saved,
+                                    size_t saved_bytes, void* workspace, size_t ws_bytes, void* stream) {
+    return no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        muon_status st = check_schedule(sch, bd);
+        if (st == MUON_OK) st = check_stacks(descs, n, shapes);
+        if (st != MUON_OK) return st;
+        if (workspace == nullptr) return MUON_ERR_INVALID_ARG;
+        if (!aligned_to(workspace, 256) || !aligned_to(saved, 256)) return MUON_ERR_ALIGNMENT;
+        size_t kept = 0;
+        const size_t need = forward_bytes(shapes, *sch, bd, saved != nullptr, &kept);
+        if (ws_bytes < need || (saved != nullptr && saved_bytes < kept)) return MUON_ERR_WORKSPACE_TOO_SMALL;
+        Call call;
+        st = make_call(call, workspace, stream);
+        if (st != MUON_OK) return st;
+        return orthogonalize(descs, shapes, *sch, bd, saved, workspace, call);
+    });
+}
+
+size_t ns_stacks_backward_workspace_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch) {
+    size_t bytes = 0;
+    no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        muon_status st = check_schedule(sch, bd);
+        if (st == MUON_OK) st = check_stacks(descs, n, shapes);
+        if (st == MUON_OK) bytes = backward_bytes(shapes, *sch, bd);
+        return st;
+    });
+    return bytes;
+}
+
+muon_status ns_orthogonalize_stacks_backward(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch,
+                                             const void* saved, size_t saved_bytes, void* workspace, size_t ws_bytes,
+                                             void* stream) {
+    return no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        muon_status st = check_schedule(sch, bd);
+        if (st == MUON_OK) st = check_stacks(descs, n, shapes);
+        if (st != MUON_OK) return st;
+        if (workspace == nullptr || saved == nullptr) return MUON_ERR_INVALID_ARG;
+        if (!aligned_to(workspace, 256) || !aligned_to(saved, 256)) return MUON_ERR_ALIGNMENT;
+        size_t kept = 0;
+        forward_bytes(shapes, *sch, bd, true, &kept);
+        if (saved_bytes < kept || ws_bytes < backward_bytes(shapes, *sch, bd)) return MUON_ERR_WORKSPACE_TOO_SMALL;
+        Call call;
+        st = make_call(call, workspace, stream);
+        if (st != MUON_OK) return st;
+        return backward(descs, shapes, *sch, bd, saved, workspace, call);
+    });
+}
+
+size_t muon_stacks_workspace_size(const muon_stack_desc* descs, int n, const muon_hyper* hp) {
+    size_t bytes = 0;
+    no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        const muon_status st = check_muon(descs, n, hp, shapes, bd);
+        if (st == MUON_OK) bytes = forward_bytes(shapes, hp->ns, bd, false, nullptr);
+        return st;
+    });
+    return bytes;
+}
+
+muon_status muon_step_stacks(const muon_stack_desc* descs, int n, const muon_hyper* hp, const float* grad_scale,
+                             void* workspace, size_t ws_bytes, void* stream) {
+    return no_throw([&] {
+        std::vector<Shape> shapes;
+        Bounds bd;
+        muon_status st = check_muon(descs, n, hp, shapes, bd);
+        if (st != MUON_OK) return st;
+        if (workspace == nullptr) return MUON_ERR_INVALID_ARG;
+        if (!aligned_to(workspace, 256) || !aligned_to(grad_scale, 4)) return MUON_ERR_ALIGNMENT;
+        if (ws_bytes < forward_bytes(shapes, hp->ns, bd, false, nullptr)) return MUON_ERR_WORKSPACE_TOO_SMALL;
+        Call call;
+        st = make_call(call, workspace, stream);
+        if (st != MUON_OK) return st;
+        return step(descs, shapes, *hp, bd, grad_scale, workspace, call);
+    });
+}
+
+size_t grad_norm_workspace_size(const adamw_tensor_desc* descs, int n) {
+    return check_tensors(descs, n, false) == MUON_OK ? norm_bytes(n) : 0;
+}
+
+muon_status grad_norm_batched(const adamw_tensor_desc* descs, int n, float max_norm, float* out, void* workspace,
+                              size_t ws_bytes, void* stream) {
+    return no_throw([&] {
+        muon_status st = check_tensors(descs, n, false);
+        if (st != MUON_OK) return st;
+        if (out == nullptr || workspace == nullptr || !(max_norm > 0.f)) return MUON_ERR_INVALID_ARG;
+        if (!aligned_to(out, 4) || !aligned_to(workspace, 256)) return MUON_ERR_ALIGNMENT;
+        if (ws_bytes < norm_bytes(n)) return MUON_ERR_WORKSPACE_TOO_SMALL;
+        Call call;
+        st = make_call(call, workspace, stream);
+        if (st != MUON_OK) return st;
+        const std::vector<AdamItem> items = adam_items(descs, n);
+        double* partials = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+        double bytes = 0.0;
+        for (const AdamItem& it : items) bytes += static_cast<double>(it.n) * elem_size(it.g_dtype);
+        const cudaError_t e = launch_timed(MUON_KERNEL_GRAD_NORM, bytes, call.stream, [&](cudaStream_t s) {
+            return grad_norm_launch(items.data(), static_cast<int>(items.size()), partials, max_norm, out, call.status,
+                                    std::min(call.sms, kMostSms), s);
+        });
+        return e == cudaSuccess ? MUON_OK : cuda_error(e, "gradient norm launch");
+    });
+}
+
+muon_status adamw_step_batched(const adamw_tensor_desc* descs, int n, const adamw_hyper* hp, const float* grad_scale,
+                               void* stream) {
+    return no_throw([&] {
+        muon_status st = check_tensors(descs, n, true);
+        if (st != MUON_OK) return st;
+        if (hp == nullptr || !std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay)) return MUON_ERR_INVALID_ARG;
+        if (!(hp->beta1 >= 0.0 && hp->beta1 < 1.0) || !(hp->beta2 >= 0.0 && hp->beta2 < 1.0)) return MUON_ERR_INVALID_ARG;
+        if (!(hp->eps >= 0.0) || !std::isfinite(hp->eps)) return MUON_ERR_INVALID_ARG;
+        if (hp->step_dev == nullptr && hp->step < 1) return MUON_ERR_INVALID_ARG;
+        if (!aligned_to(grad_scale, 4) || !aligned_to(hp->step_dev, 8)) return MUON_ERR_ALIGNMENT;
+        const std::vector<AdamItem> items = adam_items(descs, n);
+        AdamParams p = {};
+        const double t = static_cast<double>(hp->step);
+        p.lr = static_cast<float>(hp->lr);
+        p.beta1 = static_cast<float>(hp->beta1);
+        p.beta2 = static_cast<float>(hp->beta2);
+        p.omb1 = static_cast<float>(1.0 - hp->beta1);
+        p.omb2 = static_cast<float>(1.0 - hp->beta2);
+        p.eps = static_cast<float>(hp->eps);
+        p.decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
+        p.beta1_d = hp->beta1;
+        p.beta2_d = hp->beta2;
+        if (hp->step_dev == nullptr) {
+            p.c1 = static_cast<float>(1.0 / (1.0 - std::pow(p.beta1_d, t)));
+            p.c2 = static_cast<float>(1.0 / (1.0 - std::pow(p.beta2_d, t)));
+        }
+        p.step = hp->step_dev;
+        p.gscale = grad_scale;
+        double bytes = 0.0;
+        for (const AdamItem& it : items)
+            bytes += static_cast<double>(it.n) * (elem_size(it.g_dtype) + 2.0 * elem_size(it.w_dtype) + 16.0);
+        const int sms = device_sm_count();
+        cudaGetLastError();
+        const cudaError_t e = launch_timed(MUON_KERNEL_ADAMW, bytes, static_cast<cudaStream_t>(stream), [&](cudaStream_t s) {
+            return adamw_launch(items.data(), static_cast<int>(items.size()), p, sms, s);
+        });
+        return e == cudaSuccess ? MUON_OK : cuda_error(e, "AdamW launch");
+    });
+}
+
+}  // extern "C"

@@ -6,13 +6,16 @@ weight_decay, nesterov, ns_steps, scale_mode.  ``MuonCayley`` mirrors the optimi
 the Stiefel-manifold page (mlqm.cn/news/1339166, §4.3) for its Cayley branch.  Both hand
 every matrix of a parameter group to one library call per step; grouping parameters
 into Muon matrices and AdamW tensors stays with the caller, as the pages advise, so
-these classes accept 2-D parameters only.
+these classes accept 2-D parameters only.  ``StackedMuon`` takes the fused and stacked forms of
+such matrices (heads of a QKV weight, experts, any sizes), ``AdamW`` the rest, and
+``clip_scale`` the gradient norm over all of them.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding as mb
+from . import stacks as ms
 
 KJ_COEFFS = (3.4445, -4.7750, 2.0315)
 
@@ -115,4 +118,112 @@ class MuonCayley(torch.optim.Optimizer):
                 ws = self._ws.get(mb.muon_cayley_workspace_size(1, n, k), p.device)
                 mb.muon_cayley_step(p.data, p.grad.contiguous(), state["momentum_buffer"], group["lr"],
                                     group["momentum"], ws, center=group["center"])
+        return loss
+
+
+def clip_scale(params, max_norm: float, workspaces=None):
+    """A device tensor [norm, scale] of the parameters' gradients: their norm together and
+    min(1, max_norm / (norm + 1e-6)).  scale = out[1:] goes to the step() of StackedMuon and AdamW as
+    `grad_scale`, which leaves the gradients as they are and needs no synchronisation."""
+    grads = [p.grad.contiguous() for p in params if p.grad is not None]
+    if not grads:
+        raise ValueError("no parameter has a gradient")
+    out = torch.empty(2, dtype=torch.float32, device=grads[0].device)
+    ws = (workspaces or _Workspaces()).get(mb.grad_norm_workspace_size(grads), grads[0].device)
+    mb.grad_norm_batched(grads, max_norm, out, ws)
+    return out
+
+
+class StackedMuon(torch.optim.Optimizer):
+    """The Muon step on blocks of parameters: a 3-D parameter [count, rows, cols] is a stack of blocks
+    (experts); a 2-D one is a block, or, with the group option ``row_block`` or ``col_block``, a stack
+    of blocks of that many rows or columns (heads of a fused QKV weight, the halves of a fused gate/up
+    weight).  Any sizes; bf16, fp16 or fp32 parameters.  One grouped call per param group."""
+
+    def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.01, nesterov=True, ns_steps=5,
+                 scale_mode="moonlight", coeffs=None, eps=1e-7, row_block=None, col_block=None):
+        if scale_mode not in mb.SCALE_MODES:
+            raise ValueError(f"scale_mode must be one of {sorted(mb.SCALE_MODES)}")
+        super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
+                                      ns_steps=ns_steps, scale_mode=scale_mode, coeffs=coeffs, eps=eps,
+                                      row_block=row_block, col_block=col_block))
+        for g in self.param_groups:
+            for p in g["params"]:
+                if p.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+                    raise ValueError(f"unsupported parameter dtype {p.dtype}")
+                self._blocks(p, g)
+        self._ws = _Workspaces()
+
+    @staticmethod
+    def _blocks(t, group):
+        if group["row_block"] is not None and group["col_block"] is not None:
+            raise ValueError("give row_block or col_block, not both")
+        if t.dim() == 2 and group["row_block"] is not None:
+            return ms.row_blocks(t, group["row_block"])
+        if t.dim() == 2 and group["col_block"] is not None:
+            return ms.col_blocks(t, group["col_block"])
+        if t.dim() not in (2, 3):
+            raise ValueError(f"StackedMuon handles matrices and stacks of them, got shape {tuple(t.shape)}; "
+                             "give embeddings, heads, biases and norms to AdamW")
+        return t
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            stacks = []
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                state = self.state[p]
+                if "momentum_buffer" not in state:
+                    state["momentum_buffer"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                stacks.append(mb.MuonStack(*(self._blocks(t, group) for t in
+                                             (p.data, p.grad.contiguous(), state["momentum_buffer"]))))
+            if not stacks:
+                continue
+            coeffs = group["coeffs"] or [KJ_COEFFS] * group["ns_steps"]
+            hp = mb.hyper(group["lr"], group["momentum"], group["weight_decay"], group["nesterov"],
+                          group["scale_mode"], mb.Schedule(coeffs, eps=group["eps"]))
+            ws = self._ws.get(mb.muon_stacks_workspace_size(stacks, hp), stacks[0].W.device)
+            mb.muon_step_stacks(stacks, hp, ws, grad_scale=grad_scale)
+        return loss
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW for what Muon does not take, one grouped call per param group.  Parameters of any shape,
+    dense, bf16, fp16 or fp32; moments in fp32."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01):
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+        for g in self.param_groups:
+            for p in g["params"]:
+                if p.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+                    raise ValueError(f"unsupported parameter dtype {p.dtype}")
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            by_step = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                state = self.state[p]
+                if "step" not in state:
+                    state["step"] = 0
+                    state["exp_avg"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                    state["exp_avg_sq"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                state["step"] += 1
+                by_step.setdefault(state["step"], []).append(
+                    mb.AdamWTensor(p.data, p.grad.contiguous(), state["exp_avg"], state["exp_avg_sq"]))
+            hp = mb.adamw_hyper(group["lr"], *group["betas"], group["eps"], group["weight_decay"])
+            for step, tensors in by_step.items():
+                mb.adamw_step_batched(tensors, hp, step, grad_scale=grad_scale)
         return loss

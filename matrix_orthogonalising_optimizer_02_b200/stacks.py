@@ -1,0 +1,74 @@
+"""Newton-Schulz orthogonalisation of stacks of blocks as a differentiable torch function, and the
+views that cut a fused parameter into its blocks."""
+from __future__ import annotations
+
+import torch
+
+from . import binding as mb
+
+KJ_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def row_blocks(p, rows: int):
+    """A [n * rows, cols] matrix as the stack of its n row blocks (heads of a fused projection)."""
+    if p.dim() != 2 or rows <= 0 or p.shape[0] % rows:
+        raise ValueError(f"cannot cut shape {tuple(p.shape)} into blocks of {rows} rows")
+    return p.unflatten(0, (p.shape[0] // rows, rows))
+
+
+def col_blocks(p, cols: int):
+    """A [rows, n * cols] matrix as the stack of its n column blocks (a fused input projection)."""
+    if p.dim() != 2 or cols <= 0 or p.shape[1] % cols:
+        raise ValueError(f"cannot cut shape {tuple(p.shape)} into blocks of {cols} columns")
+    return p.unflatten(1, (p.shape[1] // cols, cols)).transpose(0, 1)
+
+
+def _unit_last(t):
+    """t itself where the library can read it in place (unit stride in the last dimension, row pitch of
+    at least a row), else a dense copy."""
+    ok = (t.shape[-1] == 1 or t.stride(-1) == 1) and (t.shape[-2] == 1 or t.stride(-2) >= t.shape[-1])
+    return t if ok else t.contiguous()
+
+
+class _Orthogonalize(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, schedule, dtype):
+        x3 = _unit_last(x.detach())
+        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+        st = [mb.Stack(x3, y)]
+        need = ctx.needs_input_grad[0]
+        ws = mb.workspace(mb.ns_stacks_workspace_size(st, schedule, need), device=x.device)
+        saved = mb.workspace(mb.ns_stacks_saved_size(st, schedule), device=x.device) if need else None
+        mb.ns_orthogonalize_stacks(st, schedule, ws, saved=saved)
+        ctx.schedule, ctx.dtype = schedule, x.dtype
+        if need:
+            ctx.save_for_backward(saved)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        (saved,) = ctx.saved_tensors
+        if dy.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+            dy = dy.float()
+        dx = torch.empty(dy.shape, dtype=ctx.dtype, device=dy.device)
+        st = [mb.Stack(_unit_last(dy), dx)]
+        ws = mb.workspace(mb.ns_stacks_backward_workspace_size(st, ctx.schedule), device=dy.device)
+        mb.ns_orthogonalize_stacks_backward(st, ctx.schedule, saved, ws)
+        return dx, None, None
+
+
+def orthogonalize(x, steps: int = 5, coeffs=KJ_COEFFS, eps: float = 1e-7, dtype=None):
+    """Every [rows, cols] block of x ([rows, cols] or [count, rows, cols]; bf16, fp16 or fp32) after
+    `steps` Newton-Schulz iterations with `coeffs` ((a, b, c), or a sequence of `steps` of them), in
+    `dtype` (x's own if None).  Differentiable with respect to x, once.
+
+    With the optimizer's coefficients the singular values of the result lie near 1 (0.7 to 1.2); a
+    parametrisation that needs orthonormal blocks takes converging ones, such as (1.875, -1.25, 0.375).
+    The iterates run on the tensor cores in fp16 with scales of their own (see ns_orthogonalize_stacks
+    in the C header for the accuracy)."""
+    coeffs = list(coeffs)
+    per_step = [tuple(coeffs)] * steps if not isinstance(coeffs[0], (tuple, list)) else coeffs
+    if len(per_step) != steps:
+        raise ValueError(f"{len(per_step)} coefficient triples for {steps} steps")
+    return _Orthogonalize.apply(x, mb.Schedule(per_step, eps=eps), dtype if dtype is not None else x.dtype)
