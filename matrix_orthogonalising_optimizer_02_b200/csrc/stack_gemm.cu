@@ -351,6 +351,11 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(r[j]);
+                if (col0 == row0 && P.diag != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j == lane) v[j] -= P.diag;
+                }
                 if (e0 != nullptr && !below) {
                     const uint8_t* src = stg_e + (c & 1) * STG_BYTES;
 #pragma unroll

@@ -15,7 +15,7 @@ namespace muon {
 
 // ------------------------------------------------------------------ grouped fp16 GEMM
 // One problem of a launch: `count` products of one shape,
-//   out[b] = f_b * (alpha * sum_seg A_seg[b] x B_seg[b] + beta * (E[0][b] + E[1][b])),
+//   out[b] = f_b * (alpha * sum_seg A_seg[b] x B_seg[b] + beta * (E[0][b] + E[1][b])) - diag * I,
 // f_b = dscale[b]^scale_pow, fp16 operands with fp32 accumulation in TMEM.  The K loop runs
 // over up to two operand pairs (segments) of the same K.  E and out are fp16 planes (value =
 // plane 0 + plane 1, plane 1 optional) with a row pitch and a block stride of their own.
@@ -37,6 +37,7 @@ struct alignas(64) StackProb {
     int m_out;                       // rows stored (<= M)
     int nseg;
     float alpha, beta;
+    float diag;                      // subtracted on the diagonal of out
     int scale_pow;
     uint32_t flags;
     int mbs, nbs;                    // 256 x 256 tiles of a block
@@ -98,8 +99,41 @@ struct StackPassArgs {
     int nesterov;
     float eps;
     const float* gscale;    // device: factor of G (nullable: 1)
-    unsigned* status;       // kNorm: cleared; kPack, kPackGrad: told of a norm that is not finite
+    unsigned* status;       // kNorm: cleared (unless null); kPack, kPackGrad: told of a norm that is not finite
 };
 cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const StackPassArgs& args, cudaStream_t stream);
+
+// ------------------------------------------------------------------ blocks with a short side <= 128
+// One cluster per block runs everything: momentum, norm, iterations, update or output.
+constexpr int kSmallStackSide = 128;     // longest short side
+constexpr int kSmallStackSlab = 512;     // columns of a CTA's slab at most
+constexpr int kSmallStackItems = 64;
+constexpr int kSmallStackCtas = 148;     // CTAs (one per SM) that run at once
+struct SmallStackItem {
+    const void* G;
+    float* M;             // nullable: orthogonalisation alone
+    void* W;              // W <- decay * W + step * X; decay = 0: output only
+    long long g_stride, m_stride, w_stride;
+    int g_ld, m_ld, w_ld;
+    int count, block0;
+    int g_dtype, w_dtype;
+    int vec;              // as StackItem
+    float decay, step;
+};
+struct SmallStackIter {
+    float zs;             // X^ = fp16(zs * Z)
+    float ga, diag;       // fp16 A = ga * Gram - diag on the diagonal
+    float pb, pc;         // B~ = pb * A + pc * A^2
+};
+struct SmallStackClass {
+    SmallStackIter it[32];
+    int rows, cols, cluster, slab, iters;   // slab: a multiple of 64, cluster * slab >= long side
+    float unit, out;      // Z_0 = unit * X_0; X_T = out * Z
+    float beta, eps;
+    int nesterov;
+    const float* gscale;
+    unsigned* status;
+};
+cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream);
 
 }  // namespace muon

@@ -13,6 +13,14 @@
 // flat spectrum).  In the reverse pass the gradient's bound grows by max |p'| per iteration (the
 // operator norm of the derivative of a matrix function of an odd polynomial p), and delta_t keeps
 // D_t and everything formed from it within range under that bound.
+//
+// Shift.  For a converging schedule the Gram matrix is stored as A - l I with l = sigma_t^2, sigma_t the
+// iterates of a flat spectrum (l -> 1): bA + cA^2 = (b + 2cl)(A - lI) + c(A - lI)^2 + (bl + cl^2) I, and the
+// last term joins a.  Where X nears its polar factor the stored matrices near zero and their roundings
+// vanish with them: a near-orthogonal 96 x 640 block is 5e-5 off 64 bits (2.2e-4 without), the worst case,
+// a rank-32 block with noise, 1.8e-4 (1.5e-4).  The optimizer's schedules scatter the singular values over
+// 0.7 .. 1.2 and cannot raise tiny ones to 1: there the shift costs accuracy on low-rank blocks (6e-3
+// against 8e-4), so they go without.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -43,6 +51,7 @@ struct Bounds {
     std::vector<double> sigma;    // S_0 .. S_T
     std::vector<double> growth;   // max |p_t'| on [0, S_t]
     std::vector<double> bmax;     // max |b l + c l^2| on [0, S_t^2]
+    bool converging = true;       // p_t(1) = 1 and |p_t'(1)| <= 1/2 throughout
 };
 
 // Largest |f| on [0, top] of a function whose interior extrema are among `at`.
@@ -82,6 +91,7 @@ muon_status check_schedule(const muon_ns_schedule* s, Bounds& out) {
         auto p = [=](double x) { return x * (a + x * x * (b + c * x * x)); };
         auto dp = [=](double x) { return a + x * x * (3 * b + 5 * c * x * x); };
         auto q = [=](double l) { return l * (b + c * l); };
+        if (std::fabs(p(1.0) - 1.0) > 1e-3 || std::fabs(dp(1.0)) > 0.5) out.converging = false;
         out.growth.push_back(std::max(0.25, 1.02 * largest(dp, top, inflect, 1)));
         out.bmax.push_back(std::max(1e-3, largest(q, lam, vertex, 1)));
         const double next = 1.02 * largest(p, top, at, 2) + 0.01;   // room for rounding
@@ -98,6 +108,7 @@ struct StackClass {
     bool tall = false;
     int chunks = 0;
     std::vector<double> alpha, gamma, tau;       // tau[0] unused: X_0 = f0 * plane
+    std::vector<double> shift, a, b;             // l; a + bl + cl^2 and b + 2cl (a and b without a shift)
     std::vector<__half*> X;                      // X_0 .. X_T
     __half* L[2] = {nullptr, nullptr};           // second plane of X_t in L[t & 1]
     std::vector<__half*> A, B;
@@ -119,16 +130,70 @@ StackClass make_class(int rows, int cols, const muon_ns_schedule& sch, const Bou
     c.r8 = up8(c.r);
     c.chunks = static_cast<int>((static_cast<long long>(c.rp) * c.cp + kStackChunk - 1) / kStackChunk);
     double flat = c.r;   // 1 / (mean diagonal of A_t) for a flat spectrum
+    double sigma = 1.0 / std::sqrt(static_cast<double>(c.r));
     for (int t = 0; t < sch.n_iters; ++t) {
         const double lam = bd.sigma[t] * bd.sigma[t];
         c.alpha.push_back(pow2_floor(std::min(std::max(flat, 1.0), kTop / lam)));
-        c.gamma.push_back(pow2_floor(std::min(c.alpha.back(), kTop / bd.bmax[t])));
-        const double a = sch.coeffs[3 * t];
+        c.gamma.push_back(pow2_floor(std::min(c.alpha.back(), kTop / (2.0 * bd.bmax[t]))));
+        const double a = sch.coeffs[3 * t], b = sch.coeffs[3 * t + 1], q = sch.coeffs[3 * t + 2];
+        const double l = bd.converging ? sigma * sigma : 0.0;
+        c.shift.push_back(l);
+        c.a.push_back(a + l * (b + l * q));
+        c.b.push_back(b + 2.0 * q * l);
+        sigma *= a + sigma * sigma * (b + sigma * sigma * q);
         flat = std::min(flat / std::max(a * a, 1e-6), 1e6);
     }
     const double root = std::exp2(std::round(0.5 * std::log2(static_cast<double>(c.s))));
     for (int t = 0; t <= sch.n_iters; ++t) c.tau.push_back(pow2_floor(std::min(root, kTop / bd.sigma[t])));
     return c;
+}
+
+// ---------------------------------------------------------------- classes that run on chip
+// The scales of a class whose blocks run in one cluster each (stack_small.cu), or false where they do not:
+// a long side above 8 slabs, or a schedule whose product of coefficients a leaves the range in which the
+// state's unit keeps X^ and B~ inside fp16.
+bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, const Bounds& bd, SmallStackClass& k) {
+    const int r = std::min(rows, cols), s = std::max(rows, cols);
+    if (r > kSmallStackSide || s > 8 * kSmallStackSlab) return false;
+    const StackClass c = make_class(rows, cols, sch, bd);
+    const int T = sch.n_iters;
+    double pa = 1.0, top = 1.0;
+    for (int t = 0; t < T; ++t) {
+        if (!(c.a[t] >= 0.125 && c.a[t] <= 8.0)) return false;
+        pa *= c.a[t];
+        top = std::max(top, pa);
+        if (!(pa >= 1.0 / 65536 && pa <= 65536.0)) return false;
+    }
+    std::memset(&k, 0, sizeof(k));
+    const double tau0 = std::exp2(std::min(14.0, std::round(0.5 * std::log2(static_cast<double>(r) * s))));
+    const double unit = pow2_floor(2.0 * top) * c.tau[T] * 16.0;
+    pa = 1.0;
+    for (int t = 0; t < T; ++t) {
+        const double tau = t == 0 ? tau0 : c.tau[t];
+        SmallStackIter& f = k.it[t];
+        f.zs = static_cast<float>(pa * tau / unit);
+        f.ga = static_cast<float>(c.alpha[t] / (tau * tau));
+        f.diag = static_cast<float>(c.alpha[t] * c.shift[t]);
+        pa *= c.a[t];
+        const double kappa = unit / (pa * tau);
+        if (!(kappa >= 0.0625 && kappa * 2.0 * bd.bmax[t] <= 2.0 * kTop)) return false;
+        f.pb = static_cast<float>(kappa * c.b[t] / c.alpha[t]);
+        f.pc = static_cast<float>(kappa * sch.coeffs[3 * t + 2] / (c.alpha[t] * c.alpha[t]));
+    }
+    k.rows = rows;
+    k.cols = cols;
+    k.iters = T;
+    k.unit = static_cast<float>(unit);
+    k.out = static_cast<float>(pa / unit);
+    k.eps = sch.eps;
+    // As few CTAs as hold the block; more while all blocks' CTAs still run at once.
+    const int pieces = (s + 63) / 64;
+    int C = 1;
+    while (C * kSmallStackSlab < s) C *= 2;
+    while (2 * C <= 8 && 2 * C <= pieces && 2ll * C * blocks <= kSmallStackCtas) C *= 2;
+    k.cluster = C;
+    k.slab = (pieces + C - 1) / C * 64;
+    return true;
 }
 
 // A run of blocks of one stack inside a group: the class it belongs to and its place there.
@@ -142,7 +207,42 @@ struct Group {
 };
 struct Shape {
     int count, rows, cols;
+    bool small = false;        // runs on chip: takes no part in the groups
 };
+
+// The small classes of a call, by shape, and the stacks of each.
+struct SmallSet {
+    SmallStackClass k;
+    std::vector<int> stacks;
+};
+std::vector<SmallSet> find_small(std::vector<Shape>& shapes, const muon_ns_schedule& sch, const Bounds& bd) {
+    std::vector<SmallSet> sets;
+    std::vector<std::pair<int, int>> no;
+    for (size_t i = 0; i < shapes.size(); ++i) {
+        const int rows = shapes[i].rows, cols = shapes[i].cols;
+        if (std::min(rows, cols) > kSmallStackSide) continue;
+        bool known = false;
+        for (SmallSet& s : sets)
+            if (s.k.rows == rows && s.k.cols == cols) {
+                s.stacks.push_back(static_cast<int>(i));
+                shapes[i].small = known = true;
+            }
+        for (auto& n : no) known = known || (n.first == rows && n.second == cols);
+        if (known) continue;
+        long long blocks = 0;
+        for (const Shape& s : shapes)
+            if (s.rows == rows && s.cols == cols) blocks += s.count;
+        SmallSet s;
+        if (small_class(rows, cols, static_cast<int>(blocks), sch, bd, s.k)) {
+            s.stacks.push_back(static_cast<int>(i));
+            shapes[i].small = true;
+            sets.push_back(s);
+        } else {
+            no.push_back({rows, cols});
+        }
+    }
+    return sets;
+}
 
 // Cuts the stacks into groups whose planes fit `budget` bytes and whose classes fit one launch.
 std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_schedule& sch, const Bounds& bd,
@@ -150,6 +250,7 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
     std::vector<Group> groups(1);
     size_t used = 0;
     for (size_t i = 0; i < shapes.size(); ++i) {
+        if (shapes[i].small) continue;
         int first = 0;
         while (first < shapes[i].count) {
             Group* g = &groups.back();
@@ -181,6 +282,7 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
             first += take;
         }
     }
+    if (groups.back().parts.empty()) groups.pop_back();
     return groups;
 }
 
@@ -284,6 +386,22 @@ muon_status launch_gemm(std::vector<StackProb>& probs, const std::vector<int>& c
     });
     return e == cudaSuccess ? MUON_OK : cuda_error(e, "stack GEMM launch");
 }
+muon_status launch_small(const std::vector<SmallStackItem>& items, const SmallStackClass& k, double flops, const Call& call) {
+    const cudaError_t e = launch_timed(MUON_KERNEL_NS_GEMM, flops, call.stream, [&](cudaStream_t st) {
+        return stack_small_launch(items.data(), static_cast<int>(items.size()), k, st);
+    });
+    return e == cudaSuccess ? MUON_OK : cuda_error(e, "small-block launch");
+}
+double small_flops(const SmallStackClass& k, double blocks) {
+    const double r = std::min(k.rows, k.cols), s = std::max(k.rows, k.cols);
+    return blocks * k.iters * (3.0 * r * r * s + r * r * r);
+}
+// Clears the status word ahead of the small launches (the passes of a group clear it themselves).
+muon_status clear_status(const Call& call) {
+    const cudaError_t e = cudaMemsetAsync(call.status, 0, sizeof(unsigned), call.stream);
+    return e == cudaSuccess ? MUON_OK : cuda_error(e, "status clear");
+}
+
 muon_status launch_pass(StackPass pass, std::vector<StackItem>& items, const StackPassArgs& args, int kind, double bytes,
                         const Call& call) {
     const cudaError_t e = launch_timed(kind, bytes, call.stream, [&](cudaStream_t st) {
@@ -331,13 +449,14 @@ muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vec
         }
     }
     for (int t = 0; t < T; ++t) {
-        const double a = sch.coeffs[3 * t], b = sch.coeffs[3 * t + 1], cc = sch.coeffs[3 * t + 2];
+        const double cc = sch.coeffs[3 * t + 2];
         for (int stage = 0; stage < 3; ++stage) {
             std::vector<StackProb> probs;
             std::vector<int> counts;
             double flops = 0.0;
             for (int k : order) {
                 StackClass& c = g.classes[k];
+                const double a = c.a[t], b = c.b[t];
                 const long long sq = static_cast<long long>(c.r8) * c.r8, pl = static_cast<long long>(c.rp) * c.cp;
                 StackProb P;
                 std::memset(&P, 0, sizeof(P));
@@ -345,6 +464,7 @@ muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vec
                     gram_segs(P, c, {{&mx[k][t], &mx[k][t]}});
                     planes_out(P, c.A[t], nullptr, c.r8, sq, c.r8);
                     P.alpha = static_cast<float>(t == 0 ? c.alpha[0] : c.alpha[t] / (c.tau[t] * c.tau[t]));
+                    P.diag = static_cast<float>(c.alpha[t] * c.shift[t]);
                     if (t == 0) { P.dscale = c.info; P.scale_pow = 2; }
                     flops += static_cast<double>(c.count) * c.r * c.r * c.s;
                 } else if (stage == 1) {
@@ -517,12 +637,42 @@ const uint8_t* bytes_at(const void* p, long long blocks, long long stride, int d
 }
 
 // ---------------------------------------------------------------- forward
-muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shapes, const muon_ns_schedule& sch,
-                          const Bounds& bd, void* saved, void* workspace, const Call& call) {
+muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shapes, std::vector<SmallSet>& small,
+                          const muon_ns_schedule& sch, const Bounds& bd, void* saved, void* workspace, const Call& call) {
     const bool saving = saved != nullptr;
     const int T = sch.n_iters;
     size_t kept = 0;
     bool first = true;
+    if (!small.empty()) {
+        const muon_status st = clear_status(call);
+        if (st != MUON_OK) return st;
+        first = false;
+    }
+    for (SmallSet& set : small) {
+        std::vector<SmallStackItem> items;
+        double blocks = 0.0;
+        for (int i : set.stacks) {
+            const ns_stack_desc& s = d[i];
+            SmallStackItem it;
+            std::memset(&it, 0, sizeof(it));
+            it.G = s.X;
+            it.W = s.Y;
+            it.g_stride = s.x_stride;
+            it.w_stride = s.y_stride;
+            it.g_ld = s.x_ld;
+            it.w_ld = s.y_ld;
+            it.g_dtype = s.x_dtype;
+            it.w_dtype = s.y_dtype;
+            it.count = s.count;
+            it.vec = (vec_ok(s.X, s.x_dtype, s.x_ld, s.x_stride) ? 1 : 0) | (vec_ok(s.Y, s.y_dtype, s.y_ld, s.y_stride) ? 4 : 0);
+            it.step = 1.f;
+            items.push_back(it);
+            blocks += s.count;
+        }
+        set.k.status = call.status;
+        const muon_status st = launch_small(items, set.k, small_flops(set.k, blocks), call);
+        if (st != MUON_OK) return st;
+    }
     for (Group& g : make_groups(shapes, sch, bd, saving ? SIZE_MAX : kGroupBytes)) {
         Arena ws, sv;
         ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
@@ -614,7 +764,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                     const double lam = bd.sigma[u] * bd.sigma[u];
                     const double inv_tau = u == 0 ? 2.0 / std::sqrt(static_cast<double>(c.rows) * c.cols) : 1.0 / c.tau[u];
                     const double pf = 2.0 * c.gamma[u] * inv_tau * bd.sigma[u] *
-                                      (std::fabs(sch.coeffs[3 * u + 1]) + 2.0 * std::fabs(sch.coeffs[3 * u + 2]) * lam);
+                                      (std::fabs(c.b[u]) + 2.0 * std::fabs(sch.coeffs[3 * u + 2]) * lam);
                     most = std::max({1.0, bd.sigma[u], pf});
                 }
                 delta[k][t] = pow2_floor(kTop / (nu * most));
@@ -679,7 +829,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
         }
         for (int t = T - 1; t >= 0; --t) {
-            const double a = sch.coeffs[3 * t], b = sch.coeffs[3 * t + 1], cc = sch.coeffs[3 * t + 2];
+            const double cc = sch.coeffs[3 * t + 2];
             const int cur = (t + 1) & 1, nxt = t & 1;
             for (int stage = 0; stage < 3; ++stage) {
                 std::vector<StackProb> probs;
@@ -688,6 +838,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                 for (int k : order) {
                     const StackClass& c = g.classes[k];
                     const GradPlanes& q = gp[k];
+                    const double a = c.a[t], b = c.b[t];
                     const long long sq = static_cast<long long>(c.r8) * c.r8, pl = static_cast<long long>(c.rp) * c.cp;
                     const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t];   // t = 0: f0 comes as dscale
                     StackProb P;
@@ -732,10 +883,48 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
 }
 
 // ---------------------------------------------------------------- Muon step
-muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, const muon_hyper& hp, const Bounds& bd,
-                 const float* grad_scale, void* workspace, const Call& call) {
+int step_vec(const muon_stack_desc& s) {
+    return (vec_ok(s.G, s.g_dtype, s.g_ld, s.g_stride) ? 1 : 0) | (vec_ok(s.M, MUON_F32, s.m_ld, s.m_stride) ? 2 : 0) |
+           (vec_ok(s.W, s.w_dtype, s.w_ld, s.w_stride) ? 4 : 0);
+}
+
+muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, std::vector<SmallSet>& small,
+                 const muon_hyper& hp, const Bounds& bd, const float* grad_scale, void* workspace, const Call& call) {
     const int T = hp.ns.n_iters;
     bool first = true;
+    if (!small.empty()) {
+        const muon_status st = clear_status(call);
+        if (st != MUON_OK) return st;
+        first = false;
+    }
+    for (SmallSet& set : small) {
+        std::vector<SmallStackItem> items;
+        double blocks = 0.0;
+        for (int i : set.stacks) {
+            const muon_stack_desc& s = d[i];
+            SmallStackItem it;
+            std::memset(&it, 0, sizeof(it));
+            it.G = s.G;
+            it.M = s.M;
+            it.W = s.W;
+            it.g_stride = s.g_stride; it.m_stride = s.m_stride; it.w_stride = s.w_stride;
+            it.g_ld = s.g_ld; it.m_ld = s.m_ld; it.w_ld = s.w_ld;
+            it.g_dtype = s.g_dtype;
+            it.w_dtype = s.w_dtype;
+            it.count = s.count;
+            it.vec = step_vec(s);
+            it.decay = static_cast<float>(1.0 - static_cast<double>(hp.lr) * hp.weight_decay);
+            it.step = static_cast<float>(-static_cast<double>(hp.lr) * shape_scale(s.rows, s.cols, hp.scale_mode));
+            items.push_back(it);
+            blocks += s.count;
+        }
+        set.k.beta = hp.beta;
+        set.k.nesterov = hp.nesterov;
+        set.k.gscale = grad_scale;
+        set.k.status = call.status;
+        const muon_status st = launch_small(items, set.k, small_flops(set.k, blocks), call);
+        if (st != MUON_OK) return st;
+    }
     for (Group& g : make_groups(shapes, hp.ns, bd, kGroupBytes)) {
         Arena ws, sv;
         ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
@@ -752,9 +941,7 @@ muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, con
             it.g_stride = s.g_stride; it.m_stride = s.m_stride; it.w_stride = s.w_stride;
             it.g_ld = s.g_ld; it.m_ld = s.m_ld; it.w_ld = s.w_ld;
             it.g_dtype = s.g_dtype; it.w_dtype = s.w_dtype;
-            it.vec = (vec_ok(it.G, s.g_dtype, s.g_ld, s.g_stride) ? 1 : 0) |
-                     (vec_ok(it.M, MUON_F32, s.m_ld, s.m_stride) ? 2 : 0) |
-                     (vec_ok(it.W, s.w_dtype, s.w_ld, s.w_stride) ? 4 : 0);
+            it.vec = step_vec(s);   // a later first block keeps it: its offset is a multiple of the stride
             it.hi = c.X[0] + plane_at(c, p);
             it.lo = c.L[0] + plane_at(c, p);
             in.push_back(it);
@@ -868,6 +1055,7 @@ size_t ns_stacks_workspace_size(const ns_stack_desc* descs, int n, const muon_ns
         Bounds bd;
         muon_status st = check_schedule(sch, bd);
         if (st == MUON_OK) st = check_stacks(descs, n, shapes);
+        if (st == MUON_OK && !with_saved) find_small(shapes, *sch, bd);
         if (st == MUON_OK) bytes = forward_bytes(shapes, *sch, bd, with_saved != 0, nullptr);
         return st;
     });
@@ -898,12 +1086,14 @@ muon_status ns_orthogonalize_stacks(const ns_stack_desc* descs, int n, const muo
         if (workspace == nullptr) return MUON_ERR_INVALID_ARG;
         if (!aligned_to(workspace, 256) || !aligned_to(saved, 256)) return MUON_ERR_ALIGNMENT;
         size_t kept = 0;
+        std::vector<SmallSet> small;   // the reverse pass reads what only the grouped launches keep
+        if (saved == nullptr) small = find_small(shapes, *sch, bd);
         const size_t need = forward_bytes(shapes, *sch, bd, saved != nullptr, &kept);
         if (ws_bytes < need || (saved != nullptr && saved_bytes < kept)) return MUON_ERR_WORKSPACE_TOO_SMALL;
         Call call;
         st = make_call(call, workspace, stream);
         if (st != MUON_OK) return st;
-        return orthogonalize(descs, shapes, *sch, bd, saved, workspace, call);
+        return orthogonalize(descs, shapes, small, *sch, bd, saved, workspace, call);
     });
 }
 
@@ -947,7 +1137,10 @@ size_t muon_stacks_workspace_size(const muon_stack_desc* descs, int n, const muo
         std::vector<Shape> shapes;
         Bounds bd;
         const muon_status st = check_muon(descs, n, hp, shapes, bd);
-        if (st == MUON_OK) bytes = forward_bytes(shapes, hp->ns, bd, false, nullptr);
+        if (st == MUON_OK) {
+            find_small(shapes, hp->ns, bd);
+            bytes = forward_bytes(shapes, hp->ns, bd, false, nullptr);
+        }
         return st;
     });
     return bytes;
@@ -962,11 +1155,12 @@ muon_status muon_step_stacks(const muon_stack_desc* descs, int n, const muon_hyp
         if (st != MUON_OK) return st;
         if (workspace == nullptr) return MUON_ERR_INVALID_ARG;
         if (!aligned_to(workspace, 256) || !aligned_to(grad_scale, 4)) return MUON_ERR_ALIGNMENT;
+        std::vector<SmallSet> small = find_small(shapes, hp->ns, bd);
         if (ws_bytes < forward_bytes(shapes, hp->ns, bd, false, nullptr)) return MUON_ERR_WORKSPACE_TOO_SMALL;
         Call call;
         st = make_call(call, workspace, stream);
         if (st != MUON_OK) return st;
-        return step(descs, shapes, *hp, bd, grad_scale, workspace, call);
+        return step(descs, shapes, small, *hp, bd, grad_scale, workspace, call);
     });
 }
 

@@ -137,7 +137,7 @@ def test_refused_muon_hyper():
         assert lib.muon_step_stacks(_muon(), 1, ctypes.byref(hp[0]), None, WS, 1 << 30, None) == INVALID
     hp = mb.hyper(0.1)
     assert lib.muon_step_stacks(_muon(), 1, ctypes.byref(hp[0]), ctypes.c_void_p(P + 2), WS, 1 << 30, None) == ALIGN
-    assert lib.muon_step_stacks(_muon(), 1, ctypes.byref(hp[0]), None, WS, 300, None) == SMALL
+    assert lib.muon_step_stacks(_muon(), 1, ctypes.byref(hp[0]), None, WS, 255, None) == SMALL
     assert lib.muon_step_stacks(_muon(), 1, None, None, WS, 1 << 30, None) == INVALID
 
 
