@@ -13,14 +13,16 @@
 //  - X^ = fp16(X * tau) in shared memory as 64-column panels of 128 rows x 128 bytes, 128-byte swizzled.
 //    The same panel is a K-major operand (Gram matrix, K = columns) and an MN-major one (apply, N =
 //    columns).
-// Per iteration: the slab's Gram matrix (M = N = 128, K = w); its rows go to their owner CTAs through
-// distributed shared memory, which sum them in a fixed order and send fp16 A to every CTA; every CTA
-// forms B~ = kappa (bA + cA^2) for itself; Z += B~ X^.  Three cluster barriers an iteration, the first
-// split around the conversion of Z to X^.
+// Per iteration: the slab's Gram matrix (M = N = 128, K = w); its rows go to their owner CTAs by
+// asynchronous stores to distributed shared memory that count on the receiver's mbarrier, the owners sum
+// them in rank order and send fp16 A to every CTA the same way; every CTA forms B~ = kappa (bA + cA^2)
+// for itself; Z += B~ X^.  One cluster barrier an iteration, split around the conversion of Z to X^, says
+// that a CTA's buffers are free again.  (With cluster barriers after each exchange and rows of 16 bytes
+// per lane an iteration at w = 512 took 12.2 us, 5.6 of them in the exchanges.)
 //
-// In and out: one coalesced pass over G and M (M written, norm in fp64), a second one that hits L2
-// (a wave of clusters holds 75 MB), results back through the same staging.  A step reads and writes each
-// byte of HBM once.
+// In and out: one coalesced pass over G and M (M written, norm in fp64) puts U into TMEM as it is; once
+// the norm is known it is scaled there.  Results go back through the same staging.  A step reads and
+// writes each byte of HBM once.
 #include <atomic>
 #include <cmath>
 
@@ -34,7 +36,7 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int PANEL = 128 * 128;                 // bytes: 128 rows x 64 fp16
 constexpr int A_BYTES = 2 * PANEL;               // 128 x 128 fp16
-constexpr int RED_BYTES = 128 * 128 * 4;         // the owners' partial rows; then B~ (first half)
+constexpr int RED_BYTES = 128 * 128 * 4;         // partial rows of A from every CTA; then B~ (first half)
 constexpr int FIXED_BYTES = A_BYTES + RED_BYTES;
 constexpr int STG_PITCH = 65;                    // floats per staged row of 64: conflict-free down a column
 constexpr int STG_FLOATS = 128 * STG_PITCH;
@@ -47,11 +49,11 @@ static_assert(smem_bytes(kSmallStackSlab) + 512 <= 232448, "shared memory above 
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_v4(uint32_t a, float x, float y, float z, float w) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
-}
-__device__ __forceinline__ void st_cluster_v2u(uint32_t a, uint32_t x, uint32_t y) {
-    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+// 16 bytes into a CTA of the cluster, counted on that CTA's mbarrier.
+__device__ __forceinline__ void st_async_v4(uint32_t a, uint32_t bar, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void st_cluster_f64(uint32_t a, double x) {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(x) : "memory");
@@ -109,7 +111,7 @@ struct alignas(16) SmallParamsS {
 
 __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParamsS p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t bar;
+    __shared__ uint64_t bar_gram, bar_square, bar_apply[2], bar_rows, bar_a;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double red_norm[THREADS / 32];
@@ -138,12 +140,11 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     const int q = warp & 3, cg = warp >> 2;        // TMEM lane quarter, column group
     const int row = 32 * q + lane;                 // this thread's row of X
     const int nchunk = w >> 6;
-    const int wq = w >> 2;                         // columns of a column group
     const float gs = k.gscale != nullptr ? __ldg(k.gscale) : 1.f;
     const bool mom = it.M != nullptr;
 
     if (tid == 0) {
-        mbar_init(&bar, 1);
+        for (uint64_t* x : {&bar_gram, &bar_square, &bar_apply[0], &bar_apply[1], &bar_rows, &bar_a}) mbar_init(x, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -156,7 +157,6 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    uint32_t phase = 0;
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
 
@@ -181,30 +181,59 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     };
     auto at = [&](const Group& g, long long stride, int ld) { return b * stride + static_cast<long long>(g.row) * ld + g.col; };
 
-    // ---------------------------------------------------------------- momentum and norm
+    // ---------------------------------------------------------------- momentum, norm, U -> TMEM
+    // Two chunks of loads in flight.
     double ss = 0.0;
-#pragma unroll 2
-    for (int j = 0; j < 2 * nchunk; ++j) {
-        const Group g = group(j >> 1, j & 1);
-        if (g.n == 0) continue;
-        float x[8];
-        load8(it.G, it.g_dtype, at(g, it.g_stride, it.g_ld), g.n, it.vec & 1, x);
+    struct Raw {
+        float g[2][8], m[2][8];
+    };
+    auto fetch = [&](int ch, Raw& x) {
+        if (ch >= nchunk) return;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= gs;
-        if (mom) {
-            float m[8];
-            const long long mo = at(g, it.m_stride, it.m_ld);
-            load8(it.M, MUON_F32, mo, g.n, it.vec & 2, m);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                m[e] = fmaf(k.beta, m[e], x[e]);
-                x[e] = k.nesterov ? fmaf(k.beta, m[e], x[e]) : m[e];
-            }
-            store8(it.M, MUON_F32, mo, g.n, it.vec & 2, m);
+        for (int e = 0; e < 2; ++e) {
+            const Group g = group(ch, e);
+            load8(it.G, it.g_dtype, at(g, it.g_stride, it.g_ld), g.n, it.vec & 1, x.g[e]);
+            if (mom) load8(it.M, MUON_F32, at(g, it.m_stride, it.m_ld), g.n, it.vec & 2, x.m[e]);
         }
+    };
+    auto take = [&](int ch, Raw& x) {
+        if (ch >= nchunk) return;
+        float* s = stg + (ch & 1) * STG_FLOATS;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
+        for (int e = 0; e < 2; ++e) {
+            const Group g = group(ch, e);
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                float u = x.g[e][h] * gs;
+                if (mom) {
+                    x.m[e][h] = fmaf(k.beta, x.m[e][h], u);
+                    u = k.nesterov ? fmaf(k.beta, x.m[e][h], u) : x.m[e][h];
+                }
+                if (h >= g.n) u = 0.f;     // 0 * a NaN factor is not zero
+                ss = fma(static_cast<double>(u), static_cast<double>(u), ss);
+                if (!tall) s[g.i * STG_PITCH + g.c + h] = u;
+                else s[(g.i + h) * STG_PITCH + g.c] = u;
+            }
+            if (mom) store8(it.M, MUON_F32, at(g, it.m_stride, it.m_ld), g.n, it.vec & 2, x.m[e]);
+        }
+        __syncthreads();
+        float z[16];
+#pragma unroll
+        for (int h = 0; h < 16; ++h) z[h] = s[row * STG_PITCH + cg * 16 + h];
+        tmem_st_x16(t_lane + ch * 64 + cg * 16, z);
+    };
+    {
+        Raw x0, x1;
+        fetch(0, x0);
+        fetch(1, x1);
+        for (int ch = 0; ch < nchunk; ch += 2) {
+            take(ch, x0);
+            fetch(ch + 2, x0);
+            take(ch + 1, x1);
+            fetch(ch + 3, x1);
+        }
     }
+    tmem_st_wait();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) red_norm[warp] = ss;
@@ -223,71 +252,41 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     const double norm = sqrt(sum);
     const bool fin = isfinite(norm);
     if (tid == 0 && rank == 0 && !fin) atomicOr(status, kDevErrNonfinite);
-    // Z_0 = U * 2^e * zf, so that neither factor leaves fp32's range
-    int ex = 0;
-    if (fin && norm > 0.0) ex = max(-126, min(126, -(ilogb(norm) + 1)));
-    const float up = __int_as_float((ex + 127) << 23);
-    const float zf = !fin ? NAN
-                          : norm > 0.0 ? static_cast<float>(static_cast<double>(k.unit) /
-                                                            ((norm + static_cast<double>(k.eps)) * static_cast<double>(up)))
-                                       : 0.f;
-
-    // ---------------------------------------------------------------- U -> state and first panels
-    float u[2][8];
-    auto load_u = [&](int ch) {
+    {
+        // Z_0 = U * 2^e * zf, so that neither factor leaves fp32's range
+        int ex = 0;
+        if (fin && norm > 0.0) ex = max(-126, min(126, -(ilogb(norm) + 1)));
+        const float up = __int_as_float((ex + 127) << 23);
+        const float zf = !fin ? NAN
+                              : norm > 0.0 ? static_cast<float>(static_cast<double>(k.unit) /
+                                                                ((norm + static_cast<double>(k.eps)) * static_cast<double>(up)))
+                                           : 0.f;
+        const float zs = k.it[0].zs;
+        for (int c = cg * 16; c < w; c += 64) {
+            float z[16];
+            tmem_ld_x16(t_lane + c, z);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const Group g = group(ch, e);
-#pragma unroll
-            for (int h = 0; h < 8; ++h) u[e][h] = 0.f;
-            if (g.n == 0) continue;
-            if (!mom || k.nesterov) {
-                load8(it.G, it.g_dtype, at(g, it.g_stride, it.g_ld), g.n, it.vec & 1, u[e]);
-#pragma unroll
-                for (int h = 0; h < 8; ++h) u[e][h] *= gs;
-            }
-            if (mom) {
-                float m[8];
-                load8(it.M, MUON_F32, at(g, it.m_stride, it.m_ld), g.n, it.vec & 2, m);
-#pragma unroll
-                for (int h = 0; h < 8; ++h) u[e][h] = k.nesterov ? fmaf(k.beta, m[h], u[e][h]) : m[h];
-            }
+            for (int h = 0; h < 16; ++h) z[h] = (z[h] * up) * zf;
+            tmem_st_x16(t_lane + c, z);
+            put_panel16(panels, row, c, z, zs);
         }
-    };
-    load_u(0);
-    for (int ch = 0; ch < nchunk; ++ch) {
-        float* s = stg + (ch & 1) * STG_FLOATS;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const Group g = group(ch, e);
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const float z = (u[e][h] * up) * zf;
-                if (!tall) s[g.i * STG_PITCH + g.c + h] = z;
-                else s[(g.i + h) * STG_PITCH + g.c] = z;
-            }
-        }
-        if (ch + 1 < nchunk) load_u(ch + 1);
-        __syncthreads();
-        float z[16];
-#pragma unroll
-        for (int h = 0; h < 16; ++h) z[h] = s[row * STG_PITCH + cg * 16 + h];
-        tmem_st_x16(t_lane + ch * 64 + cg * 16, z);
-        put_panel16(panels, row, ch * 64 + cg * 16, z, k.it[0].zs);
+        tmem_st_wait();
     }
-    tmem_st_wait();
     fence_async_proxy();
     tc_fence_before();
     __syncthreads();
-    cluster_arrive();      // staging is over: peers may write into this CTA's partial rows
+    if (C > 1) cluster_arrive();      // staging is over: peers may write into this CTA's buffers
 
     // ---------------------------------------------------------------- iterations
     const bool spill = w > ACC;
     const int rc = 128 / C;                        // rows of the Gram matrix that a CTA owns
+    const int own = row / rc, orow = row - own * rc, rmask = min(rc, 8) - 1;
     const uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
     const uint32_t pan0 = smem_u32(panels), a0 = smem_u32(Am), b0 = smem_u32(Bm);
+    const int pn = cg >> 1, ps = (cg & 1) * 4;     // panel and first 16-byte piece of columns 32 cg ...
     for (int t = 0; t < k.iters; ++t) {
         const SmallStackIter& f = k.it[t];
+        const uint32_t phase = t & 1;
         float sp[32];
         if (spill) {       // the state's last columns make room for the small products
             uint32_t r[32];
@@ -299,6 +298,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             __syncthreads();
         }
         if (tid == 0) {
+            if (C > 1) {
+                mbar_arrive_expect_tx(&bar_rows, RED_BYTES);
+                mbar_arrive_expect_tx(&bar_a, A_BYTES);
+            }
             tc_fence_after();
             fence_async_proxy();
             for (int j = 0; j < nchunk; ++j)
@@ -307,74 +310,92 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                     const uint64_t d = smem_desc_sw128(pan0 + j * PANEL + s * 32, 16, 1024);
                     tc_mma_bf16(tmem + ACC, d, d, idesc, j + s > 0);   // kind::f16, types from idesc
                 }
-            tc_commit(&bar);
+            tc_commit(&bar_gram);
         }
-        mbar_wait(&bar, phase, abort, status);
-        phase ^= 1u;
+        mbar_wait(&bar_gram, phase, abort, status);
         __syncwarp();
         tc_fence_after();
-        {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_lane + ACC + 32 * cg, r);
-            tmem_ld_wait();
-            tc_fence_before();
-            cluster_wait();        // the owner's partial rows are free
-            const int own = row / rc;
-            const uint32_t dst = mapa_shared(smem_u32(red), own) + static_cast<uint32_t>((rank * rc + row - own * rc) * 512);
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t_lane + ACC + 32 * cg, r);
+        tmem_ld_wait();
+        tc_fence_before();
+        if (C > 1) {
+            // Partial rows to their owners, as [rank][16-byte piece][row]: a warp's store of one piece fills
+            // whole sectors, and the row's place is turned by the piece so that the owner reads without
+            // bank conflicts.
+            cluster_wait();        // every CTA's buffers are free
+            const uint32_t dst = mapa_shared(smem_u32(red), own) + static_cast<uint32_t>(rank * rc * 512);
+            const uint32_t bar = mapa_shared(smem_u32(&bar_rows), own);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-                st_cluster_v4(dst + (((8 * cg + s) ^ (row & 7)) << 4), __uint_as_float(r[4 * s]), __uint_as_float(r[4 * s + 1]),
-                              __uint_as_float(r[4 * s + 2]), __uint_as_float(r[4 * s + 3]));
-        }
-        cluster_arrive();
-        cluster_wait();
-        // rows rank * rc ... of A: the sum over the cluster in rank order, to every CTA
-        for (int g = tid; g < rc * 32; g += THREADS) {
-            const int rr = g >> 5, seg = g & 31, ar = rank * rc + rr;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i = 0; i < C; ++i) {
-                const float4 v = *reinterpret_cast<const float4*>(red + (i * rc + rr) * 512 + ((seg ^ (ar & 7)) << 4));
-                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            for (int s = 0; s < 8; ++s) {
+                const int seg = 8 * cg + s;
+                st_async_v4(dst + ((seg * rc + (orow ^ (seg & rmask))) << 4), bar, r[4 * s], r[4 * s + 1], r[4 * s + 2], r[4 * s + 3]);
             }
-            float v[4] = {s.x * f.ga, s.y * f.ga, s.z * f.ga, s.w * f.ga};
+            mbar_wait(&bar_rows, phase, abort, status);
+            __syncwarp();
+            // rows rank * rc ... of A: the sum over the cluster in rank order, 8 columns a thread, to every CTA
+            for (int g = tid; g < rc * 16; g += THREADS) {
+                const int rr = g >> 4, pc = g & 15, ar = rank * rc + rr;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (4 * seg + e == ar) v[e] -= f.diag;
-            const uint32_t x = half2_bits(v[0], v[1]), y = half2_bits(v[2], v[3]);
-            const uint32_t off = (seg >> 4) * PANEL + ar * 128 + ((((seg & 15) >> 1) ^ (ar & 7)) << 4) + (seg & 1) * 8;
-            for (int i = 0; i < C; ++i) st_cluster_v2u(mapa_shared(a0 + off, (rank + i) % C), x, y);
+                for (int h = 0; h < 2; ++h) {
+                    const int seg = 2 * pc + h;
+                    const uint8_t* src = red + ((seg * rc + (rr ^ (seg & rmask))) << 4);
+                    for (int i = 0; i < C; ++i) {
+                        const float4 x = *reinterpret_cast<const float4*>(src + i * rc * 512);
+                        v[4 * h] += x.x; v[4 * h + 1] += x.y; v[4 * h + 2] += x.z; v[4 * h + 3] += x.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] *= f.ga;
+                    if (8 * pc + e == ar) v[e] -= f.diag;
+                }
+                const uint4 x = pack8(MUON_F16, v);
+                const uint32_t off = (pc >> 3) * PANEL + ar * 128 + (((pc & 7) ^ (ar & 7)) << 4);
+                for (int i = 0; i < C; ++i) {
+                    const int to = (rank + i) & (C - 1);
+                    st_async_v4(mapa_shared(a0 + off, to), mapa_shared(smem_u32(&bar_a), to), x.x, x.y, x.z, x.w);
+                }
+            }
+            mbar_wait(&bar_a, phase, abort, status);
+            __syncwarp();
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] = __uint_as_float(r[8 * s + e]) * f.ga;
+                    if (32 * cg + 8 * s + e == row) v[e] -= f.diag;
+                }
+                *reinterpret_cast<uint4*>(Am + pn * PANEL + row * 128 + (((ps + s) ^ (row & 7)) << 4)) = pack8(MUON_F16, v);
+            }
         }
         fence_async_proxy();
-        cluster_arrive();
-        cluster_wait();
+        __syncthreads();
         if (tid == 0) {
             tc_fence_after();
-            fence_async_proxy();
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const uint64_t d = smem_desc_sw128(a0 + (s >> 2) * PANEL + (s & 3) * 32, 16, 1024);
                 tc_mma_bf16(tmem + ACC, d, d, idesc, s > 0);
             }
-            tc_commit(&bar);
+            tc_commit(&bar_square);
         }
-        mbar_wait(&bar, phase, abort, status);
-        phase ^= 1u;
+        mbar_wait(&bar_square, phase, abort, status);
         __syncwarp();
         tc_fence_after();
-        {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_lane + ACC + 32 * cg, r);
-            tmem_ld_wait();
-            const int pn = cg >> 1, s0 = (cg & 1) * 4;     // panel and first 16-byte piece of these columns
+        tmem_ld_32x32b_x32(t_lane + ACC + 32 * cg, r);
+        tmem_ld_wait();
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t off = pn * PANEL + row * 128 + (((s0 + s) ^ (row & 7)) << 4);
-                float av[8];
-                unpack8(*reinterpret_cast<const uint4*>(Am + off), MUON_F16, av);
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t off = pn * PANEL + row * 128 + (((ps + s) ^ (row & 7)) << 4);
+            float av[8];
+            unpack8(*reinterpret_cast<const uint4*>(Am + off), MUON_F16, av);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) av[e] = fmaf(f.pb, av[e], f.pc * __uint_as_float(r[8 * s + e]));
-                *reinterpret_cast<uint4*>(Bm + off) = pack8(MUON_F16, av);
-            }
+            for (int e = 0; e < 8; ++e) av[e] = fmaf(f.pb, av[e], f.pc * __uint_as_float(r[8 * s + e]));
+            *reinterpret_cast<uint4*>(Bm + off) = pack8(MUON_F16, av);
         }
         if (spill) {
             tmem_st_x16(t_lane + ACC + 32 * cg, sp);
@@ -395,21 +416,26 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                     const uint64_t xd = smem_desc_sw128(pan0 + (n0 >> 6) * PANEL + s * 2048, PANEL, 1024);
                     tc_mma_bf16(tmem + n0, ad, xd, id, 1);
                 }
+                tc_commit(&bar_apply[n0 >> 8]);
             }
-            tc_commit(&bar);
         }
-        mbar_wait(&bar, phase, abort, status);
-        phase ^= 1u;
-        __syncwarp();
-        tc_fence_after();
-        if (t + 1 < k.iters) {
-            cluster_arrive();      // B~ and A of this CTA are done with
-            const float zs = k.it[t + 1].zs;
-            for (int c = cg * wq; c < (cg + 1) * wq; c += 16) {
-                float z[16];
-                tmem_ld_x16(t_lane + c, z);
-                put_panel16(panels, row, c, z, zs);
-            }
+        // The first 256 columns are converted while the others are multiplied.
+        const bool last = t + 1 == k.iters;
+        const float zs = k.it[last ? t : t + 1].zs;
+        for (int n0 = 0; n0 < w; n0 += 256) {
+            mbar_wait(&bar_apply[n0 >> 8], phase, abort, status);
+            __syncwarp();
+            tc_fence_after();
+            if (!last && n0 + 256 >= w && C > 1) cluster_arrive();   // this CTA's A, B~ and partial rows are done with
+            const int nq = min(256, w - n0) >> 2;
+            if (!last)
+                for (int c = n0 + cg * nq; c < n0 + (cg + 1) * nq; c += 16) {
+                    float z[16];
+                    tmem_ld_x16(t_lane + c, z);
+                    put_panel16(panels, row, c, z, zs);
+                }
+        }
+        if (!last) {
             fence_async_proxy();
             tc_fence_before();
             __syncthreads();
@@ -417,23 +443,24 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     }
 
     // ---------------------------------------------------------------- result
-    // Peers have read and written this CTA's shared memory for the last time before the last barrier.
+    // Peers' last stores into this CTA are the last rows of A, which it has waited for.
     const float out = k.out;
-    __syncthreads();
-    for (int ch = 0; ch < nchunk; ++ch) {
+    const bool update = it.decay != 0.f;
+    auto fetch_w = [&](int ch, float (&x)[2][8]) {
+        if (!update || ch >= nchunk) return;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const Group g = group(ch, e);
+            load8(it.W, it.w_dtype, at(g, it.w_stride, it.w_ld), g.n, it.vec & 4, x[e]);
+        }
+    };
+    auto give = [&](int ch, float (&x)[2][8]) {
+        if (ch >= nchunk) return;
         float* s = stg + (ch & 1) * STG_FLOATS;
         float z[16];
         tmem_ld_x16(t_lane + ch * 64 + cg * 16, z);
 #pragma unroll
         for (int h = 0; h < 16; ++h) s[row * STG_PITCH + cg * 16 + h] = z[h] * out;
-        float x[2][8];
-        if (it.decay != 0.f) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const Group g = group(ch, e);
-                load8(it.W, it.w_dtype, at(g, it.w_stride, it.w_ld), g.n, it.vec & 4, x[e]);
-            }
-        }
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -443,9 +470,21 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
                 const float v = !tall ? s[g.i * STG_PITCH + g.c + h] : s[(g.i + h) * STG_PITCH + g.c];
-                o[h] = it.decay != 0.f ? fmaf(it.step, v, it.decay * x[e][h]) : it.step * v;
+                o[h] = update ? fmaf(it.step, v, it.decay * x[e][h]) : it.step * v;
             }
             store8(it.W, it.w_dtype, at(g, it.w_stride, it.w_ld), g.n, it.vec & 4, o);
+        }
+    };
+    {
+        float x0[2][8], x1[2][8];
+        fetch_w(0, x0);
+        fetch_w(1, x1);
+        __syncthreads();       // every warp is past the last reads of A and B~
+        for (int ch = 0; ch < nchunk; ch += 2) {
+            give(ch, x0);
+            fetch_w(ch + 2, x0);
+            give(ch + 1, x1);
+            fetch_w(ch + 3, x1);
         }
     }
     tc_fence_before();

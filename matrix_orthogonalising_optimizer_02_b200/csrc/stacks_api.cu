@@ -186,11 +186,12 @@ bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, co
     k.unit = static_cast<float>(unit);
     k.out = static_cast<float>(pa / unit);
     k.eps = sch.eps;
-    // As few CTAs as hold the block; more while all blocks' CTAs still run at once.
+    // As few CTAs as hold the block; more while all blocks' CTAs still run at once.  Up to 256 columns
+    // one CTA is faster than several that have to exchange their sums.
     const int pieces = (s + 63) / 64;
     int C = 1;
     while (C * kSmallStackSlab < s) C *= 2;
-    while (2 * C <= 8 && 2 * C <= pieces && 2ll * C * blocks <= kSmallStackCtas) C *= 2;
+    while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && 2ll * C * blocks <= kSmallStackCtas) C *= 2;
     k.cluster = C;
     k.slab = (pieces + C - 1) / C * 64;
     return true;
