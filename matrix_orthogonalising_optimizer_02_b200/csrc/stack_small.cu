@@ -6,7 +6,9 @@
 // grouped GEMMs its three products would each read and write X from L2 with a launch in between (96
 // heads of 128 x 4096: 1.31 ms of products and 0.24 ms of passes, against 0.11 ms for its HBM bytes).
 //
-// The block, turned so that X is r x s, is cut along s into slabs of w <= 512 columns, one per CTA:
+// The block, turned so that X is r x s, is cut along s into chunks of 64 columns that the cluster's CTAs take
+// in turn (so that together they walk along whole rows of the caller's arrays: pieces of 128 bytes a row would
+// halve what HBM gives); a CTA's slab has w <= 512 columns:
 //  - state Z = X * u / (a_0 ... a_{t-1}) in TMEM, fp32, 128 lanes x w columns.  In these units an
 //    iteration X' = aX + BX is Z' = Z + B~ X^, the accumulation that the tensor core does anyway: the
 //    state never leaves TMEM, and the term aX keeps 24 bits at no cost;
@@ -20,9 +22,13 @@
 // that a CTA's buffers are free again.  (With cluster barriers after each exchange and rows of 16 bytes
 // per lane an iteration at w = 512 took 12.2 us, 5.6 of them in the exchanges.)
 //
-// In and out: one coalesced pass over G and M (M written, norm in fp64) puts U into TMEM as it is; once
-// the norm is known it is scaled there.  Results go back through the same staging.  A step reads and
-// writes each byte of HBM once.
+// In and out: one pass over G and M (M written, norm in fp64) puts U into TMEM as it is; once the norm is
+// known it is scaled there.  A step reads and writes each byte of HBM once.  Chunks come and go as TMA
+// boxes, several in flight, 128-byte swizzled so that a thread finds its own row of X without bank
+// conflicts, zero-filled and clipped at the block's edges.  (Loads through registers took twice as long,
+// 26 us for a slab of 128 x 512: a quarter of the stalls were instruction fetches of the code for every
+// type and edge, another the loads' latency.  Row by row, bulk copies took 42 us: about 20 ns each.)
+// Arrays whose rows TMA cannot address go element by element through shared memory.
 #include <atomic>
 #include <cmath>
 
@@ -40,7 +46,8 @@ constexpr int RED_BYTES = 128 * 128 * 4;         // partial rows of A from every
 constexpr int FIXED_BYTES = A_BYTES + RED_BYTES;
 constexpr int STG_PITCH = 65;                    // floats per staged row of 64: conflict-free down a column
 constexpr int STG_FLOATS = 128 * STG_PITCH;
-static_assert(2 * STG_FLOATS * 4 <= FIXED_BYTES, "two staging buffers overlay A and the partial rows");
+static_assert(2 * STG_FLOATS * 4 <= FIXED_BYTES, "two staging buffers fit the smallest slab's shared memory");
+static_assert(4 * PANEL <= FIXED_BYTES + PANEL, "one chunk of fp32 G and M fits the smallest slab's shared memory");
 constexpr int TMEM_COLS = 512, ACC = 384;        // Gram and A^2 accumulate in columns ACC .. ACC + 127
 
 __host__ __device__ constexpr int smem_bytes(int w) { return (w / 64) * PANEL + FIXED_BYTES + 1024; }
@@ -98,12 +105,296 @@ __device__ __forceinline__ void put_panel16(uint8_t* panels, int row, int c, con
     }
 }
 
-struct Group {      // 8 consecutive elements of the caller's arrays: row, first column, valid count
-    int row, col, n;
-    int i, c;       // X's row and chunk column of the first one
+// ---------------------------------------------------------------- a slab in and out
+struct Slab {
+    int rows, cols, rank, cluster, nchunk;
+    bool tall;
+    uint8_t* buf;          // all of the shared memory that the iterations use, 1024-byte aligned
+    int bytes;
+    uint32_t t_lane;       // TMEM address of this warp's lanes
+    uint64_t* bars;        // kRing mbarriers
+    volatile int* abort;
+    unsigned* status;
+    __device__ __forceinline__ int first(int ch) const { return (ch * cluster + rank) * 64; }   // first column of a chunk
+};
+constexpr int kRing = 4;
+constexpr int BOX = 128 * 128;   // bytes of a box: 128 rows (two times 64 for a tall block) of 128 bytes
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m), "r"(src),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// One array's part of a chunk: two boxes of 64 x 128 (64-column halves of a tall block's rows) or one of 128 x 64
+// for 16-bit elements, twice as many for fp32.  A box's row has 128 bytes: 64 or 32 elements.
+struct Boxes {
+    const CUtensorMap* map;
+    int dtype, es, block;
+    __device__ __forceinline__ int bytes() const { return BOX * es / 2; }
+    // Calls f(byte offset in the buffer, x, y) for every box of the chunk at column c.
+    template <class F>
+    __device__ __forceinline__ void each(const Slab& s, int c, F f) const {
+        const int per = 128 / es;
+        if (!s.tall) {
+            for (int h = 0; h < es / 2; ++h) f(h * BOX, c + h * per, 0);
+        } else {
+            for (int h = 0; h < es; ++h) f(h * (BOX / 2), h * per, c);
+        }
+    }
+    __device__ __forceinline__ void load(const Slab& s, int c, uint32_t buf, uint32_t bar) const {
+        each(s, c, [&](int o, int x, int y) { tma_load_3d(buf + o, map, bar, x, y, block); });
+    }
+    __device__ __forceinline__ void prefetch(const Slab& s, int c) const {
+        each(s, c, [&](int, int x, int y) { if (x < s.cols && y < s.rows) tma_prefetch_3d(map, x, y, block); });
+    }
+    __device__ __forceinline__ void store(const Slab& s, int c, uint32_t buf) const {
+        each(s, c, [&](int o, int x, int y) { if (x < s.cols && y < s.rows) tma_store_3d(map, buf + o, x, y, block); });
+    }
+    // This thread's 16 elements (X's row `row`, columns 16 cg ...) in a buffer: piece h (0, 1) of 8 for wide
+    // blocks, element h (0..15) for tall ones.
+    __device__ __forceinline__ uint8_t* piece(uint8_t* buf, int row, int cg, int h, int half) const {
+        const int e = cg * 16 + 8 * h;                                   // column
+        if (es == 2) return buf + row * 128 + (((e >> 3) ^ (row & 7)) << 4);
+        return buf + (e >> 5) * BOX + row * 128 + (((((e & 31) >> 2) + half) ^ (row & 7)) << 4);
+    }
+    __device__ __forceinline__ uint8_t* elem(uint8_t* buf, int row, int c) const {
+        if (es == 2) return buf + (row >> 6) * (BOX / 2) + c * 128 + ((((row & 63) >> 3) ^ (c & 7)) << 4) + (row & 7) * 2;
+        return buf + (row >> 5) * (BOX / 2) + c * 128 + ((((row & 31) >> 2) ^ (c & 7)) << 4) + (row & 3) * 4;
+    }
+    __device__ __forceinline__ void get(const Slab& s, uint8_t* buf, int row, int cg, float (&v)[16]) const {
+        if (!s.tall) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[8];
+                if (es == 2) {
+                    unpack8(*reinterpret_cast<const uint4*>(piece(buf, row, cg, h, 0)), dtype, x);
+                } else {
+                    const float4 a = *reinterpret_cast<const float4*>(piece(buf, row, cg, h, 0));
+                    const float4 b = *reinterpret_cast<const float4*>(piece(buf, row, cg, h, 1));
+                    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * h + e] = x[e];
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 16; ++h) v[h] = load_elem(elem(buf, row, cg * 16 + h), dtype, 0);
+        }
+    }
+    __device__ __forceinline__ void put(const Slab& s, uint8_t* buf, int row, int cg, const float (&v)[16]) const {
+        if (!s.tall) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = v[8 * h + e];
+                if (es == 2) {
+                    *reinterpret_cast<uint4*>(piece(buf, row, cg, h, 0)) = pack8(dtype, x);
+                } else {
+                    *reinterpret_cast<float4*>(piece(buf, row, cg, h, 0)) = make_float4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<float4*>(piece(buf, row, cg, h, 1)) = make_float4(x[4], x[5], x[6], x[7]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 16; ++h) store_elem(elem(buf, row, cg * 16 + h), dtype, 0, v[h]);
+        }
+    }
 };
 
-struct alignas(16) SmallParamsS {
+// Chunk buffers that TMA fills in turn; thread 0 issues.  `turns`: the phases of the mbarriers, as bits.
+template <int N>
+struct Ring {
+    Boxes a[N];
+    int n, size, bufs;
+    __device__ __forceinline__ void shape(const Slab& s) {
+        size = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) size += a[i].bytes();
+        bufs = min(min(kRing, s.bytes / size), s.nchunk);
+    }
+    __device__ __forceinline__ uint8_t* buf(const Slab& s, int ch) const { return s.buf + (ch % bufs) * size; }
+    __device__ __forceinline__ void fill(const Slab& s, int ch) const {
+        const uint32_t bar = smem_u32(s.bars + ch % bufs);
+        mbar_arrive_expect_tx(s.bars + ch % bufs, size);
+        uint32_t dst = smem_u32(buf(s, ch));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i >= n) break;
+            a[i].load(s, s.first(ch), dst, bar);
+            dst += a[i].bytes();
+        }
+    }
+    __device__ __forceinline__ void wait(const Slab& s, int ch, uint32_t& turns) const {
+        const int b = ch % bufs;
+        mbar_wait(s.bars + b, (turns >> b) & 1u, s.abort, s.status);
+        turns ^= 1u << b;
+        __syncwarp();
+    }
+    // After the barrier that ends chunk ch, with its store (if any) committed: fills a buffer whose chunk is done.
+    // With several buffers that is the one before, whose store has had a chunk's time.
+    __device__ __forceinline__ void refill(const Slab& s, int ch) const {
+        const int back = bufs > 1 ? ch - 1 : ch;
+        if (back < 0 || back + bufs >= s.nchunk) return;
+        if (bufs > 1) bulk_wait_read<1>();
+        else bulk_wait_read<0>();
+        fill(s, back + bufs);
+    }
+};
+
+struct Momentum {
+    float gs, beta;
+    bool on, nesterov;
+    // The input of the iterations from gradient elements (in u); m is updated.  Zeros stay zeros, unless
+    // the factor is not finite, and then the block is not.
+    __device__ __forceinline__ void operator()(float (&u)[16], float (&m)[16]) const {
+#pragma unroll
+        for (int h = 0; h < 16; ++h) u[h] *= gs;
+        if (on) {
+#pragma unroll
+            for (int h = 0; h < 16; ++h) m[h] = fmaf(beta, m[h], u[h]);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) u[h] = nesterov ? fmaf(beta, m[h], u[h]) : m[h];
+        }
+    }
+};
+__device__ __forceinline__ float sum_squares(const float (&u)[16]) {
+    float s = 0.f;
+#pragma unroll
+    for (int h = 0; h < 16; ++h) s = fmaf(u[h], u[h], s);
+    return s;
+}
+
+// Element j (0..15) of this thread in chunk ch, a warp along a row of the caller's.
+struct Spot {
+    int i, c;              // X's row, chunk column
+    long long at;          // place in an array with row pitch ld
+    bool ok;
+};
+__device__ __forceinline__ Spot spot(const Slab& s, int ch, int j, int ld) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Spot p;
+    int row, col;
+    if (!s.tall) {
+        p.i = row = warp + 16 * (j >> 1);
+        p.c = lane + 32 * (j & 1);
+        col = s.first(ch) + p.c;
+    } else {
+        p.c = warp + 16 * (j >> 2);
+        p.i = col = lane + 32 * (j & 3);
+        row = s.first(ch) + p.c;
+    }
+    p.at = static_cast<long long>(row) * ld + col;
+    p.ok = row < s.rows && col < s.cols;
+    return p;
+}
+template <class F>
+__device__ __forceinline__ void by_type(int dtype, F f) {
+    if (dtype == MUON_F32) f(float());
+    else if (dtype == MUON_F16) f(__half());
+    else f(__nv_bfloat16());
+}
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void narrow(float& d, float x) { d = x; }
+__device__ __forceinline__ void narrow(__half& d, float x) { d = __float2half_rn(x); }
+__device__ __forceinline__ void narrow(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+
+// The element-wise walks, out of line: their registers and code are not the iterations'.
+__device__ __noinline__ double slab_in_any(const Slab s, const SmallStackItem& item, long long b, const Momentum mo) {
+    const SmallStackItem it = item;    // by value: the stores below cannot alias it
+    const int warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
+    const uint8_t* g0 = static_cast<const uint8_t*>(it.G) + b * it.g_stride * (it.g_dtype == MUON_F32 ? 4 : 2);
+    float* m0 = it.M + b * it.m_stride;
+    double ss = 0.0;
+#pragma unroll 1
+    for (int ch = 0; ch < s.nchunk; ++ch) {
+        float* buf = reinterpret_cast<float*>(s.buf) + (ch & 1) * STG_FLOATS;
+        float u[16], m[16];
+        by_type(it.g_dtype, [&](auto t) {
+            using E = decltype(t);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const Spot p = spot(s, ch, j, it.g_ld);
+                u[j] = p.ok ? widen(reinterpret_cast<const E*>(g0)[p.at]) : 0.f;
+            }
+        });
+        if (mo.on) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const Spot p = spot(s, ch, j, it.m_ld);
+                m[j] = p.ok ? m0[p.at] : 0.f;
+            }
+        }
+        mo(u, m);
+        ss += static_cast<double>(sum_squares(u));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const Spot p = spot(s, ch, j, it.m_ld);
+            buf[p.i * STG_PITCH + p.c] = u[j];
+            if (mo.on && p.ok) m0[p.at] = m[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 16; ++h) u[h] = buf[row * STG_PITCH + cg * 16 + h];
+        tmem_st_x16(s.t_lane + ch * 64 + cg * 16, u);
+    }
+    return ss;
+}
+__device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& item, long long b, float out) {
+    const SmallStackItem it = item;
+    const int warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
+    uint8_t* w0 = static_cast<uint8_t*>(it.W) + b * it.w_stride * (it.w_dtype == MUON_F32 ? 4 : 2);
+    const float decay = it.decay, step = it.step * out;
+    const bool update = decay != 0.f;
+#pragma unroll 1
+    for (int ch = 0; ch < s.nchunk; ++ch) {
+        float* buf = reinterpret_cast<float*>(s.buf) + (ch & 1) * STG_FLOATS;
+        float z[16];
+        tmem_ld_x16(s.t_lane + ch * 64 + cg * 16, z);
+#pragma unroll
+        for (int h = 0; h < 16; ++h) buf[row * STG_PITCH + cg * 16 + h] = z[h];
+        __syncthreads();
+        by_type(it.w_dtype, [&](auto t) {
+            using E = decltype(t);
+            E* wt = reinterpret_cast<E*>(w0);
+            float x[16];
+            if (update) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const Spot p = spot(s, ch, j, it.w_ld);
+                    x[j] = p.ok ? widen(wt[p.at]) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const Spot p = spot(s, ch, j, it.w_ld);
+                const float v = buf[p.i * STG_PITCH + p.c];
+                if (p.ok) narrow(wt[p.at], update ? fmaf(step, v, decay * x[j]) : step * v);
+            }
+        });
+    }
+}
+
+struct SmallParamsS {
     SmallStackItem item[kSmallStackItems];
     SmallStackClass k;
     int n;
@@ -111,7 +402,7 @@ struct alignas(16) SmallParamsS {
 
 __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParamsS p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t bar_gram, bar_square, bar_apply[2], bar_rows, bar_a;
+    __shared__ uint64_t bar_gram, bar_square, bar_apply[2], bar_rows, bar_a, bar_ring[kRing];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double red_norm[THREADS / 32];
@@ -123,7 +414,6 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     uint8_t* Am = panels + (w >> 6) * PANEL;
     uint8_t* red = Am + A_BYTES;
     uint8_t* Bm = red;
-    float* stg = reinterpret_cast<float*>(Am);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -136,7 +426,6 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     const SmallStackItem& it = p.item[lo];
     const long long b = blk - it.block0;
     const bool tall = k.rows > k.cols;
-    const int c0 = rank * w;                       // first column of this slab
     const int q = warp & 3, cg = warp >> 2;        // TMEM lane quarter, column group
     const int row = 32 * q + lane;                 // this thread's row of X
     const int nchunk = w >> 6;
@@ -145,6 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
 
     if (tid == 0) {
         for (uint64_t* x : {&bar_gram, &bar_square, &bar_apply[0], &bar_apply[1], &bar_rows, &bar_a}) mbar_init(x, 1);
+        for (uint64_t& x : bar_ring) mbar_init(&x, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -160,95 +450,83 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
 
-    // Group e (0 or 1) of this thread in 64-column chunk ch.
-    auto group = [&](int ch, int e) {
-        Group g;
-        const int i = e * THREADS + tid;
-        if (!tall) {
-            g.i = i >> 3;
-            g.c = (i & 7) * 8;
-            g.row = g.i;
-            g.col = c0 + ch * 64 + g.c;
-            g.n = g.row < k.rows ? max(0, min(8, k.cols - g.col)) : 0;
-        } else {
-            g.c = i >> 4;
-            g.i = (i & 15) * 8;
-            g.row = c0 + ch * 64 + g.c;
-            g.col = g.i;
-            g.n = g.row < k.rows ? max(0, min(8, k.cols - g.col)) : 0;
-        }
-        return g;
-    };
-    auto at = [&](const Group& g, long long stride, int ld) { return b * stride + static_cast<long long>(g.row) * ld + g.col; };
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, panels, (w >> 6) * PANEL + FIXED_BYTES, t_lane, bar_ring, abort, status};
+    const Momentum mo = {gs, k.beta, mom, k.nesterov != 0};
+    const bool tma_in = (it.vec & 1) && (!mom || (it.vec & 2)), tma_out = (it.vec & 4) != 0, update = it.decay != 0.f;
+    const Boxes boxes_w = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+    uint32_t turns = 0;
 
     // ---------------------------------------------------------------- momentum, norm, U -> TMEM
-    // Two chunks of loads in flight.
     double ss = 0.0;
-    struct Raw {
-        float g[2][8], m[2][8];
-    };
-    auto fetch = [&](int ch, Raw& x) {
-        if (ch >= nchunk) return;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const Group g = group(ch, e);
-            load8(it.G, it.g_dtype, at(g, it.g_stride, it.g_ld), g.n, it.vec & 1, x.g[e]);
-            if (mom) load8(it.M, MUON_F32, at(g, it.m_stride, it.m_ld), g.n, it.vec & 2, x.m[e]);
+    if (tma_in) {
+        Ring<2> ring;
+        ring.a[0] = {&it.map_g, it.g_dtype, it.g_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+        ring.a[1] = {&it.map_m, MUON_F32, 4, static_cast<int>(b)};
+        ring.n = mom ? 2 : 1;
+        ring.shape(slab);
+        if (tid == 0) {
+            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch);
+            if (tma_out && update)      // on its way to L2 while the block iterates
+                for (int ch = 0; ch < nchunk; ++ch) boxes_w.prefetch(slab, slab.first(ch));
         }
-    };
-    auto take = [&](int ch, Raw& x) {
-        if (ch >= nchunk) return;
-        float* s = stg + (ch & 1) * STG_FLOATS;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const Group g = group(ch, e);
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                float u = x.g[e][h] * gs;
-                if (mom) {
-                    x.m[e][h] = fmaf(k.beta, x.m[e][h], u);
-                    u = k.nesterov ? fmaf(k.beta, x.m[e][h], u) : x.m[e][h];
-                }
-                if (h >= g.n) u = 0.f;     // 0 * a NaN factor is not zero
-                ss = fma(static_cast<double>(u), static_cast<double>(u), ss);
-                if (!tall) s[g.i * STG_PITCH + g.c + h] = u;
-                else s[(g.i + h) * STG_PITCH + g.c] = u;
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+            ring.wait(slab, ch, turns);
+            uint8_t* buf = ring.buf(slab, ch);
+            uint8_t* buf_m = buf + ring.a[0].bytes();
+            float u[16], m[16];
+            ring.a[0].get(slab, buf, row, cg, u);
+            if (mom) ring.a[1].get(slab, buf_m, row, cg, m);
+            mo(u, m);
+            ss += static_cast<double>(sum_squares(u));   // 16 squares in fp32 at most
+            tmem_st_x16(t_lane + ch * 64 + cg * 16, u);
+            if (mom) {
+                ring.a[1].put(slab, buf_m, row, cg, m);
+                fence_async_proxy();
             }
-            if (mom) store8(it.M, MUON_F32, at(g, it.m_stride, it.m_ld), g.n, it.vec & 2, x.m[e]);
+            __syncthreads();
+            if (tid == 0) {
+                if (mom) {
+                    ring.a[1].store(slab, slab.first(ch), smem_u32(buf_m));
+                    bulk_commit();
+                }
+                ring.refill(slab, ch);
+            }
         }
-        __syncthreads();
-        float z[16];
-#pragma unroll
-        for (int h = 0; h < 16; ++h) z[h] = s[row * STG_PITCH + cg * 16 + h];
-        tmem_st_x16(t_lane + ch * 64 + cg * 16, z);
-    };
-    {
-        Raw x0, x1;
-        fetch(0, x0);
-        fetch(1, x1);
-        for (int ch = 0; ch < nchunk; ch += 2) {
-            take(ch, x0);
-            fetch(ch + 2, x0);
-            take(ch + 1, x1);
-            fetch(ch + 3, x1);
-        }
+        if (tid == 0) bulk_wait_read<0>();
+        __syncthreads();       // the buffers are free
+    } else {
+        ss = slab_in_any(slab, it, b, mo);
     }
     tmem_st_wait();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) red_norm[warp] = ss;
-    __syncthreads();
-    cluster_arrive();      // every CTA of the cluster runs
-    cluster_wait();
-    if (tid < C) {
-        double s = 0.0;
-        for (int i = 0; i < THREADS / 32; ++i) s += red_norm[i];
-        st_cluster_f64(mapa_shared(smem_u32(&parts[rank]), tid), s);
-    }
-    cluster_arrive();
-    cluster_wait();
     double sum = 0.0;
-    for (int i = 0; i < C; ++i) sum += parts[i];
+    for (int again = 0; again < 2; ++again) {
+        if (again) {       // squares outside fp32's range: once more in fp64, from TMEM
+            ss = 0.0;
+            for (int c = cg * 16; c < w; c += 64) {
+                float z[16];
+                tmem_ld_x16(t_lane + c, z);
+#pragma unroll
+                for (int h = 0; h < 16; ++h) ss = fma(static_cast<double>(z[h]), static_cast<double>(z[h]), ss);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) red_norm[warp] = ss;
+        __syncthreads();
+        cluster_arrive();      // every CTA of the cluster runs, and is past its last read of `parts`
+        cluster_wait();
+        if (tid < C) {
+            double s = 0.0;
+            for (int i = 0; i < THREADS / 32; ++i) s += red_norm[i];
+            st_cluster_f64(mapa_shared(smem_u32(&parts[rank]), tid), s);
+        }
+        cluster_arrive();
+        cluster_wait();
+        sum = 0.0;
+        for (int i = 0; i < C; ++i) sum += parts[i];
+        if (sum > 1e-25 && sum < 1e36) break;      // the same in every CTA of the cluster
+    }
     const double norm = sqrt(sum);
     const bool fin = isfinite(norm);
     if (tid == 0 && rank == 0 && !fin) atomicOr(status, kDevErrNonfinite);
@@ -444,48 +722,46 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
 
     // ---------------------------------------------------------------- result
     // Peers' last stores into this CTA are the last rows of A, which it has waited for.
-    const float out = k.out;
-    const bool update = it.decay != 0.f;
-    auto fetch_w = [&](int ch, float (&x)[2][8]) {
-        if (!update || ch >= nchunk) return;
+    __syncthreads();           // every warp is past the last reads of A and B~
+    if (tma_out) {
+        const float step = it.step * k.out, decay = it.decay;
+        Ring<1> ring;
+        ring.a[0] = boxes_w;
+        ring.n = 1;
+        ring.shape(slab);
+        if (update && tid == 0)
+            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch);
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+            uint8_t* buf = ring.buf(slab, ch);
+            float z[16];
+            tmem_ld_x16(t_lane + ch * 64 + cg * 16, z);
+            if (update) {
+                float x[16];
+                ring.wait(slab, ch, turns);
+                boxes_w.get(slab, buf, row, cg, x);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const Group g = group(ch, e);
-            load8(it.W, it.w_dtype, at(g, it.w_stride, it.w_ld), g.n, it.vec & 4, x[e]);
-        }
-    };
-    auto give = [&](int ch, float (&x)[2][8]) {
-        if (ch >= nchunk) return;
-        float* s = stg + (ch & 1) * STG_FLOATS;
-        float z[16];
-        tmem_ld_x16(t_lane + ch * 64 + cg * 16, z);
+                for (int h = 0; h < 16; ++h) z[h] = fmaf(step, z[h], decay * x[h]);
+            } else {
+                if (ch >= ring.bufs) {     // the buffer's last store has been read out
+                    if (tid == 0) bulk_wait_read<0>();
+                    __syncthreads();
+                }
 #pragma unroll
-        for (int h = 0; h < 16; ++h) s[row * STG_PITCH + cg * 16 + h] = z[h] * out;
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const Group g = group(ch, e);
-            if (g.n == 0) continue;
-            float o[8];
-#pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const float v = !tall ? s[g.i * STG_PITCH + g.c + h] : s[(g.i + h) * STG_PITCH + g.c];
-                o[h] = update ? fmaf(it.step, v, it.decay * x[e][h]) : it.step * v;
+                for (int h = 0; h < 16; ++h) z[h] *= step;
             }
-            store8(it.W, it.w_dtype, at(g, it.w_stride, it.w_ld), g.n, it.vec & 4, o);
+            boxes_w.put(slab, buf, row, cg, z);
+            fence_async_proxy();
+            __syncthreads();
+            if (tid == 0) {
+                boxes_w.store(slab, slab.first(ch), smem_u32(buf));
+                bulk_commit();
+                if (update) ring.refill(slab, ch);
+            }
         }
-    };
-    {
-        float x0[2][8], x1[2][8];
-        fetch_w(0, x0);
-        fetch_w(1, x1);
-        __syncthreads();       // every warp is past the last reads of A and B~
-        for (int ch = 0; ch < nchunk; ch += 2) {
-            give(ch, x0);
-            fetch_w(ch + 2, x0);
-            give(ch + 1, x1);
-            fetch_w(ch + 3, x1);
-        }
+        if (tid == 0) bulk_wait_read<0>();
+    } else {
+        slab_out_any(slab, it, b, k.out);
     }
     tc_fence_before();
     __syncthreads();

@@ -107,9 +107,10 @@ cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const Sta
 // One cluster per block runs everything: momentum, norm, iterations, update or output.
 constexpr int kSmallStackSide = 128;     // longest short side
 constexpr int kSmallStackSlab = 512;     // columns of a CTA's slab at most
-constexpr int kSmallStackItems = 64;
+constexpr int kSmallStackItems = 48;    // of a launch: parameters are limited to 32 KB
 constexpr int kSmallStackCtas = 148;     // CTAs (one per SM) that run at once
-struct SmallStackItem {
+struct alignas(64) SmallStackItem {
+    CUtensorMap map_g, map_m, map_w;   // where `vec` says that TMA moves the array
     const void* G;
     float* M;             // nullable: orthogonalisation alone
     void* W;              // W <- decay * W + step * X; decay = 0: output only
@@ -117,7 +118,7 @@ struct SmallStackItem {
     int g_ld, m_ld, w_ld;
     int count, block0;
     int g_dtype, w_dtype;
-    int vec;              // as StackItem
+    int vec;              // bit 0: G, bit 1: M, bit 2: W go by TMA
     float decay, step;
 };
 struct SmallStackIter {
@@ -134,6 +135,8 @@ struct SmallStackClass {
     const float* gscale;
     unsigned* status;
 };
+// Fills the item's maps and `vec` from its arrays.
+void small_stack_maps(SmallStackItem& it, int rows, int cols);
 cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream);
 
 }  // namespace muon

@@ -665,8 +665,8 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
             it.g_dtype = s.x_dtype;
             it.w_dtype = s.y_dtype;
             it.count = s.count;
-            it.vec = (vec_ok(s.X, s.x_dtype, s.x_ld, s.x_stride) ? 1 : 0) | (vec_ok(s.Y, s.y_dtype, s.y_ld, s.y_stride) ? 4 : 0);
             it.step = 1.f;
+            small_stack_maps(it, s.rows, s.cols);
             items.push_back(it);
             blocks += s.count;
         }
@@ -913,9 +913,9 @@ muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, std
             it.g_dtype = s.g_dtype;
             it.w_dtype = s.w_dtype;
             it.count = s.count;
-            it.vec = step_vec(s);
             it.decay = static_cast<float>(1.0 - static_cast<double>(hp.lr) * hp.weight_decay);
             it.step = static_cast<float>(-static_cast<double>(hp.lr) * shape_scale(s.rows, s.cols, hp.scale_mode));
+            small_stack_maps(it, s.rows, s.cols);
             items.push_back(it);
             blocks += s.count;
         }
@@ -1021,10 +1021,11 @@ size_t norm_bytes(int n) {
 
 }  // namespace
 
-bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows) {
-    using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+namespace {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
     static const EncodeFn fn = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -1033,14 +1034,49 @@ bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, i
             p = nullptr;
         return reinterpret_cast<EncodeFn>(p);
     }();
+    return fn;
+}
+// A map of `count` matrices (strides in elements): boxes of 128 bytes x box_rows rows of one matrix, 128-byte
+// swizzle, zeros outside.
+bool encode_map(CUtensorMap* out, const void* base, CUtensorMapDataType type, int es, int rows, int cols, int count,
+                long long ld, long long stride, int box_rows) {
+    const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t gdim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
-    const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * rows * 2};
-    const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+    const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(ld) * es, static_cast<cuuint64_t>(stride) * es};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1u};
     const cuuint32_t estride[3] = {1u, 1u, 1u};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(out, type, 3, const_cast<void*>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows) {
+    return encode_map(out, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, count, cols,
+                      static_cast<long long>(rows) * cols, box_rows);
+}
+
+void small_stack_maps(SmallStackItem& it, int rows, int cols) {
+    it.vec = 0;
+    auto one = [&](CUtensorMap& m, int bit, const void* p, int dtype, int ld, long long stride) {
+        if (p == nullptr) return;
+        // a map's strides are positive: single rows and single blocks get the dense ones
+        const long long per16 = 16 / static_cast<long long>(elem_size(dtype));
+        const long long l = rows > 1 ? ld : cols;
+        const long long t = it.count > 1 ? stride : l * rows;
+        // Rows are whole 16-byte pieces: a store's clipping at the row's end is no finer (measured: a row of one
+        // fp16 came out four long).  Blocks whose rows interleave have legal maps too.
+        if (!aligned_to(p, 16) || cols % per16 != 0 || l % per16 != 0 || t % per16 != 0 || l <= 0 || t <= 0) return;
+        const CUtensorMapDataType type = dtype == MUON_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        // what the encoder refuses goes element by element
+        if (encode_map(&m, p, type, static_cast<int>(elem_size(dtype)), rows, cols, it.count, l, t, rows > cols ? 64 : 128))
+            it.vec |= bit;
+    };
+    one(it.map_g, 1, it.G, it.g_dtype, it.g_ld, it.g_stride);
+    one(it.map_m, 2, it.M, MUON_F32, it.m_ld, it.m_stride);
+    one(it.map_w, 4, it.W, it.w_dtype, it.w_ld, it.w_stride);
 }
 
 }  // namespace muon
