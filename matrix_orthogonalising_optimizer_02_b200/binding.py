@@ -7,7 +7,9 @@ fails, a ``MuonError`` is raised.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import itertools
 import os
 from ctypes import POINTER, c_double, c_float, c_int, c_longlong, c_size_t, c_void_p
 from dataclasses import dataclass
@@ -416,12 +418,22 @@ class AdamWTensor:
     v: object
 
 
+_CODES: dict = {}
+
+
+def _codes() -> dict:
+    """muon_dtype by torch dtype (filled on first use: the module imports without torch)."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: MUON_BF16, torch.float32: MUON_F32, torch.float16: MUON_F16})
+    return _CODES
+
+
 def _dtype16(t, name: str) -> int:
-    import torch
-    codes = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32, torch.float16: MUON_F16}
-    if t.dtype not in codes:
+    code = _codes().get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}: bf16, fp16 or fp32 expected")
-    return codes[t.dtype]
+    return code
 
 
 def _view3(t, name: str, device):
@@ -499,16 +511,17 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
-        self.guard = torch.cuda.device(device)
+        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
         self.device, self.stream = device, stream
 
     def __enter__(self):
         import torch
-        self.guard.__enter__()
+        if self.guard is not None:
+            self.guard.__enter__()
         return _stream(self.stream if self.stream is not None else torch.cuda.current_stream(self.device))
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        return self.guard.__exit__(*exc) if self.guard is not None else None
 
 
 def ns_stacks_workspace_size(stacks: Sequence[Stack], schedule: Schedule, with_saved: bool = False) -> int:
@@ -561,15 +574,34 @@ def muon_step_stacks(stacks: Sequence[MuonStack], hp, workspace, grad_scale=None
 
 
 # ---------------------------------------------------------------------------- gradient norm, AdamW
+# One row of 6 64-bit words per tensor, as adamw_tensor_desc lies in memory, made with maps over whole lists:
+# sets of hundreds of small tensors cost more on the host than on the GPU otherwise.
+def _adam_table(W, G, m, v, n, codes):
+    table = array.array("q", itertools.chain.from_iterable(zip(W, G, m, v, n, codes)))
+    return (AdamWTensorDesc * len(n)).from_buffer(table)
+
+
+def _dense(tensors, name, device):
+    """Checks that all are dense on `device`; returns their pointers and type codes."""
+    import torch
+    T = torch.Tensor
+    codes = list(map(_codes().get, [t.dtype for t in tensors]))
+    if not device.type == "cuda" or None in codes or not all(map(T.is_contiguous, tensors)) or \
+            set(map(T.get_device, tensors)) != {device.index}:
+        for t in tensors:      # one of them says what is wrong
+            _need(t, name, device=device)
+            _dtype16(t, name)
+    return list(map(T.data_ptr, tensors)), codes
+
+
 def _grad_descs(grads):
+    import torch
     if not grads:
         raise ValueError("no gradients")
-    arr = (AdamWTensorDesc * len(grads))()
     device = grads[0].device
-    for i, g in enumerate(grads):
-        _need(g, "G", device=device)
-        arr[i] = AdamWTensorDesc(None, g.data_ptr(), None, None, g.numel(), 0, _dtype16(g, "G"))
-    return arr, device
+    ptrs, codes = _dense(grads, "G", device)
+    none = itertools.repeat(0)
+    return _adam_table(none, ptrs, none, none, list(map(torch.Tensor.numel, grads)), [c << 32 for c in codes]), device
 
 
 def grad_norm_workspace_size(grads) -> int:
@@ -600,18 +632,16 @@ def adamw_step_batched(tensors: Sequence[AdamWTensor], hp: AdamWHyper, step, gra
     import torch
     if not tensors:
         raise ValueError("no tensors")
-    arr = (AdamWTensorDesc * len(tensors))()
-    device = tensors[0].W.device
-    for i, t in enumerate(tensors):
-        if tuple(t.G.shape) != tuple(t.W.shape) or tuple(t.m.shape) != tuple(t.W.shape) or \
-                tuple(t.v.shape) != tuple(t.W.shape):
-            raise ValueError("W, G, m and v must have the same shape")
-        if t.m.dtype != torch.float32 or t.v.dtype != torch.float32:
-            raise TypeError("the moments m and v must be fp32")
-        for x, name in ((t.W, "W"), (t.G, "G"), (t.m, "m"), (t.v, "v")):
-            _need(x, name, device=device)
-        arr[i] = AdamWTensorDesc(t.W.data_ptr(), t.G.data_ptr(), t.m.data_ptr(), t.v.data_ptr(), t.W.numel(),
-                                 _dtype16(t.W, "W"), _dtype16(t.G, "G"))
+    W, G, m, v = [t.W for t in tensors], [t.G for t in tensors], [t.m for t in tensors], [t.v for t in tensors]
+    shapes = [t.shape for t in W]
+    if any([t.shape for t in x] != shapes for x in (G, m, v)):
+        raise ValueError("W, G, m and v must have the same shape")
+    device = W[0].device
+    (wp, wc), (gp, gc), (mp, mc), (vp, vc) = (_dense(x, name, device) for x, name in
+                                              ((W, "W"), (G, "G"), (m, "m"), (v, "v")))
+    if {MUON_F32} != set(mc) | set(vc):
+        raise TypeError("the moments m and v must be fp32")
+    arr = _adam_table(wp, gp, mp, vp, list(map(torch.Tensor.numel, W)), [a | b << 32 for a, b in zip(wc, gc)])
     h = AdamWHyper(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, 0, None)
     if isinstance(step, torch.Tensor):
         h.step_dev = _scalar(step, "step", device, torch.int64)

@@ -13,6 +13,7 @@ namespace muon {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int kAdamFewItems = 60;
 constexpr int CHUNK = kAdamChunk;
 constexpr int GROUPS = CHUNK / 8 / THREADS;
 static_assert(GROUPS * 8 * THREADS == CHUNK, "a chunk is a whole number of groups per thread");
@@ -23,6 +24,8 @@ struct Params {
     int n;
     long long chunks;
 };
+
+static_assert(sizeof(Params<kAdamFewItems>) + sizeof(AdamParams) <= 4000, "the small form's parameters launch faster");
 
 template <int N>
 __device__ __forceinline__ int find(const Params<N>& p, long long chunk) {
@@ -157,7 +160,7 @@ cudaError_t grad_norm_launch(const AdamItem* items, int n, double* partials, flo
     int used = 0;
     for (int i = 0; i < n; i += kAdamMaxItems) {
         const int m = n - i < kAdamMaxItems ? n - i : kAdamMaxItems;
-        const cudaError_t e = m <= 8 ? norm_part<8>(items + i, m, partials, used, num_sms, stream)
+        const cudaError_t e = m <= kAdamFewItems ? norm_part<kAdamFewItems>(items + i, m, partials, used, num_sms, stream)
                                      : norm_part<kAdamMaxItems>(items + i, m, partials, used, num_sms, stream);
         if (e != cudaSuccess) return e;
     }
@@ -168,7 +171,7 @@ cudaError_t grad_norm_launch(const AdamItem* items, int n, double* partials, flo
 cudaError_t adamw_launch(const AdamItem* items, int n, const AdamParams& h, int num_sms, cudaStream_t stream) {
     for (int i = 0; i < n; i += kAdamMaxItems) {
         const int m = n - i < kAdamMaxItems ? n - i : kAdamMaxItems;
-        const cudaError_t e = m <= 8 ? adamw_part<8>(items + i, m, h, num_sms, stream)
+        const cudaError_t e = m <= kAdamFewItems ? adamw_part<kAdamFewItems>(items + i, m, h, num_sms, stream)
                                      : adamw_part<kAdamMaxItems>(items + i, m, h, num_sms, stream);
         if (e != cudaSuccess) return e;
     }

@@ -53,6 +53,8 @@ struct alignas(64) GemmParams {
     int n, tiles;
 };
 
+constexpr int kFewProbs = 5;
+
 struct Tile {
     int p, b, m0, n0;
 };
@@ -504,9 +506,10 @@ cudaError_t stack_gemm_launch(StackProb* probs, const int* counts, int n, unsign
     }
     if (tiles <= 0) return cudaSuccess;
     if (n > kStackMaxProbs || tiles > INT32_MAX) return cudaErrorInvalidValue;
-    // Parameters are copied with every launch: the small form where one or two problems suffice.
-    return n <= 2 ? launch<2>(probs, n, static_cast<int>(tiles), d_status, num_sms, stream)
-                  : launch<kStackMaxProbs>(probs, n, static_cast<int>(tiles), d_status, num_sms, stream);
+    // Parameters of up to 4 KB launch in 4 us, larger ones in 30 to 40 (10 KB): few problems take the small form.
+    static_assert(sizeof(GemmParams<kFewProbs>) <= 4000, "the small form's parameters stay below 4 KB");
+    return n <= kFewProbs ? launch<kFewProbs>(probs, n, static_cast<int>(tiles), d_status, num_sms, stream)
+                          : launch<kStackMaxProbs>(probs, n, static_cast<int>(tiles), d_status, num_sms, stream);
 }
 
 }  // namespace muon

@@ -24,6 +24,7 @@ struct PassParams {
     int n;
 };
 
+constexpr int kFewItems = 22;
 constexpr int GROUPS = kStackChunk / 8 / kStackThreads;   // 8-element groups per thread
 
 __device__ __forceinline__ float pow2f(int k) {   // 2^k, |k| <= 126
@@ -198,8 +199,9 @@ cudaError_t launch_any(StackItem* items, int n, const StackPassArgs& a, cudaStre
         if (chunks == 0) continue;
         StackPassArgs b = a;
         if (PASS == StackPass::kNorm && i0 > 0) b.status = nullptr;   // cleared once
-        const cudaError_t e = m <= 4 ? launch<PASS, 4>(items + i0, m, b, chunks, stream)
-                                     : launch<PASS, kStackMaxItems>(items + i0, m, b, chunks, stream);
+        static_assert(sizeof(PassParams<kFewItems>) <= 4000, "the small form's parameters launch faster (see stack_gemm.cu)");
+        const cudaError_t e = m <= kFewItems ? launch<PASS, kFewItems>(items + i0, m, b, chunks, stream)
+                                             : launch<PASS, kStackMaxItems>(items + i0, m, b, chunks, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

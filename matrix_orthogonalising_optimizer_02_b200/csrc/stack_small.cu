@@ -394,13 +394,17 @@ __device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& it
     }
 }
 
-struct SmallParamsS {
-    SmallStackItem item[kSmallStackItems];
+template <int N>
+struct SmallParams {
+    SmallStackItem item[N];
     SmallStackClass k;
     int n;
 };
+constexpr int kFewItems = 6;
+static_assert(sizeof(SmallParams<kFewItems>) <= 4096, "the small form's parameters launch faster");
 
-__global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParamsS p) {
+template <int N>
+__global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParams<N> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t bar_gram, bar_square, bar_apply[2], bar_rows, bar_a, bar_ring[kRing];
     __shared__ uint32_t tmem_slot;
@@ -771,9 +775,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     }
 }
 
-}  // namespace
-
-cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
+template <int N>
+cudaError_t launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
@@ -781,13 +784,13 @@ cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallSt
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!ready[dev].load()) {
-        e = cudaFuncSetAttribute(stack_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kSmallStackSlab));
+        e = cudaFuncSetAttribute(stack_small_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kSmallStackSlab));
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
-    for (int i0 = 0; i0 < n; i0 += kSmallStackItems) {
-        SmallParamsS p;
-        p.n = n - i0 < kSmallStackItems ? n - i0 : kSmallStackItems;
+    for (int i0 = 0; i0 < n; i0 += N) {
+        SmallParams<N> p;
+        p.n = n - i0 < N ? n - i0 : N;
         p.k = k;
         int blocks = 0;
         for (int i = 0; i < p.n; ++i) {
@@ -807,11 +810,17 @@ cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallSt
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, stack_small_kernel, p);
+        e = cudaLaunchKernelEx(&cfg, stack_small_kernel<N>, p);
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
+    return n <= kFewItems ? launch<kFewItems>(items, n, k, stream) : launch<kSmallStackItems>(items, n, k, stream);
 }
 
 }  // namespace muon
