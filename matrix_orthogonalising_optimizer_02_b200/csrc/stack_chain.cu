@@ -13,16 +13,25 @@
 // with 1% noise 5e-4 (1.6e-1).  Every product and every combination is held in fp32; a plane is
 // rounded once, when it is stored.
 //
+// One launch for the whole chain.  Pairs of CTAs stay and draw tiles from a counter in the order of the
+// operations; a tile waits until its block's earlier operations are done (a counter per block that every
+// finished epilogue warp raises).  A tile depends on tiles drawn earlier alone, and whoever has drawn one
+// is running, so the chain ends whatever else holds SMs.  Against a launch per operation this saves the
+// launch and its prologue (about 8 of the 12 us of a small product) and, with several blocks, the last
+// wave of every operation: 24 blocks of 509 x 1021 are 72 + 72 + 192 tiles an iteration on 74 pairs, 1 + 1 + 3
+// waves with gaps between them before, 4.5 without now.
+//
 // Two CTAs of a cluster compute one 256 x 256 tile with tcgen05.mma.cta_group::2 (K = 16 a step):
 // each stages its 128 rows of A and 128 columns of B, so an SM reads half the B bytes that a
 // one-SM tile would.  Roles per CTA (384 threads): warp 0 lane 0 TMA producer, warp 1 lane 0 of the
-// leader MMA issuer, warp 2 TMEM, warps 4..11 epilogue (TMEM double buffered, so the epilogue of
-// one tile overlaps the products of the next).  Global accesses of the epilogue are turned through
-// shared memory into 8 rows x 64 bytes per instruction.  The tiles of all problems form one list,
-// computed from the parameters; pair p takes tiles p, p + pairs, ...  Every wait is bounded
-// (ptx_sm100.cuh); no load uses cluster multicast.
+// leader MMA issuer, warp 2 TMEM, warp 3 lane 0 of the leader draws tiles (one ahead), warps 4..11
+// epilogue (TMEM double buffered, so the epilogue of one tile overlaps the products of the next).
+// Global accesses of the epilogue are turned through shared memory into 8 rows x 64 bytes per
+// instruction, E arrives there a chunk ahead.  Every wait is bounded (ptx_sm100.cuh); no load uses
+// cluster multicast.
 //
-// Bound: the tensor pipe for large blocks; launch and pipeline latency below about 1024 x 1024.
+// Bound: the tensor pipe for large blocks (under the 1 kW cap); latency of the chain's operations below about
+// 1024 x 1024.
 #include <atomic>
 
 #include "ptx_sm100.cuh"
@@ -40,54 +49,98 @@ constexpr int MN_CHUNK_BYTES = 64 * BK * 2;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int BAR_BYTES = 256;
 constexpr int THREADS = 384, EPI_THREADS = 256;
-// Per epilogue warp four 32 x 32 fp16 chunks (64-byte rows): direct store, transposed mirror, and
-// two of E (the one in use and the one being fetched).
+// Per epilogue warp six 32 x 32 fp16 chunks (64-byte rows): direct store, transposed mirror, and two of
+// each plane of E (the one in use and the one being fetched).
 constexpr int STG_BYTES = 32 * 64;
-constexpr int STG_WARP_BYTES = 4 * STG_BYTES;
+constexpr int STG_WARP_BYTES = 6 * STG_BYTES;
 constexpr int SMEM_TOTAL = STAGES * STAGE_BYTES + BAR_BYTES + (EPI_THREADS / 32) * STG_WARP_BYTES + 1024;
 static_assert(SMEM_TOTAL <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
 
-template <int N>
-struct alignas(64) GemmParams {
-    StackProb p[N];
+template <int NC, int NO>
+struct ChainParams {
+    ChainClass cls[NC];
+    ChainOp op[NO];
     int n, tiles;
+    int* ticket;
+    unsigned* status;
 };
-
-constexpr int kFewProbs = 5;
 
 struct Tile {
-    int p, b, m0, n0;
+    int b, m0, n0, M, N, K;
 };
-// Tile t of the launch: problem, block, and position (symmetric problems list the tiles with
-// mb <= nb, column by column).
-template <int N>
-__device__ __forceinline__ Tile tile_at(const GemmParams<N>& g, int t) {
+// Moves `op` on to the operation of tile t (tiles come in rising order) and gives the tile's place
+// (symmetric operations list the tiles with mb <= nb, column by column).
+template <class P>
+__device__ __forceinline__ Tile tile_at(const P& g, int t, int& op) {
+    while (op + 1 < g.n && g.op[op + 1].tile0 <= t) ++op;
+    const ChainOp& o = g.op[op];
+    const ChainClass& c = g.cls[o.cls];
     Tile r;
-    r.p = 0;
-    if (N > 1) {
-        while (r.p + 1 < g.n && g.p[r.p + 1].tile0 <= t) ++r.p;
-    }
-    const StackProb& P = g.p[r.p];
-    const int i = t - P.tile0;
-    r.b = i / P.block_tiles;
-    const int l = i - r.b * P.block_tiles;
+    const int nr = (c.r8 + BM - 1) / BM;
+    const int mbs = o.kind < 2 ? nr : (c.rp + BM - 1) / BM, nbs = o.kind < 2 ? nr : (c.cp + BN - 1) / BN;
+    r.M = o.kind < 2 ? c.r8 : c.rp;
+    r.N = o.kind < 2 ? c.r8 : c.cp;
+    r.K = o.kind == 0 ? max(c.rp, c.cp) : c.r8;
+    const int per = chain_tiles(c, o), i = t - o.tile0;
+    r.b = i / per;
+    const int l = i - r.b * per;
     int mb, nb;
-    if (P.flags & kStackSym) {
+    if (o.flags & kStackSym) {
         nb = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
         while (nb * (nb + 1) / 2 > l) --nb;
         while ((nb + 1) * (nb + 2) / 2 <= l) ++nb;
         mb = l - nb * (nb + 1) / 2;
-    } else if (P.flags & kStackRowMajor) {
-        mb = l / P.nbs;
-        nb = l - mb * P.nbs;
+    } else if (o.flags & kStackRowMajor) {
+        mb = l / nbs;
+        nb = l - mb * nbs;
     } else {
-        nb = l / P.mbs;
-        mb = l - nb * P.mbs;
+        nb = l / mbs;
+        mb = l - nb * mbs;
     }
     r.m0 = mb * BM;
     r.n0 = nb * BN;
     return r;
 }
+
+// Bounded wait until *p >= need; what the counted warps wrote is visible afterwards.
+__device__ __forceinline__ bool wait_done(const int* p, int need, volatile int* abort, unsigned* status) {
+    const unsigned long long t0 = global_ns();
+    while (true) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        if (v >= need) return true;
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicOr(status, kDevErrTimeout);
+            return false;
+        }
+        __nanosleep(32);
+    }
+}
+__device__ __forceinline__ void add_done(int* p) {
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+// Global data written by ordinary stores and read by TMA (on either side of a signal).
+__device__ __forceinline__ void fence_proxy_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// Tile numbers from the leader's drawer to both CTAs: a ring of two slots.
+struct Draws {
+    int* slot;             // this CTA's two slots
+    uint64_t* full;        // this CTA's: a number is there
+    uint32_t empty_leader; // the leader's: all readers of both CTAs have taken it
+    int i = 0;
+    // The next tile, or a negative number at the end.  By one thread per reader.
+    __device__ __forceinline__ int next(volatile int* abort, unsigned* status) {
+        const int k = i & 1;
+        if (!mbar_wait_cluster(&full[k], (i >> 1) & 1, abort, status)) return -1;
+        const int t = *reinterpret_cast<volatile int*>(&slot[k]);
+        mbar_arrive_cluster(empty_leader + 8u * k);
+        ++i;
+        return t;
+    }
+};
+constexpr int kReaders = 1 + 1 + 8 + 1 + 8;   // producer, issuer, epilogue warps; producer, epilogue warps
 
 __device__ __forceinline__ int stg_off64(int row, int seg) { return row * 64 + 16 * (seg ^ ((row >> 1) & 3)); }
 
@@ -126,9 +179,9 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-template <int N>
+template <int NC, int NO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status) {
+stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
@@ -136,14 +189,16 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
     uint64_t* empty_bar = bars + STAGES;            // both: MMAs reading the stage are done
     uint64_t* tfull_bar = bars + 2 * STAGES;        // both: accumulator ready
     uint64_t* tempty_bar = bars + 2 * STAGES + 2;   // leader: both epilogues drained it
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+    uint64_t* dfull_bar = bars + 2 * STAGES + 4;    // both: a tile has been drawn
+    uint64_t* dempty_bar = bars + 2 * STAGES + 6;   // leader: every reader has it
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* draw_slot = reinterpret_cast<int*>(tmem_slot + 2);
+    unsigned* dev_status = g.status;
 
-    griddep_launch_dependents();   // the next launch waits for this grid before it touches memory
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -153,6 +208,8 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull_bar[a], 1);
             mbar_init(&tempty_bar[a], 2 * EPI_THREADS);
+            mbar_init(&dfull_bar[a], 1);
+            mbar_init(&dempty_bar[a], kReaders);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -167,26 +224,45 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t full_leader = mapa_shared(smem_u32(full_bar), 0);
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty_bar), 0);
+    Draws draws = {draw_slot, dfull_bar, mapa_shared(smem_u32(dempty_bar), 0)};
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 3 && lane == 0 && rank == 0) {
+        // ------------------------------------------------------------ draws tiles
+        const uint32_t peer_slot = mapa_shared(smem_u32(draw_slot), 1), peer_full = mapa_shared(smem_u32(dfull_bar), 1);
+        for (int i = 0;; ++i) {
+            const int k = i & 1;
+            int t = atomicAdd(g.ticket, 1);
+            if (t >= g.tiles) t = -1;
+            if (!mbar_wait_cluster(&dempty_bar[k], ((i >> 1) & 1) ^ 1u, abort_flag, dev_status)) break;
+            *reinterpret_cast<volatile int*>(&draw_slot[k]) = t;
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_slot + 4u * k), "r"(t) : "memory");
+            mbar_arrive_cluster(mapa_shared(smem_u32(&dfull_bar[k]), 0));
+            mbar_arrive_cluster(peer_full + 8u * k);
+            if (t < 0) break;
+        }
+    } else if (warp == 0 && lane == 0) {
         // ------------------------------------------------------------ TMA producer
-        griddep_wait();
         uint32_t stage = 0, phase = 0;
         bool ok = true;
+        int op = 0;
         int issued_parity[STAGES];
 #pragma unroll
         for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
-        for (int t = pair; t < g.tiles && ok; t += npairs) {
-            const Tile ti = tile_at(g, t);
-            const StackProb& P = g.p[ti.p];
+        for (int t; ok && (t = draws.next(abort_flag, dev_status)) >= 0;) {
+            const Tile ti = tile_at(g, t, op);
+            const ChainOp& P = g.op[op];
+            const ChainClass& c = g.cls[P.cls];
+            if (!wait_done(c.done + ti.b, P.need, abort_flag, dev_status)) { ok = false; break; }
+            fence_proxy_global();
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
             const int am0 = ti.m0 + HM * static_cast<int>(rank);
             const int bn0 = ti.n0 + HN * static_cast<int>(rank);
-            const int kblocks = (P.K + BK - 1) / BK;
+            const int kblocks = (ti.K + BK - 1) / BK;
             for (int seg = 0; seg < P.nseg && ok; ++seg) {
-                const CUtensorMap* ta = &P.tmA[seg];
-                const CUtensorMap* tb = &P.tmB[seg];
+                const CUtensorMap* ta = &c.map[P.ma[seg]];
+                const CUtensorMap* tb = &c.map[P.mb[seg]];
+                const int za = P.sa[seg] * c.count + ti.b, zb = P.sb[seg] * c.count + ti.b;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, dev_status)) { ok = false; break; }
                     uint8_t* sa = smem + stage * STAGE_BYTES;
@@ -198,18 +274,18 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
                         issued_parity[stage] = static_cast<int>(phase);
                     }
                     if (!a_mn) {
-                        tma_load_3d_pair(sa, ta, fb, k0, am0, ti.b);
+                        tma_load_3d_pair(sa, ta, fb, k0, am0, za);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < HM / 64; ++c)
-                            tma_load_3d_pair(sa + c * MN_CHUNK_BYTES, ta, fb, am0 + 64 * c, k0, ti.b);
+                        for (int h = 0; h < HM / 64; ++h)
+                            tma_load_3d_pair(sa + h * MN_CHUNK_BYTES, ta, fb, am0 + 64 * h, k0, za);
                     }
                     if (!b_mn) {
-                        tma_load_3d_pair(sb, tb, fb, k0, bn0, ti.b);
+                        tma_load_3d_pair(sb, tb, fb, k0, bn0, zb);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < HN / 64; ++c)
-                            tma_load_3d_pair(sb + c * MN_CHUNK_BYTES, tb, fb, bn0 + 64 * c, k0, ti.b);
+                        for (int h = 0; h < HN / 64; ++h)
+                            tma_load_3d_pair(sb + h * MN_CHUNK_BYTES, tb, fb, bn0 + 64 * h, k0, zb);
                     }
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -231,13 +307,14 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
         // ------------------------------------------------------------ MMA issuer (leader)
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
         bool ok = true;
-        for (int t = pair; t < g.tiles && ok; t += npairs) {
-            const Tile ti = tile_at(g, t);
-            const StackProb& P = g.p[ti.p];
+        int op = 0;
+        for (int t; ok && (t = draws.next(abort_flag, dev_status)) >= 0;) {
+            const Tile ti = tile_at(g, t, op);
+            const ChainOp& P = g.op[op];
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
             const uint32_t idesc = idesc_f16_f32(BM, BN, a_mn, b_mn);
-            const int kblocks = (P.K + BK - 1) / BK * P.nseg;
+            const int kblocks = (ti.K + BK - 1) / BK * P.nseg;
             if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag, dev_status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
@@ -280,41 +357,57 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
         const int c_end = c_beg + BN / 64;
         uint8_t* stg = smem + STAGES * STAGE_BYTES + BAR_BYTES + (warp - 4) * STG_WARP_BYTES;
         uint8_t* stg_t = stg + STG_BYTES;
-        uint8_t* stg_e = stg + 2 * STG_BYTES;
+        uint8_t* stg_e = stg + 2 * STG_BYTES;          // plane 0 of E: two buffers; plane 1: the next two
         const int crow = lane >> 2, cseg = lane & 3;   // coalesced layout: rows crow + 8i, segment cseg
-        griddep_wait();
         uint32_t acc = 0, acc_phase = 0;
-        for (int t = pair; t < g.tiles; t += npairs) {
-            const Tile ti = tile_at(g, t);
-            const StackProb& P = g.p[ti.p];
+        int op = 0;
+        while (true) {
+            int t = 0;
+            if (lane == 0) t = draws.next(abort_flag, dev_status);
+            t = __shfl_sync(0xffffffffu, t, 0);
+            if (t < 0) break;
+            const Tile ti = tile_at(g, t, op);
+            const ChainOp& P = g.op[op];
+            const ChainClass& cl = g.cls[P.cls];
+            int ready = 0;
+            if (lane == 0) ready = wait_done(cl.done + ti.b, P.need, abort_flag, dev_status);
+            if (!__shfl_sync(0xffffffffu, ready, 0)) break;
             float f = 1.0f;
-            if (P.dscale != nullptr) {
-                const float s = __ldg(P.dscale + static_cast<size_t>(ti.b) * kStackInfo);
-                f = (P.scale_pow == 1) ? s : s * s;
+            if (P.pow != 0) {
+                const float x = cl.info[static_cast<size_t>(ti.b) * kStackInfo];
+                f = P.pow == 1 ? x : x * x;
             }
             const float alpha = P.alpha * f, beta = P.beta * f;
             const bool sym = (P.flags & kStackSym) != 0;
             const bool bf = (P.flags & kStackOutBf16) != 0;
             const int row0 = ti.m0 + HM * static_cast<int>(rank) + q * 32;
-            const __half* e0 = P.E[0] != nullptr ? P.E[0] + static_cast<size_t>(ti.b) * P.e_stride : nullptr;
-            const __half* e1 = P.E[1] != nullptr ? P.E[1] + static_cast<size_t>(ti.b) * P.e_stride : nullptr;
-            const int planes = P.out[1] != nullptr ? 2 : 1;
-            const size_t o_base = static_cast<size_t>(ti.b) * P.o_stride;
+            auto plane_of = [&](int pl, int slot) {
+                return pl == kPlaneNone ? nullptr
+                                        : cl.plane[pl].p + (static_cast<size_t>(slot) * cl.count + ti.b) * cl.plane[pl].block;
+            };
+            const __half* e0 = plane_of(P.e[0], P.es[0]);
+            const __half* e1 = plane_of(P.e[1], P.es[1]);
+            __half* o_plane[2] = {plane_of(P.o[0], P.os[0]), plane_of(P.o[1], P.os[1])};
+            const int planes = o_plane[1] != nullptr ? 2 : 1;
+            const int e_ld = ti.N, o_ld = cl.plane[P.o[0]].ld;
+            const int m_out = P.o[0] == kPlaneOut ? cl.rows : ti.M;
             const uint32_t t_row = tmem_base + acc * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
 
-            // Plane 0 of E for chunk c goes by cp.async into staging slot c & 1, one commit group
-            // per chunk, so it is in flight while the previous chunk is processed.
+            // E of chunk c goes by cp.async into staging slot c & 1, one commit group per chunk, so it is in
+            // flight while the previous chunk is processed.
             auto prefetch_e = [&](int c) {
                 const int col0 = ti.n0 + c * 32;
-                if (e0 != nullptr && col0 < P.N && !(sym && col0 + 31 < row0)) {
+                if (e0 != nullptr && col0 < ti.N && !(sym && col0 + 31 < row0)) {
                     uint8_t* dst = stg_e + (c & 1) * STG_BYTES;
                     const int cc = col0 + 8 * cseg;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int rr = row0 + crow + 8 * i;
-                        const bool in = rr < P.M && cc < P.N;
-                        cp_async16_zfill(dst + stg_off64(crow + 8 * i, cseg),
-                                         in ? e0 + static_cast<size_t>(rr) * P.e_ld + cc : e0, in ? 16 : 0);
+                        const bool in = rr < ti.M && cc < ti.N;
+                        const size_t at = in ? static_cast<size_t>(rr) * e_ld + cc : 0;
+                        cp_async16_zfill(dst + stg_off64(crow + 8 * i, cseg), e0 + at, in ? 16 : 0);
+                        if (e1 != nullptr)
+                            cp_async16_zfill(dst + 2 * STG_BYTES + stg_off64(crow + 8 * i, cseg), e1 + at, in ? 16 : 0);
                     }
                 }
                 cp_async_commit();
@@ -328,21 +421,9 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
 #pragma unroll 1
             for (int c = c_beg; c < c_end; ++c) {
                 const int col0 = ti.n0 + c * 32;
-                if (col0 >= P.N) break;  // uniform across the warp
+                if (col0 >= ti.N) break;  // uniform across the warp
                 const bool below = sym && col0 < row0;    // its mirror image is stored instead
                 const bool mirror = sym && col0 > row0;   // a chunk on the diagonal holds both halves
-                // plane 1 of E of this chunk: read directly, in the coalesced layout
-                uint4 el[4];
-                if (e1 != nullptr && !below) {
-                    const int cc = col0 + 8 * cseg;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int rr = row0 + crow + 8 * i;
-                        el[i] = rr < P.M && cc < P.N
-                                    ? *reinterpret_cast<const uint4*>(e1 + static_cast<size_t>(rr) * P.e_ld + cc)
-                                    : make_uint4(0, 0, 0, 0);
-                    }
-                }
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_row + c * 32, r);
                 if (c + 1 < c_end) prefetch_e(c + 1);
@@ -359,25 +440,11 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
                         if (j == lane) v[j] -= P.diag;
                 }
                 if (e0 != nullptr && !below) {
-                    const uint8_t* src = stg_e + (c & 1) * STG_BYTES;
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(src + stg_off64(lane, s));
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const float2 e = unpack_half2(x[h]);
-                            v[8 * s + 2 * h] = fmaf(beta, e.x, v[8 * s + 2 * h]);
-                            v[8 * s + 2 * h + 1] = fmaf(beta, e.y, v[8 * s + 2 * h + 1]);
-                        }
-                    }
-                    if (e1 != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(stg + stg_off64(crow + 8 * i, cseg)) = el[i];
-                        __syncwarp();
+                    for (int pl = 0; pl < (e1 != nullptr ? 2 : 1); ++pl) {
+                        const uint8_t* src = stg_e + ((c & 1) + 2 * pl) * STG_BYTES;
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(stg + stg_off64(lane, s));
+                            const uint4 w = *reinterpret_cast<const uint4*>(src + stg_off64(lane, s));
                             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                             for (int h = 0; h < 4; ++h) {
@@ -408,13 +475,13 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
                             *reinterpret_cast<uint4*>(stg + stg_off64(lane, s)) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                         __syncwarp();
-                        __half* o = static_cast<__half*>(P.out[pl]) + o_base;   // bf16: the same 2 bytes
+                        __half* o = o_plane[pl];   // bf16: the same 2 bytes
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int rr = row0 + crow + 8 * i, cc = col0 + 8 * cseg;
                             const uint4 val = *reinterpret_cast<const uint4*>(stg + stg_off64(crow + 8 * i, cseg));
-                            if (rr < P.m_out && cc < P.N)
-                                *reinterpret_cast<uint4*>(o + static_cast<size_t>(rr) * P.o_ld + cc) = val;
+                            if (rr < m_out && cc < ti.N)
+                                *reinterpret_cast<uint4*>(o + static_cast<size_t>(rr) * o_ld + cc) = val;
                         }
                         if (mirror) {
                             stg_transpose32(stg, stg_t, lane);
@@ -423,8 +490,8 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
                             for (int i = 0; i < 4; ++i) {
                                 const int rr = col0 + crow + 8 * i, cc = row0 + 8 * cseg;
                                 const uint4 val = *reinterpret_cast<const uint4*>(stg_t + stg_off64(crow + 8 * i, cseg));
-                                if (rr < P.N && cc < P.M)
-                                    *reinterpret_cast<uint4*>(o + static_cast<size_t>(rr) * P.o_ld + cc) = val;
+                                if (rr < ti.N && cc < ti.M)
+                                    *reinterpret_cast<uint4*>(o + static_cast<size_t>(rr) * o_ld + cc) = val;
                             }
                         }
                         __syncwarp();
@@ -434,6 +501,11 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
             cp_async_wait_all();
             tc_fence_before();
             mbar_arrive_cluster(tempty_leader + acc * 8u);
+            // the block's next operation may read what this warp stored, by TMA among other ways
+            fence_proxy_global();
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) add_done(cl.done + ti.b);
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
     }
@@ -444,8 +516,9 @@ stack_gemm_kernel(const __grid_constant__ GemmParams<N> g, unsigned* dev_status)
 }
 
 // The launch of one instantiation; its attributes and occupancy are looked up once per device.
-template <int N>
-cudaError_t launch(const StackProb* probs, int n, int tiles, unsigned* d_status, int num_sms, cudaStream_t stream) {
+template <int NC, int NO>
+cudaError_t launch(const ChainClass* classes, int nc, const ChainOp* ops, int n, int tiles, int* ticket, unsigned* d_status,
+                   int num_sms, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static std::atomic<int> max_pairs_of[kMaxDevices];
     int dev = 0;
@@ -457,7 +530,7 @@ cudaError_t launch(const StackProb* probs, int n, int tiles, unsigned* d_status,
     cfg.dynamicSmemBytes = SMEM_TOTAL;
     int max_pairs = max_pairs_of[dev].load();
     if (max_pairs == 0) {
-        e = cudaFuncSetAttribute(stack_gemm_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+        e = cudaFuncSetAttribute(stack_chain_kernel<NC, NO>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
         cudaLaunchAttribute attr;
@@ -467,49 +540,48 @@ cudaError_t launch(const StackProb* probs, int n, int tiles, unsigned* d_status,
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&max_pairs, stack_gemm_kernel<N>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&max_pairs, stack_chain_kernel<NC, NO>, &cfg);
         if (e != cudaSuccess || max_pairs <= 0) {
             cudaGetLastError();
             max_pairs = num_sms / 2;
         }
         max_pairs_of[dev].store(max_pairs);
     }
-    GemmParams<N> g;
-    for (int i = 0; i < n; ++i) g.p[i] = probs[i];
+    ChainParams<NC, NO> g;
+    for (int i = 0; i < nc; ++i) g.cls[i] = classes[i];
+    for (int i = 0; i < n; ++i) g.op[i] = ops[i];
     g.n = n;
     g.tiles = tiles;
-    // At most the resident capacity: every CTA runs from the start, so the CTAs of the next launch,
-    // which wait for this grid, only take SMs that finished CTAs released.
+    g.ticket = ticket;
+    g.status = d_status;
     cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < max_pairs ? tiles : max_pairs), 1, 1);
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, stack_gemm_kernel<N>, g, d_status);
+    cfg.attrs = nullptr;
+    cfg.numAttrs = 0;
+    e = cudaLaunchKernelEx(&cfg, stack_chain_kernel<NC, NO>, g);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t stack_gemm_launch(StackProb* probs, const int* counts, int n, unsigned* d_status, int num_sms,
-                              cudaStream_t stream) {
+cudaError_t stack_chain_launch(const ChainClass* classes, int nc, ChainOp* ops, int n, int* ticket, unsigned* d_status,
+                               int num_sms, cudaStream_t stream) {
     long long tiles = 0;
     for (int i = 0; i < n; ++i) {
-        StackProb& P = probs[i];
-        P.mbs = (P.M + BM - 1) / BM;
-        P.nbs = (P.N + BN - 1) / BN;
-        P.block_tiles = stack_block_tiles(P.mbs, P.nbs, (P.flags & kStackSym) != 0);
-        P.tile0 = static_cast<int>(tiles);
-        tiles += static_cast<long long>(P.block_tiles) * counts[i];
+        ops[i].tile0 = static_cast<int>(tiles);
+        const ChainClass& c = classes[ops[i].cls];
+        tiles += static_cast<long long>(chain_tiles(c, ops[i])) * c.count;
+        if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     }
-    if (tiles <= 0) return cudaSuccess;
-    if (n > kStackMaxProbs || tiles > INT32_MAX) return cudaErrorInvalidValue;
-    // Parameters of up to 4 KB launch in 4 us, larger ones in 30 to 40 (10 KB): few problems take the small form.
-    static_assert(sizeof(GemmParams<kFewProbs>) <= 4000, "the small form's parameters stay below 4 KB");
-    return n <= kFewProbs ? launch<kFewProbs>(probs, n, static_cast<int>(tiles), d_status, num_sms, stream)
-                          : launch<kStackMaxProbs>(probs, n, static_cast<int>(tiles), d_status, num_sms, stream);
+    if (tiles == 0) return cudaSuccess;
+    if (nc > kChainMaxClasses || n > kChainMaxOps) return cudaErrorInvalidValue;
+    // Parameters of up to 4 KB launch in 4 us, larger ones in 30 to 40 (10 KB): short chains take the small form.
+    static_assert(sizeof(ChainParams<2, 30>) <= 4000, "the small form's parameters stay below 4 KB");
+    static_assert(sizeof(ChainParams<kChainMaxClasses, kChainMaxOps>) <= 32700, "the limit of a launch's parameters");
+    if (nc <= 2 && n <= 30)
+        return launch<2, 30>(classes, nc, ops, n, static_cast<int>(tiles), ticket, d_status, num_sms, stream);
+    return launch<kChainMaxClasses, kChainMaxOps>(classes, nc, ops, n, static_cast<int>(tiles), ticket, d_status, num_sms,
+                                                  stream);
 }
 
 }  // namespace muon

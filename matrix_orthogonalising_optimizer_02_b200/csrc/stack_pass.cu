@@ -24,7 +24,7 @@ struct PassParams {
     int n;
 };
 
-constexpr int kFewItems = 22;
+constexpr int kFewItems = 21;
 constexpr int GROUPS = kStackChunk / 8 / kStackThreads;   // 8-element groups per thread
 
 __device__ __forceinline__ float pow2f(int k) {   // 2^k, |k| <= 126
@@ -79,6 +79,8 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
                 info[3] = static_cast<float>(n);
                 if (!fin && p.a.status != nullptr) atomicOr(p.a.status, kDevErrNonfinite);
             }
+            if (c == 0 && threadIdx.x == 1) it.done[b] = 0;
+            if (blockIdx.x == 0 && threadIdx.x < kStackTickets) p.a.tickets[threadIdx.x] = 0;
             if (PASS == StackPass::kPackGrad) up *= it.step;
         }
     }

@@ -13,47 +13,64 @@
 
 namespace muon {
 
-// ------------------------------------------------------------------ grouped fp16 GEMM
-// One problem of a launch: `count` products of one shape,
-//   out[b] = f_b * (alpha * sum_seg A_seg[b] x B_seg[b] + beta * (E[0][b] + E[1][b])) - diag * I,
-// f_b = dscale[b]^scale_pow, fp16 operands with fp32 accumulation in TMEM.  The K loop runs
-// over up to two operand pairs (segments) of the same K.  E and out are fp16 planes (value =
-// plane 0 + plane 1, plane 1 optional) with a row pitch and a block stride of their own.
+// ------------------------------------------------------------------ chains of fp16 products
+// One launch runs a whole chain: a list of operations, each a product for every block of a class
+//   out[b] = f_b * (alpha * sum_seg A_seg[b] x B_seg[b] + beta * (E0[b] + E1[b])) - diag * I,
+// f_b = info[b][0]^pow, fp16 operands with fp32 accumulation in TMEM.  An operation of a block starts when
+// the block's operations before it are done; blocks do not wait for each other.
+//
+// A class's planes lie in slots (iterations, or ping and pong) of `count` dense matrices one behind the
+// other; a tensor map covers all slots of a plane.
 constexpr uint32_t kStackAMn = 1u;       // A is contiguous along M (else along K)
 constexpr uint32_t kStackBMn = 2u;       // B is contiguous along N (else along K)
 constexpr uint32_t kStackSym = 4u;       // symmetric output: upper tiles computed, stored mirrored
 constexpr uint32_t kStackOutBf16 = 8u;   // plane 0 of the output is bf16
 constexpr uint32_t kStackRowMajor = 16u; // tiles swept along the rows of a block first
 
-struct alignas(64) StackProb {
-    CUtensorMap tmA[2];
-    CUtensorMap tmB[2];
-    const __half* E[2];
-    void* out[2];
-    const float* dscale;
-    long long e_stride, o_stride;    // elements between blocks
-    int e_ld, o_ld;                  // elements between rows
-    int M, N, K;                     // multiples of 8
-    int m_out;                       // rows stored (<= M)
-    int nseg;
-    float alpha, beta;
-    float diag;                      // subtracted on the diagonal of out
-    int scale_pow;
-    uint32_t flags;
-    int mbs, nbs;                    // 256 x 256 tiles of a block
-    int tile0, block_tiles;          // first tile of this problem, tiles per block
+enum StackPlane { kPlaneX, kPlaneL, kPlaneA, kPlaneB, kPlaneOut, kPlaneD, kPlaneDL, kPlaneS, kPlaneP, kPlanes, kPlaneNone = 255 };
+enum StackMap { kMapXk, kMapXmn, kMapA, kMapB, kMapDk, kMapDmn, kMapS, kMapP, kMaps };
+
+struct ChainPlane {
+    __half* p;
+    long long block;       // elements between blocks
+    int ld;                // elements between rows
 };
-constexpr int kStackMaxProbs = 16;
+struct alignas(64) ChainClass {
+    CUtensorMap map[kMaps];
+    ChainPlane plane[kPlanes];
+    const float* info;     // kStackInfo floats per block
+    int* done;             // per block: epilogue warps that have finished a tile
+    int rp, cp, r8;        // padded sides of a block, padded shorter side
+    int rows;              // rows that kPlaneOut takes
+    int count;
+};
+struct ChainOp {
+    float alpha, beta, diag;
+    int tile0;             // first tile of the operation in the launch (filled by the launcher)
+    int need;              // value of `done` at which a block's operation may start (filled by the caller)
+    uint8_t cls, kind;     // kind 0: r8 x r8 over the long side, 1: r8 x r8 over r8, 2: rp x cp over r8
+    uint8_t flags, nseg, pow;
+    uint8_t ma[2], mb[2];  // tensor maps of the segments' operands
+    uint8_t sa[2], sb[2];  // and their slots
+    uint8_t e[2], es[2];   // planes and slots of E
+    uint8_t o[2], os[2];   // and of the output
+};
+constexpr int kChainWarps = 16;          // epilogue warps of a tile: what a finished tile adds to `done`
+constexpr int kChainMaxClasses = 12, kChainMaxOps = 360;
 
 // Tensor map of `count` row-major fp16 matrices (rows x cols, dense): a box of 64 columns x
 // box_rows rows of one matrix, 128-byte swizzle, zero fill out of bounds.
 bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows);
 
-inline int stack_block_tiles(int mbs, int nbs, bool sym) { return sym ? nbs * (nbs + 1) / 2 : mbs * nbs; }
-
-// Fills mbs, nbs, tile0, block_tiles of every problem and launches.
-cudaError_t stack_gemm_launch(StackProb* probs, const int* counts, int n, unsigned* d_status, int num_sms,
-                              cudaStream_t stream);
+// Tiles of one block of an operation.
+__host__ __device__ inline int chain_tiles(const ChainClass& c, const ChainOp& o) {
+    const int nr = (c.r8 + 255) / 256;
+    return o.kind < 2 ? nr * (nr + 1) / 2 : ((c.rp + 255) / 256) * ((c.cp + 255) / 256);
+}
+// Launches ops[0 .. n) (in order; dependencies point backwards).  `ticket`: an int of the workspace that
+// is zero; `done` counters carry on from earlier launches of the chain.
+cudaError_t stack_chain_launch(const ChainClass* classes, int nc, ChainOp* ops, int n, int* ticket, unsigned* d_status,
+                               int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------ elementwise passes
 // A run of blocks of one stack, as the elementwise kernels see it.  Element (b, i, j) of a
@@ -77,6 +94,7 @@ struct alignas(16) StackItem {
     int g_dtype, w_dtype;
     int vec;              // bit 0: G, bit 1: M, bit 2: W allow 8-element vector accesses
     float decay, step;    // W <- decay * W + step * X (step kernels); X * step (output)
+    int* done;            // kPack, kPackGrad: per block, set to zero
 };
 constexpr int kStackMaxItems = 128;
 constexpr int kStackThreads = 256;
@@ -84,6 +102,7 @@ constexpr int kStackChunk = 8192;        // padded elements per chunk: 256 threa
 // Per block: info[0] = f0 (X_0 = f0 * hi), info[1] = 2^k (hi = U * 2^k), info[2] = 1 / (N + eps),
 // info[3] = N
 constexpr int kStackInfo = 4;
+constexpr int kStackTickets = 64;
 
 enum class StackPass {
     kNorm,      // partials <- sum of U^2 (M updated in place where there is one)
@@ -99,6 +118,7 @@ struct StackPassArgs {
     int nesterov;
     float eps;
     const float* gscale;    // device: factor of G (nullable: 1)
+    int* tickets;           // kPack, kPackGrad: kStackTickets ints set to zero
     unsigned* status;       // kNorm: cleared (unless null); kPack, kPackGrad: told of a norm that is not finite
 };
 cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const StackPassArgs& args, cudaStream_t stream);

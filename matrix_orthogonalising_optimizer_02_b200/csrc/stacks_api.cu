@@ -2,9 +2,9 @@
 // checks, scales, workspace layout and launches.
 //
 // Blocks of one shape, whatever stack they come from, form a class: their planes lie one behind the
-// other in the workspace and one problem of a launch covers them.  An iteration is three launches
-// for all classes together (Gram, polynomial, apply); tall blocks are not transposed (their Gram
-// matrix is X^T X and the apply step X B).
+// other in the workspace and one operation of a chain (stack_chain.cu) covers them.  An iteration is three
+// operations per class (Gram, polynomial, apply); tall blocks are not transposed (their Gram matrix is
+// X^T X and the apply step X B).
 //
 // Scales.  With S_t a bound of the singular values of X_t, computed from the schedule (S_0 = 1), the
 // planes hold  X_t * tau_t,  A_t * alpha_t,  B_t * gamma_t  with powers of two such that no element
@@ -109,11 +109,15 @@ struct StackClass {
     int chunks = 0;
     std::vector<double> alpha, gamma, tau;       // tau[0] unused: X_0 = f0 * plane
     std::vector<double> shift, a, b;             // l; a + bl + cl^2 and b + 2cl (a and b without a shift)
-    std::vector<__half*> X;                      // X_0 .. X_T
-    __half* L[2] = {nullptr, nullptr};           // second plane of X_t in L[t & 1]
-    std::vector<__half*> A, B;
+    __half* X = nullptr;                         // x_slots slots: X_t in slot t % x_slots
+    __half* L = nullptr;                         // second plane of X_t in slot t & 1
+    __half* A = nullptr;                         // a_slots slots: A_t, B_t in slot t % a_slots
+    __half* B = nullptr;
+    __half* last = nullptr;                      // X_T
+    int x_slots = 2, a_slots = 1;
     float* info = nullptr;
     double* partials = nullptr;
+    int* done = nullptr;
     size_t plane() const { return static_cast<size_t>(count) * rp * cp * sizeof(__half); }
     size_t square() const { return static_cast<size_t>(count) * r8 * r8 * sizeof(__half); }
 };
@@ -258,7 +262,7 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
             StackClass one = make_class(shapes[i].rows, shapes[i].cols, sch, bd);
             one.count = 1;
             const size_t each = 4 * one.plane() + 2 * one.square() + static_cast<size_t>(one.chunks) * sizeof(double) +
-                                kStackInfo * sizeof(float);
+                                kStackInfo * sizeof(float) + sizeof(int);
             int cls = -1;
             for (size_t k = 0; k < g->classes.size(); ++k)
                 if (g->classes[k].rows == one.rows && g->classes[k].cols == one.cols) cls = static_cast<int>(k);
@@ -266,7 +270,7 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
             int take = static_cast<int>(std::min<size_t>(shapes[i].count - first, room));
             const bool empty = g->parts.empty();
             if (take == 0 && empty) take = 1;                    // a single block above the budget
-            if (take == 0 || (cls < 0 && static_cast<int>(g->classes.size()) == kStackMaxProbs)) {
+            if (take == 0 || (cls < 0 && static_cast<int>(g->classes.size()) == kChainMaxClasses)) {
                 groups.emplace_back();
                 used = 0;
                 continue;
@@ -287,92 +291,94 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
     return groups;
 }
 
-// Pointers of a group's planes; `sv` takes what the reverse pass reads.  Returns the workspace used.
+// Pointers of a group's planes; `sv` takes what the reverse pass reads.  Returns the workspace used.  The
+// workspace begins with the chain's tile counters.
 size_t layout_forward(Group& g, int T, bool saving, Arena& ws, Arena& sv) {
+    auto take = [](Arena& a, size_t bytes) { return a.at(a.take(bytes)); };
+    take(ws, kStackTickets * sizeof(int));
     for (StackClass& c : g.classes) {
         Arena& keep = saving ? sv : ws;
-        auto take = [](Arena& a, size_t bytes) { return static_cast<uint8_t*>(a.at(a.take(bytes))); };
-        c.info = reinterpret_cast<float*>(take(keep, static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
-        c.partials = reinterpret_cast<double*>(take(ws, static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
-        c.X.assign(T + 1, nullptr);
-        c.A.assign(T, nullptr);
-        c.B.assign(T, nullptr);
-        for (int t = 0; t <= T; ++t) {
-            if (saving) c.X[t] = reinterpret_cast<__half*>(take(t < T ? keep : ws, c.plane()));
-            else c.X[t] = t < 2 ? reinterpret_cast<__half*>(take(ws, c.plane())) : c.X[t - 2];
-        }
-        for (int t = 0; t < T; ++t) {
-            c.A[t] = saving || t == 0 ? reinterpret_cast<__half*>(take(keep, c.square())) : c.A[0];
-            c.B[t] = saving || t == 0 ? reinterpret_cast<__half*>(take(keep, c.square())) : c.B[0];
-        }
-        for (auto& l : c.L) l = reinterpret_cast<__half*>(take(ws, c.plane()));
+        c.info = static_cast<float*>(take(keep, static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
+        c.partials = static_cast<double*>(take(ws, static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
+        c.done = static_cast<int*>(take(ws, static_cast<size_t>(c.count) * sizeof(int)));
+        c.x_slots = saving ? T : 2;
+        c.a_slots = saving ? T : 1;
+        c.X = static_cast<__half*>(take(keep, c.x_slots * c.plane()));
+        c.A = static_cast<__half*>(take(keep, c.a_slots * c.square()));
+        c.B = static_cast<__half*>(take(keep, c.a_slots * c.square()));
+        c.L = static_cast<__half*>(take(ws, 2 * c.plane()));
+        if (saving) c.last = static_cast<__half*>(take(ws, c.plane()));
+        else c.last = c.X != nullptr ? c.X + (T & 1) * (c.plane() / sizeof(__half)) : nullptr;
     }
     return align_up(ws.used, kAlign);
 }
 
-// ---------------------------------------------------------------- one class's problems
-struct Maps {   // tensor maps of one plane, by box
-    CUtensorMap k, mn;
-};
-bool make_maps(Maps& m, const __half* p, int rows, int cols, int count) {
-    return encode_stack_tmap(&m.k, p, rows, cols, count, 128) && encode_stack_tmap(&m.mn, p, rows, cols, count, 64);
+// ---------------------------------------------------------------- chains
+// Description of a class for the kernel, and of its operations.
+bool chain_class(ChainClass& o, const StackClass& c) {
+    std::memset(&o, 0, sizeof(o));
+    o.info = c.info;
+    o.done = c.done;
+    o.rp = c.rp;
+    o.cp = c.cp;
+    o.r8 = c.r8;
+    o.rows = c.rows;
+    o.count = c.count;
+    const long long pl = static_cast<long long>(c.rp) * c.cp, sq = static_cast<long long>(c.r8) * c.r8;
+    o.plane[kPlaneX] = {c.X, pl, c.cp};
+    o.plane[kPlaneL] = {c.L, pl, c.cp};
+    o.plane[kPlaneA] = {c.A, sq, c.r8};
+    o.plane[kPlaneB] = {c.B, sq, c.r8};
+    o.plane[kPlaneOut] = {c.last, pl, c.cp};
+    const int nx = c.x_slots * c.count, na = c.a_slots * c.count;
+    return encode_stack_tmap(&o.map[kMapXk], c.X, c.rp, c.cp, nx, 128) &&
+           encode_stack_tmap(&o.map[kMapXmn], c.X, c.rp, c.cp, nx, 64) &&
+           encode_stack_tmap(&o.map[kMapA], c.A, c.r8, c.r8, na, 128) &&
+           encode_stack_tmap(&o.map[kMapB], c.B, c.r8, c.r8, na, 128);
 }
 
-void planes_out(StackProb& P, void* hi, void* lo, int ld, long long stride, int m_out) {
-    P.out[0] = hi;
-    P.out[1] = lo;
-    P.o_ld = ld;
-    P.o_stride = stride;
-    P.m_out = m_out;
+ChainOp new_op(int cls, int kind) {
+    ChainOp o;
+    std::memset(&o, 0, sizeof(o));
+    o.cls = static_cast<uint8_t>(cls);
+    o.kind = static_cast<uint8_t>(kind);
+    o.e[0] = o.e[1] = o.o[0] = o.o[1] = kPlaneNone;
+    return o;
 }
-void planes_in(StackProb& P, const __half* hi, const __half* lo, int ld, long long stride) {
-    P.E[0] = hi;
-    P.E[1] = lo;
-    P.e_ld = ld;
-    P.e_stride = stride;
+void op_e(ChainOp& o, int i, int plane, int slot) {
+    o.e[i] = static_cast<uint8_t>(plane);
+    o.es[i] = static_cast<uint8_t>(slot);
 }
-
-// Sets A x B of one segment: X-like (rows x cols) and symmetric (r x r) factors.
-struct Seg {
-    const Maps* x;
-    const Maps* y;
+void op_out(ChainOp& o, int i, int plane, int slot) {
+    o.o[i] = static_cast<uint8_t>(plane);
+    o.os[i] = static_cast<uint8_t>(slot);
+}
+void op_seg(ChainOp& o, int ma, int sa, int mb, int sb) {
+    o.ma[o.nseg] = static_cast<uint8_t>(ma);
+    o.sa[o.nseg] = static_cast<uint8_t>(sa);
+    o.mb[o.nseg] = static_cast<uint8_t>(mb);
+    o.sb[o.nseg] = static_cast<uint8_t>(sb);
+    ++o.nseg;
+}
+struct Map2 {
+    int k, mn, slot;    // maps of a plane by box, and the slot
 };
 // r x r product of two rows x cols planes over the long side: X Y^T (wide) or X^T Y (tall).
-void gram_segs(StackProb& P, const StackClass& c, std::initializer_list<Seg> segs) {
-    P.nseg = 0;
-    for (const Seg& s : segs) {
-        P.tmA[P.nseg] = c.tall ? s.x->mn : s.x->k;
-        P.tmB[P.nseg] = c.tall ? s.y->mn : s.y->k;
-        ++P.nseg;
-    }
-    P.M = P.N = c.r8;
-    P.K = c.tall ? c.rp : c.cp;
-    P.flags = kStackSym | (c.tall ? kStackAMn | kStackBMn : 0u);
+void gram_seg(ChainOp& o, const StackClass& c, Map2 x, Map2 y) {
+    op_seg(o, c.tall ? x.mn : x.k, x.slot, c.tall ? y.mn : y.k, y.slot);
+    o.flags = kStackSym | (c.tall ? kStackAMn | kStackBMn : 0u);
 }
 // r x r product of two symmetric matrices (both read along their rows).
-void square_segs(StackProb& P, const StackClass& c, std::initializer_list<Seg> segs) {
-    P.nseg = 0;
-    for (const Seg& s : segs) {
-        P.tmA[P.nseg] = s.x->k;
-        P.tmB[P.nseg] = s.y->k;
-        ++P.nseg;
-    }
-    P.M = P.N = P.K = c.r8;
-    P.flags = kStackSym;
+void square_seg(ChainOp& o, int mx, int sx, int my, int sy) {
+    op_seg(o, mx, sx, my, sy);
+    o.flags = kStackSym;
 }
-// Symmetric x plane (wide) or plane x symmetric (tall), rows x cols.  A pair of CTAs sweeps the tiles
-// that share its block of the plane, so the symmetric factor stays in L2.
-void apply_segs(StackProb& P, const StackClass& c, std::initializer_list<Seg> segs) {
-    P.nseg = 0;
-    for (const Seg& s : segs) {   // s.x symmetric, s.y the plane
-        P.tmA[P.nseg] = c.tall ? s.y->k : s.x->k;
-        P.tmB[P.nseg] = c.tall ? s.x->k : s.y->mn;
-        ++P.nseg;
-    }
-    P.M = c.rp;
-    P.N = c.cp;
-    P.K = c.r8;
-    P.flags = c.tall ? kStackRowMajor : kStackBMn;
+// Symmetric x plane (wide) or plane x symmetric (tall).  Neighbouring tiles share a block of the plane, so that
+// the symmetric factor stays in L2.
+void apply_seg(ChainOp& o, const StackClass& c, int ms, int ss, Map2 x) {
+    if (c.tall) op_seg(o, x.k, x.slot, ms, ss);
+    else op_seg(o, ms, ss, x.mn, x.slot);
+    o.flags = c.tall ? kStackRowMajor : kStackBMn;
 }
 
 struct Call {
@@ -381,11 +387,25 @@ struct Call {
     int sms = 148;
 };
 
-muon_status launch_gemm(std::vector<StackProb>& probs, const std::vector<int>& counts, double flops, const Call& call) {
-    const cudaError_t e = launch_timed(MUON_KERNEL_NS_GEMM, flops, call.stream, [&](cudaStream_t st) {
-        return stack_gemm_launch(probs.data(), counts.data(), static_cast<int>(probs.size()), call.status, call.sms, st);
-    });
-    return e == cudaSuccess ? MUON_OK : cuda_error(e, "stack GEMM launch");
+// Launches a chain: whole iterations (of `per` operations) at a time, as many as a launch's parameters hold.
+muon_status launch_chain(const std::vector<ChainClass>& classes, std::vector<ChainOp>& ops, int per, double flops, int* tickets,
+                         const Call& call) {
+    // a block's operation starts when all earlier ones of the block are done
+    std::vector<int> done(classes.size(), 0);
+    for (ChainOp& o : ops) {
+        o.need = done[o.cls];
+        done[o.cls] += chain_tiles(classes[o.cls], o) * kChainWarps;
+    }
+    const int all = static_cast<int>(ops.size()), step = std::max(1, kChainMaxOps / per) * per;
+    for (int i = 0, k = 0; i < all; i += step, ++k) {
+        const int n = std::min(step, all - i);
+        const cudaError_t e = launch_timed(MUON_KERNEL_NS_GEMM, flops * n / all, call.stream, [&](cudaStream_t st) {
+            return stack_chain_launch(classes.data(), static_cast<int>(classes.size()), ops.data() + i, n, tickets + k,
+                                      call.status, call.sms, st);
+        });
+        if (e != cudaSuccess) return cuda_error(e, "stack chain launch");
+    }
+    return MUON_OK;
 }
 muon_status launch_small(const std::vector<SmallStackItem>& items, const SmallStackClass& k, double flops, const Call& call) {
     const cudaError_t e = launch_timed(MUON_KERNEL_NS_GEMM, flops, call.stream, [&](cudaStream_t st) {
@@ -426,80 +446,70 @@ struct Direct {
     int ld = 0, dtype = 0;
     long long stride = 0;
 };
-muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vector<Direct>& direct, const Call& call) {
+muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vector<Direct>& direct, int* tickets,
+                           const Call& call) {
     const int T = sch.n_iters;
     const std::vector<int> order = class_order(g);
-    std::vector<std::vector<Maps>> mx(g.classes.size()), ma(g.classes.size()), mb(g.classes.size());
-    for (size_t k = 0; k < g.classes.size(); ++k) {
-        StackClass& c = g.classes[k];
-        mx[k].resize(T);
-        ma[k].resize(T);
-        mb[k].resize(T);
-        for (int t = 0; t < T; ++t) {
-            bool ok = true;
-            if (t >= 2 && c.X[t] == c.X[t - 2]) mx[k][t] = mx[k][t - 2];
-            else ok = make_maps(mx[k][t], c.X[t], c.rp, c.cp, c.count);
-            if (t >= 1 && c.A[t] == c.A[0]) {
-                ma[k][t] = ma[k][0];
-                mb[k][t] = mb[k][0];
-            } else {
-                ok = ok && make_maps(ma[k][t], c.A[t], c.r8, c.r8, c.count) &&
-                     make_maps(mb[k][t], c.B[t], c.r8, c.r8, c.count);
-            }
-            if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
-        }
+    std::vector<ChainClass> classes(g.classes.size());
+    for (size_t k = 0; k < classes.size(); ++k) {
+        if (!chain_class(classes[k], g.classes[k]))
+            return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        if (direct[k].p != nullptr)
+            classes[k].plane[kPlaneOut] = {static_cast<__half*>(direct[k].p), direct[k].stride, direct[k].ld};
+        else
+            classes[k].rows = g.classes[k].rp;
     }
+    std::vector<ChainOp> ops;
+    double flops = 0.0;
     for (int t = 0; t < T; ++t) {
         const double cc = sch.coeffs[3 * t + 2];
         for (int stage = 0; stage < 3; ++stage) {
-            std::vector<StackProb> probs;
-            std::vector<int> counts;
-            double flops = 0.0;
             for (int k : order) {
-                StackClass& c = g.classes[k];
+                const StackClass& c = g.classes[k];
                 const double a = c.a[t], b = c.b[t];
-                const long long sq = static_cast<long long>(c.r8) * c.r8, pl = static_cast<long long>(c.rp) * c.cp;
-                StackProb P;
-                std::memset(&P, 0, sizeof(P));
+                const int xs = t % c.x_slots, as = t % c.a_slots;
+                const Map2 x = {kMapXk, kMapXmn, xs};
+                ChainOp o = new_op(k, stage);
                 if (stage == 0) {
-                    gram_segs(P, c, {{&mx[k][t], &mx[k][t]}});
-                    planes_out(P, c.A[t], nullptr, c.r8, sq, c.r8);
-                    P.alpha = static_cast<float>(t == 0 ? c.alpha[0] : c.alpha[t] / (c.tau[t] * c.tau[t]));
-                    P.diag = static_cast<float>(c.alpha[t] * c.shift[t]);
-                    if (t == 0) { P.dscale = c.info; P.scale_pow = 2; }
+                    gram_seg(o, c, x, x);
+                    op_out(o, 0, kPlaneA, as);
+                    o.alpha = static_cast<float>(t == 0 ? c.alpha[0] : c.alpha[t] / (c.tau[t] * c.tau[t]));
+                    o.diag = static_cast<float>(c.alpha[t] * c.shift[t]);
+                    o.pow = t == 0 ? 2 : 0;
                     flops += static_cast<double>(c.count) * c.r * c.r * c.s;
                 } else if (stage == 1) {
-                    square_segs(P, c, {{&ma[k][t], &ma[k][t]}});
-                    planes_in(P, c.A[t], nullptr, c.r8, sq);
-                    planes_out(P, c.B[t], nullptr, c.r8, sq, c.r8);
-                    P.alpha = static_cast<float>(cc * c.gamma[t] / (c.alpha[t] * c.alpha[t]));
-                    P.beta = static_cast<float>(b * c.gamma[t] / c.alpha[t]);
+                    square_seg(o, kMapA, as, kMapA, as);
+                    op_e(o, 0, kPlaneA, as);
+                    op_out(o, 0, kPlaneB, as);
+                    o.alpha = static_cast<float>(cc * c.gamma[t] / (c.alpha[t] * c.alpha[t]));
+                    o.beta = static_cast<float>(b * c.gamma[t] / c.alpha[t]);
                     flops += static_cast<double>(c.count) * c.r * c.r * c.r;
                 } else {
-                    apply_segs(P, c, {{&mb[k][t], &mx[k][t]}});
-                    planes_in(P, c.X[t], c.L[t & 1], c.cp, pl);
+                    apply_seg(o, c, kMapB, as, x);
+                    op_e(o, 0, kPlaneX, xs);
+                    op_e(o, 1, kPlaneL, t & 1);
                     double up = c.tau[t + 1];
-                    if (t + 1 == T && direct[k].p != nullptr) {
-                        planes_out(P, direct[k].p, nullptr, direct[k].ld, direct[k].stride, c.rows);
-                        if (direct[k].dtype == MUON_BF16) P.flags |= kStackOutBf16;
-                        up = 1.0;
+                    if (t + 1 == T) {
+                        op_out(o, 0, kPlaneOut, 0);
+                        if (direct[k].p != nullptr) {
+                            if (direct[k].dtype == MUON_BF16) o.flags |= kStackOutBf16;
+                            up = 1.0;
+                        }
                     } else {
-                        planes_out(P, c.X[t + 1], t + 1 < T ? c.L[(t + 1) & 1] : nullptr, c.cp, pl, c.rp);
+                        op_out(o, 0, kPlaneX, (t + 1) % c.x_slots);
+                        op_out(o, 1, kPlaneL, (t + 1) & 1);
                     }
                     const double down = t == 0 ? 1.0 : c.tau[t];
-                    P.alpha = static_cast<float>(up / (c.gamma[t] * down));
-                    P.beta = static_cast<float>(a * up / down);
-                    if (t == 0) { P.dscale = c.info; P.scale_pow = 1; }
+                    o.alpha = static_cast<float>(up / (c.gamma[t] * down));
+                    o.beta = static_cast<float>(a * up / down);
+                    o.pow = t == 0 ? 1 : 0;
                     flops += 2.0 * c.count * c.r * c.r * c.s;
                 }
-                probs.push_back(P);
-                counts.push_back(c.count);
+                ops.push_back(o);
             }
-            const muon_status st = launch_gemm(probs, counts, flops, call);
-            if (st != MUON_OK) return st;
         }
     }
-    return MUON_OK;
+    return launch_chain(classes, ops, 3 * static_cast<int>(classes.size()), flops, tickets, call);
 }
 
 // ---------------------------------------------------------------- arguments
@@ -587,23 +597,27 @@ size_t forward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& s
     return kHeaderBytes + most;
 }
 
-// Planes of the reverse pass of a group.
+// Planes of the reverse pass of a group: D_t and its second plane in slot t & 1.
 struct GradPlanes {
-    __half* D[2][2];     // [ping/pong][plane]
+    __half* D;
+    __half* DL;
     __half* S;
     __half* P;
     float* info;
     double* partials;
+    int* done;
 };
 std::vector<GradPlanes> layout_backward(const Group& g, Arena& ws) {
     std::vector<GradPlanes> out;
+    auto take = [&](size_t bytes) { return ws.at(ws.take(bytes)); };
+    take(kStackTickets * sizeof(int));
     for (const StackClass& c : g.classes) {
         GradPlanes p;
-        auto take = [&](size_t bytes) { return ws.at(ws.take(bytes)); };
         p.info = static_cast<float*>(take(static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
         p.partials = static_cast<double*>(take(static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
-        for (auto& b : p.D)
-            for (auto& x : b) x = static_cast<__half*>(take(c.plane()));
+        p.done = static_cast<int*>(take(static_cast<size_t>(c.count) * sizeof(int)));
+        p.D = static_cast<__half*>(take(2 * c.plane()));
+        p.DL = static_cast<__half*>(take(2 * c.plane()));
         p.S = static_cast<__half*>(take(c.square()));
         p.P = static_cast<__half*>(take(c.square()));
         out.push_back(p);
@@ -631,6 +645,8 @@ StackItem base_item(const StackClass& c, const Part& p) {
     it.partials = c.partials + static_cast<size_t>(p.at) * c.chunks;
     return it;
 }
+// The chain's counters are the first thing in the workspace after the status word.
+int* tickets_at(void* workspace) { return reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + kHeaderBytes); }
 size_t plane_at(const StackClass& c, const Part& p) { return static_cast<size_t>(p.at) * c.rp * c.cp; }
 
 const uint8_t* bytes_at(const void* p, long long blocks, long long stride, int dtype) {
@@ -696,8 +712,9 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
             it.g_ld = s.x_ld;
             it.g_dtype = s.x_dtype;
             it.vec = vec_ok(it.G, s.x_dtype, s.x_ld, s.x_stride) ? 1 : 0;
-            it.hi = c.X[0] + plane_at(c, p);
-            it.lo = c.L[0] + plane_at(c, p);
+            it.hi = c.X + plane_at(c, p);
+            it.lo = c.L + plane_at(c, p);
+            it.done = c.done + p.at;
             in.push_back(it);
             read += n * elem_size(s.x_dtype);
             StackItem o = base_item(c, p);
@@ -706,7 +723,7 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
             o.w_ld = s.y_ld;
             o.w_dtype = s.y_dtype;
             o.vec = vec_ok(o.W, s.y_dtype, s.y_ld, s.y_stride) ? 4 : 0;
-            o.hi = c.X[T] + plane_at(c, p);
+            o.hi = c.last + plane_at(c, p);
             o.step = static_cast<float>(1.0 / c.tau[T]);
             // The last product writes a 16-bit result where it belongs, if one stack is the whole class
             // and its rows are whole 16-byte pieces.
@@ -720,12 +737,13 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
         StackPassArgs args = {};
         args.eps = sch.eps;
         args.status = first ? call.status : nullptr;
+        args.tickets = tickets_at(workspace);
         muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_SCALE, read, call);
         if (st != MUON_OK) return st;
         args.status = call.status;
         st = launch_pass(StackPass::kPack, in, args, MUON_KERNEL_MOMENTUM, 2 * read, call);
         if (st != MUON_OK) return st;
-        st = run_iterations(g, sch, direct, call);
+        st = run_iterations(g, sch, direct, args.tickets, call);
         if (st != MUON_OK) return st;
         if (!out.empty()) {
             st = launch_pass(StackPass::kOut, out, args, MUON_KERNEL_MISC, 2 * written, call);
@@ -788,15 +806,17 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             it.g_ld = s.x_ld;
             it.g_dtype = s.x_dtype;
             it.vec = vec_ok(it.G, s.x_dtype, s.x_ld, s.x_stride) ? 1 : 0;
-            it.hi = q.D[T & 1][0] + plane_at(c, p);
-            it.lo = q.D[T & 1][1] + plane_at(c, p);
+            const size_t slot = c.plane() / sizeof(__half);
+            it.hi = q.D + (T & 1) * slot + plane_at(c, p);
+            it.lo = q.DL + (T & 1) * slot + plane_at(c, p);
+            it.done = q.done + p.at;
             it.step = static_cast<float>(delta[p.cls][T]);
             in.push_back(it);
             read += static_cast<double>(p.count) * c.rows * c.cols * elem_size(s.x_dtype);
             o.ginfo = it.info;
-            o.hi = q.D[0][0] + plane_at(c, p);
-            o.lo = q.D[0][1] + plane_at(c, p);
-            o.hi2 = c.X[0] + plane_at(c, p);
+            o.hi = q.D + plane_at(c, p);
+            o.lo = q.DL + plane_at(c, p);
+            o.hi2 = c.X + plane_at(c, p);
             o.W = const_cast<uint8_t*>(bytes_at(s.Y, p.first, s.y_stride, s.y_dtype));
             o.w_stride = s.y_stride;
             o.w_ld = s.y_ld;
@@ -808,71 +828,74 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
         StackPassArgs args = {};
         args.eps = sch.eps;
         args.status = first ? call.status : nullptr;
+        args.tickets = tickets_at(workspace);
         muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_SCALE, read, call);
         if (st != MUON_OK) return st;
         args.status = call.status;
         st = launch_pass(StackPass::kPackGrad, in, args, MUON_KERNEL_MOMENTUM, 2 * read, call);
         if (st != MUON_OK) return st;
 
-        std::vector<std::vector<Maps>> mx(nc), ma(nc), mb(nc);
-        std::vector<Maps> md[2] = {std::vector<Maps>(nc), std::vector<Maps>(nc)}, ms(nc), mp(nc);
+        std::vector<ChainClass> classes(nc);
         for (size_t k = 0; k < nc; ++k) {
             const StackClass& c = g.classes[k];
-            mx[k].resize(T);
-            ma[k].resize(T);
-            mb[k].resize(T);
-            bool ok = make_maps(ms[k], gp[k].S, c.r8, c.r8, c.count) && make_maps(mp[k], gp[k].P, c.r8, c.r8, c.count) &&
-                      make_maps(md[0][k], gp[k].D[0][0], c.rp, c.cp, c.count) &&
-                      make_maps(md[1][k], gp[k].D[1][0], c.rp, c.cp, c.count);
-            for (int t = 0; t < T && ok; ++t)
-                ok = make_maps(mx[k][t], c.X[t], c.rp, c.cp, c.count) && make_maps(ma[k][t], c.A[t], c.r8, c.r8, c.count) &&
-                     make_maps(mb[k][t], c.B[t], c.r8, c.r8, c.count);
+            const GradPlanes& q = gp[k];
+            ChainClass& o = classes[k];
+            const long long pl = static_cast<long long>(c.rp) * c.cp, sq = static_cast<long long>(c.r8) * c.r8;
+            const bool ok = chain_class(o, c) && encode_stack_tmap(&o.map[kMapDk], q.D, c.rp, c.cp, 2 * c.count, 128) &&
+                            encode_stack_tmap(&o.map[kMapDmn], q.D, c.rp, c.cp, 2 * c.count, 64) &&
+                            encode_stack_tmap(&o.map[kMapS], q.S, c.r8, c.r8, c.count, 128) &&
+                            encode_stack_tmap(&o.map[kMapP], q.P, c.r8, c.r8, c.count, 128);
             if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+            o.done = q.done;
+            o.plane[kPlaneD] = {q.D, pl, c.cp};
+            o.plane[kPlaneDL] = {q.DL, pl, c.cp};
+            o.plane[kPlaneS] = {q.S, sq, c.r8};
+            o.plane[kPlaneP] = {q.P, sq, c.r8};
         }
+        std::vector<ChainOp> ops;
+        double flops = 0.0;
         for (int t = T - 1; t >= 0; --t) {
             const double cc = sch.coeffs[3 * t + 2];
-            const int cur = (t + 1) & 1, nxt = t & 1;
+            const Map2 x = {kMapXk, kMapXmn, t}, dd = {kMapDk, kMapDmn, (t + 1) & 1};
             for (int stage = 0; stage < 3; ++stage) {
-                std::vector<StackProb> probs;
-                std::vector<int> counts;
-                double flops = 0.0;
                 for (int k : order) {
                     const StackClass& c = g.classes[k];
-                    const GradPlanes& q = gp[k];
                     const double a = c.a[t], b = c.b[t];
-                    const long long sq = static_cast<long long>(c.r8) * c.r8, pl = static_cast<long long>(c.rp) * c.cp;
-                    const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t];   // t = 0: f0 comes as dscale
-                    StackProb P;
-                    std::memset(&P, 0, sizeof(P));
+                    const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t];   // t = 0: f0 comes from info
+                    ChainOp o = new_op(k, stage);
                     if (stage == 0) {          // S = (D X^T + X D^T) / 2
-                        gram_segs(P, c, {{&md[cur][k], &mx[k][t]}, {&mx[k][t], &md[cur][k]}});
-                        planes_out(P, q.S, nullptr, c.r8, sq, c.r8);
-                        P.alpha = static_cast<float>(0.5 * inv_tau);
+                        gram_seg(o, c, dd, x);
+                        gram_seg(o, c, x, dd);
+                        op_out(o, 0, kPlaneS, 0);
+                        o.alpha = static_cast<float>(0.5 * inv_tau);
                         flops += 2.0 * c.count * c.r * c.r * c.s;
                     } else if (stage == 1) {   // P * 2 gamma / tau, P = bS + c(SA + AS)
-                        square_segs(P, c, {{&ms[k], &ma[k][t]}, {&ma[k][t], &ms[k]}});
-                        planes_in(P, q.S, nullptr, c.r8, sq);
-                        planes_out(P, q.P, nullptr, c.r8, sq, c.r8);
-                        P.alpha = static_cast<float>(cc * 2.0 * c.gamma[t] * inv_tau / c.alpha[t]);
-                        P.beta = static_cast<float>(b * 2.0 * c.gamma[t] * inv_tau);
+                        square_seg(o, kMapS, 0, kMapA, t);
+                        square_seg(o, kMapA, t, kMapS, 0);
+                        op_e(o, 0, kPlaneS, 0);
+                        op_out(o, 0, kPlaneP, 0);
+                        o.alpha = static_cast<float>(cc * 2.0 * c.gamma[t] * inv_tau / c.alpha[t]);
+                        o.beta = static_cast<float>(b * 2.0 * c.gamma[t] * inv_tau);
                         flops += 2.0 * c.count * c.r * c.r * c.r;
                     } else {                   // D' = aD + BD + 2PX
-                        apply_segs(P, c, {{&mb[k][t], &md[cur][k]}, {&mp[k], &mx[k][t]}});
-                        planes_in(P, q.D[cur][0], q.D[cur][1], c.cp, pl);
-                        planes_out(P, q.D[nxt][0], q.D[nxt][1], c.cp, pl, c.rp);
+                        apply_seg(o, c, kMapB, t, dd);
+                        apply_seg(o, c, kMapP, 0, x);
+                        op_e(o, 0, kPlaneD, (t + 1) & 1);
+                        op_e(o, 1, kPlaneDL, (t + 1) & 1);
+                        op_out(o, 0, kPlaneD, t & 1);
+                        op_out(o, 1, kPlaneDL, t & 1);
                         const double kappa = delta[k][t] / delta[k][t + 1];
-                        P.alpha = static_cast<float>(kappa / c.gamma[t]);
-                        P.beta = static_cast<float>(kappa * a);
+                        o.alpha = static_cast<float>(kappa / c.gamma[t]);
+                        o.beta = static_cast<float>(kappa * a);
                         flops += 4.0 * c.count * c.r * c.r * c.s;
                     }
-                    if (t == 0 && stage < 2) { P.dscale = c.info; P.scale_pow = 1; }
-                    probs.push_back(P);
-                    counts.push_back(c.count);
+                    if (t == 0 && stage < 2) o.pow = 1;
+                    ops.push_back(o);
                 }
-                st = launch_gemm(probs, counts, flops, call);
-                if (st != MUON_OK) return st;
             }
         }
+        st = launch_chain(classes, ops, 3 * static_cast<int>(nc), flops, args.tickets, call);
+        if (st != MUON_OK) return st;
         dot = out;
         st = launch_pass(StackPass::kDot, dot, args, MUON_KERNEL_SCALE, 0.0, call);
         if (st != MUON_OK) return st;
@@ -943,10 +966,11 @@ muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, std
             it.g_ld = s.g_ld; it.m_ld = s.m_ld; it.w_ld = s.w_ld;
             it.g_dtype = s.g_dtype; it.w_dtype = s.w_dtype;
             it.vec = step_vec(s);   // a later first block keeps it: its offset is a multiple of the stride
-            it.hi = c.X[0] + plane_at(c, p);
-            it.lo = c.L[0] + plane_at(c, p);
+            it.hi = c.X + plane_at(c, p);
+            it.lo = c.L + plane_at(c, p);
+            it.done = c.done + p.at;
             in.push_back(it);
-            it.hi = c.X[T] + plane_at(c, p);
+            it.hi = c.last + plane_at(c, p);
             it.decay = static_cast<float>(1.0 - static_cast<double>(hp.lr) * hp.weight_decay);
             it.step = static_cast<float>(-static_cast<double>(hp.lr) * shape_scale(c.rows, c.cols, hp.scale_mode) / c.tau[T]);
             out.push_back(it);
@@ -961,12 +985,13 @@ muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, std
         args.nesterov = hp.nesterov;
         args.gscale = grad_scale;
         args.status = first ? call.status : nullptr;
+        args.tickets = tickets_at(workspace);
         muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_MOMENTUM, norm_bytes, call);
         if (st != MUON_OK) return st;
         args.status = call.status;
         st = launch_pass(StackPass::kPack, in, args, MUON_KERNEL_MISC, pack_bytes, call);
         if (st != MUON_OK) return st;
-        st = run_iterations(g, hp.ns, std::vector<Direct>(g.classes.size()), call);
+        st = run_iterations(g, hp.ns, std::vector<Direct>(g.classes.size()), args.tickets, call);
         if (st != MUON_OK) return st;
         st = launch_pass(StackPass::kUpdate, out, args, MUON_KERNEL_UPDATE, upd_bytes, call);
         if (st != MUON_OK) return st;
