@@ -24,7 +24,7 @@
 // Two CTAs of a cluster compute one 256 x 256 tile with tcgen05.mma.cta_group::2 (K = 16 a step):
 // each stages its 128 rows of A and 128 columns of B, so an SM reads half the B bytes that a
 // one-SM tile would.  Roles per CTA (384 threads): warp 0 lane 0 TMA producer, warp 1 lane 0 of the
-// leader MMA issuer, warp 2 TMEM, warp 3 lane 0 of the leader draws tiles (one ahead), warps 4..11
+// leader MMA issuer, warp 2 TMEM, warp 3 lane 0 of the leader draws tiles and waits until they may start (one ahead), warps 4..11
 // epilogue (TMEM double buffered, so the epilogue of one tile overlaps the products of the next).
 // Global accesses of the epilogue are turned through shared memory into 8 rows x 64 bytes per
 // instruction, E arrives there a chunk ahead.  Every wait is bounded (ptx_sm100.cuh); no load uses
@@ -229,10 +229,19 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
     if (warp == 3 && lane == 0 && rank == 0) {
         // ------------------------------------------------------------ draws tiles
         const uint32_t peer_slot = mapa_shared(smem_u32(draw_slot), 1), peer_full = mapa_shared(smem_u32(dfull_bar), 1);
+        int op = 0;
         for (int i = 0;; ++i) {
             const int k = i & 1;
             int t = atomicAdd(g.ticket, 1);
-            if (t >= g.tiles) t = -1;
+            if (t >= g.tiles) {
+                t = -1;
+            } else {
+                // Waiting here, a tile ahead, keeps the readers' pipelines full; what the earlier operations
+                // wrote becomes visible to them with the number.
+                const Tile ti = tile_at(g, t, op);
+                if (!wait_done(g.cls[g.op[op].cls].done + ti.b, g.op[op].need, abort_flag, dev_status)) t = -1;
+                fence_proxy_global();
+            }
             if (!mbar_wait_cluster(&dempty_bar[k], ((i >> 1) & 1) ^ 1u, abort_flag, dev_status)) break;
             *reinterpret_cast<volatile int*>(&draw_slot[k]) = t;
             asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_slot + 4u * k), "r"(t) : "memory");
@@ -252,8 +261,6 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const Tile ti = tile_at(g, t, op);
             const ChainOp& P = g.op[op];
             const ChainClass& c = g.cls[P.cls];
-            if (!wait_done(c.done + ti.b, P.need, abort_flag, dev_status)) { ok = false; break; }
-            fence_proxy_global();
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
             const int am0 = ti.m0 + HM * static_cast<int>(rank);
@@ -369,9 +376,6 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const Tile ti = tile_at(g, t, op);
             const ChainOp& P = g.op[op];
             const ChainClass& cl = g.cls[P.cls];
-            int ready = 0;
-            if (lane == 0) ready = wait_done(cl.done + ti.b, P.need, abort_flag, dev_status);
-            if (!__shfl_sync(0xffffffffu, ready, 0)) break;
             float f = 1.0f;
             if (P.pow != 0) {
                 const float x = cl.info[static_cast<size_t>(ti.b) * kStackInfo];
