@@ -21,8 +21,9 @@
 // wave of every operation: 24 blocks of 509 x 1021 are 72 + 72 + 192 tiles an iteration on 74 pairs, 1 + 1 + 3
 // waves with gaps between them before, 4.5 without now.
 //
-// Two CTAs of a cluster compute one 256 x 256 tile with tcgen05.mma.cta_group::2 (K = 16 a step):
-// each stages its 128 rows of A and 128 columns of B, so an SM reads half the B bytes that a
+// Two CTAs of a cluster compute one tile of 256 x 256 (128 or 64 columns where that many tiles would leave
+// pairs idle) with tcgen05.mma.cta_group::2 (K = 16 a step):
+// each stages its 128 rows of A and half the columns of B, so an SM reads half the B bytes that a
 // one-SM tile would.  Roles per CTA (384 threads): warp 0 lane 0 TMA producer, warp 1 lane 0 of the
 // leader MMA issuer, warp 2 TMEM, warp 3 lane 0 of the leader draws tiles and waits until they may start (one ahead), warps 4..11
 // epilogue (TMEM double buffered, so the epilogue of one tile overlaps the products of the next).
@@ -44,7 +45,6 @@ constexpr int BM = 256, BN = 256, BK = 64, STAGES = 4;
 constexpr int HM = BM / 2, HN = BN / 2;
 constexpr int A_BYTES = HM * BK * 2, B_BYTES = HN * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
 constexpr int MN_CHUNK_BYTES = 64 * BK * 2;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int BAR_BYTES = 256;
@@ -67,6 +67,7 @@ struct ChainParams {
 
 struct Tile {
     int b, m0, n0, M, N, K;
+    int w;                 // columns of the tile
 };
 // Moves `op` on to the operation of tile t (tiles come in rising order) and gives the tile's place
 // (symmetric operations list the tiles with mb <= nb, column by column).
@@ -76,20 +77,25 @@ __device__ __forceinline__ Tile tile_at(const P& g, int t, int& op) {
     const ChainOp& o = g.op[op];
     const ChainClass& c = g.cls[o.cls];
     Tile r;
-    const int nr = (c.r8 + BM - 1) / BM;
-    const int mbs = o.kind < 2 ? nr : (c.rp + BM - 1) / BM, nbs = o.kind < 2 ? nr : (c.cp + BN - 1) / BN;
+    const int w = 64 * o.bn;
     r.M = o.kind < 2 ? c.r8 : c.rp;
     r.N = o.kind < 2 ? c.r8 : c.cp;
     r.K = o.kind == 0 ? max(c.rp, c.cp) : c.r8;
+    r.w = w;
+    const int mbs = (r.M + BM - 1) / BM, nbs = (r.N + w - 1) / w;
     const int per = chain_tiles(c, o), i = t - o.tile0;
     r.b = i / per;
-    const int l = i - r.b * per;
-    int mb, nb;
+    int l = i - r.b * per, mb, nb;
     if (o.flags & kStackSym) {
-        nb = static_cast<int>((sqrtf(8.f * l + 1.f) - 1.f) * 0.5f);
-        while (nb * (nb + 1) / 2 > l) --nb;
-        while ((nb + 1) * (nb + 2) / 2 <= l) ++nb;
-        mb = l - nb * (nb + 1) / 2;
+        // column groups of 256: group g has 4 / bn columns of g + 1 tiles
+        const int cols = 4 / o.bn, u = l / cols;
+        int gcol = static_cast<int>((sqrtf(8.f * u + 1.f) - 1.f) * 0.5f);
+        while (cols * (gcol * (gcol + 1) / 2) > l) --gcol;
+        while (cols * ((gcol + 1) * (gcol + 2) / 2) <= l) ++gcol;
+        l -= cols * (gcol * (gcol + 1) / 2);
+        const int k = l / (gcol + 1);
+        mb = l - k * (gcol + 1);
+        nb = gcol * cols + k;
     } else if (o.flags & kStackRowMajor) {
         mb = l / nbs;
         nb = l - mb * nbs;
@@ -98,7 +104,7 @@ __device__ __forceinline__ Tile tile_at(const P& g, int t, int& op) {
         mb = l - nb * mbs;
     }
     r.m0 = mb * BM;
-    r.n0 = nb * BN;
+    r.n0 = nb * w;
     return r;
 }
 
@@ -264,7 +270,10 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
             const int am0 = ti.m0 + HM * static_cast<int>(rank);
-            const int bn0 = ti.n0 + HN * static_cast<int>(rank);
+            const int hn = ti.w / 2;                      // columns of B that this CTA uses: 128, 64 or 32
+            const int bn0 = ti.n0 + hn * static_cast<int>(rank);
+            // a K-major box has 128 rows whatever the tile takes; MN-major ones come 64 columns at a time
+            const int b_chunks = (hn + 63) / 64, b_bytes = b_mn ? b_chunks * MN_CHUNK_BYTES : B_BYTES;
             const int kblocks = (ti.K + BK - 1) / BK;
             for (int seg = 0; seg < P.nseg && ok; ++seg) {
                 const CUtensorMap* ta = &c.map[P.ma[seg]];
@@ -277,7 +286,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                     const int k0 = kb * BK;
                     const uint32_t fb = full_leader + stage * 8u;
                     if (rank == 0) {
-                        mbar_arrive_expect_tx(&full_bar[stage], PAIR_STAGE_BYTES);
+                        mbar_arrive_expect_tx(&full_bar[stage], 2u * static_cast<uint32_t>(A_BYTES + b_bytes));
                         issued_parity[stage] = static_cast<int>(phase);
                     }
                     if (!a_mn) {
@@ -290,8 +299,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                     if (!b_mn) {
                         tma_load_3d_pair(sb, tb, fb, k0, bn0, zb);
                     } else {
-#pragma unroll
-                        for (int h = 0; h < HN / 64; ++h)
+                        for (int h = 0; h < b_chunks; ++h)
                             tma_load_3d_pair(sb + h * MN_CHUNK_BYTES, tb, fb, bn0 + 64 * h, k0, zb);
                     }
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -320,7 +328,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const ChainOp& P = g.op[op];
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
-            const uint32_t idesc = idesc_f16_f32(BM, BN, a_mn, b_mn);
+            const uint32_t idesc = idesc_f16_f32(BM, ti.w, a_mn, b_mn);
             const int kblocks = (ti.K + BK - 1) / BK * P.nseg;
             if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag, dev_status)) { ok = false; break; }
             tc_fence_after();
@@ -360,8 +368,6 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
         // ------------------------------------------------------------ epilogue
         // warp & 3 selects the TMEM lane quarter (rows), (warp - 4) >> 2 the half of the columns.
         const int q = warp & 3;
-        const int c_beg = ((warp - 4) >> 2) * (BN / 64);
-        const int c_end = c_beg + BN / 64;
         uint8_t* stg = smem + STAGES * STAGE_BYTES + BAR_BYTES + (warp - 4) * STG_WARP_BYTES;
         uint8_t* stg_t = stg + STG_BYTES;
         uint8_t* stg_e = stg + 2 * STG_BYTES;          // plane 0 of E: two buffers; plane 1: the next two
@@ -382,6 +388,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 f = P.pow == 1 ? x : x * x;
             }
             const float alpha = P.alpha * f, beta = P.beta * f;
+            const int c_beg = ((warp - 4) >> 2) * (ti.w / 64), c_end = c_beg + ti.w / 64;   // this warp's chunks of 32 columns
             const bool sym = (P.flags & kStackSym) != 0;
             const bool bf = (P.flags & kStackOutBf16) != 0;
             const int row0 = ti.m0 + HM * static_cast<int>(rank) + q * 32;
@@ -461,45 +468,45 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 }
                 __syncwarp();               // slot c & 1 is free for chunk c + 2, stg for the store
                 if (!below) {
-#pragma unroll 1
-                    for (int pl = 0; pl < planes; ++pl) {
+                    // rows -> staging -> 8 rows x 64 bytes per instruction; plane 1 (what plane 0 has lost) beside it
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            uint32_t w[4];
+                    for (int s = 0; s < 4; ++s) {
+                        uint32_t w[4], l[4];
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const float x = v[8 * s + 2 * h], y = v[8 * s + 2 * h + 1];
-                                w[h] = bf ? pack_bf16x2(x, y) : pack_half2(x, y);
-                                if (planes == 2) {   // what plane 0 has lost, for plane 1
-                                    const float2 e = unpack_half2(w[h]);
-                                    v[8 * s + 2 * h] = x - e.x;
-                                    v[8 * s + 2 * h + 1] = y - e.y;
-                                }
-                            }
-                            *reinterpret_cast<uint4*>(stg + stg_off64(lane, s)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int h = 0; h < 4; ++h) {
+                            const float x = v[8 * s + 2 * h], y = v[8 * s + 2 * h + 1];
+                            w[h] = bf ? pack_bf16x2(x, y) : pack_half2(x, y);
+                            const float2 e = unpack_half2(w[h]);
+                            l[h] = pack_half2(x - e.x, y - e.y);
                         }
+                        *reinterpret_cast<uint4*>(stg + stg_off64(lane, s)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (planes == 2) *reinterpret_cast<uint4*>(stg_t + stg_off64(lane, s)) = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = row0 + crow + 8 * i, cc = col0 + 8 * cseg;
+                        if (rr < m_out && cc < ti.N) {
+                            const size_t at = static_cast<size_t>(rr) * o_ld + cc;
+                            *reinterpret_cast<uint4*>(o_plane[0] + at) =     // bf16: the same 2 bytes
+                                *reinterpret_cast<const uint4*>(stg + stg_off64(crow + 8 * i, cseg));
+                            if (planes == 2)
+                                *reinterpret_cast<uint4*>(o_plane[1] + at) =
+                                    *reinterpret_cast<const uint4*>(stg_t + stg_off64(crow + 8 * i, cseg));
+                        }
+                    }
+                    if (mirror) {      // symmetric outputs have one plane
+                        stg_transpose32(stg, stg_t, lane);
                         __syncwarp();
-                        __half* o = o_plane[pl];   // bf16: the same 2 bytes
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int rr = row0 + crow + 8 * i, cc = col0 + 8 * cseg;
-                            const uint4 val = *reinterpret_cast<const uint4*>(stg + stg_off64(crow + 8 * i, cseg));
-                            if (rr < m_out && cc < ti.N)
-                                *reinterpret_cast<uint4*>(o + static_cast<size_t>(rr) * o_ld + cc) = val;
+                            const int rr = col0 + crow + 8 * i, cc = row0 + 8 * cseg;
+                            if (rr < ti.N && cc < ti.M)
+                                *reinterpret_cast<uint4*>(o_plane[0] + static_cast<size_t>(rr) * o_ld + cc) =
+                                    *reinterpret_cast<const uint4*>(stg_t + stg_off64(crow + 8 * i, cseg));
                         }
-                        if (mirror) {
-                            stg_transpose32(stg, stg_t, lane);
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int rr = col0 + crow + 8 * i, cc = row0 + 8 * cseg;
-                                const uint4 val = *reinterpret_cast<const uint4*>(stg_t + stg_off64(crow + 8 * i, cseg));
-                                if (rr < ti.N && cc < ti.M)
-                                    *reinterpret_cast<uint4*>(o + static_cast<size_t>(rr) * o_ld + cc) = val;
-                            }
-                        }
-                        __syncwarp();
                     }
+                    __syncwarp();
                 }
             }
             cp_async_wait_all();

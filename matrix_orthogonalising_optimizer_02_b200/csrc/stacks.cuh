@@ -50,6 +50,7 @@ struct ChainOp {
     int need;              // value of `done` at which a block's operation may start (filled by the caller)
     uint8_t cls, kind;     // kind 0: r8 x r8 over the long side, 1: r8 x r8 over r8, 2: rp x cp over r8
     uint8_t flags, nseg, pow;
+    uint8_t bn;            // tile width / 64: 1, 2 or 4
     uint8_t ma[2], mb[2];  // tensor maps of the segments' operands
     uint8_t sa[2], sb[2];  // and their slots
     uint8_t e[2], es[2];   // planes and slots of E
@@ -62,10 +63,13 @@ constexpr int kChainMaxClasses = 12, kChainMaxOps = 360;
 // box_rows rows of one matrix, 128-byte swizzle, zero fill out of bounds.
 bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows);
 
-// Tiles of one block of an operation.
+// Tiles of one block of an operation: 256 rows x 64 bn columns.  Symmetric ones are those that reach the upper
+// triangle: with 4 / bn tile columns to 256, column nb has nb / (4 / bn) + 1 of them.
 __host__ __device__ inline int chain_tiles(const ChainClass& c, const ChainOp& o) {
-    const int nr = (c.r8 + 255) / 256;
-    return o.kind < 2 ? nr * (nr + 1) / 2 : ((c.rp + 255) / 256) * ((c.cp + 255) / 256);
+    const int w = 64 * o.bn, per = 4 / o.bn;
+    if (o.kind == 2) return ((c.rp + 255) / 256) * ((c.cp + w - 1) / w);
+    const int nbs = (c.r8 + w - 1) / w, whole = nbs / per, rest = nbs - whole * per;
+    return per * whole * (whole + 1) / 2 + rest * (whole + 1);
 }
 // Launches ops[0 .. n) (in order; dependencies point backwards).  `ticket`: an int of the workspace that
 // is zero; `done` counters carry on from earlier launches of the chain.

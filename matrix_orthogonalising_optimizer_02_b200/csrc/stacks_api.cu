@@ -337,11 +337,34 @@ bool chain_class(ChainClass& o, const StackClass& c) {
            encode_stack_tmap(&o.map[kMapB], c.B, c.r8, c.r8, na, 128);
 }
 
-ChainOp new_op(int cls, int kind) {
+// Tile width of an operation (in 64 columns): the one whose time is least in this model, in us measured on a
+// pair of CTAs: a 64-deep step of the product takes 0.41, 0.29, 0.24 at 256, 128, 64 columns, the epilogue 4.4 (one
+// plane) or 7 (two planes in and out) per 256, and a tile's products overlap the epilogue of the one before.
+// 2 blocks of 320 x 257: 256 columns make 6 tiles and 13 us per operation, 64 columns 22 tiles.
+int tile_width(const ChainClass& c, ChainOp o, int segments, int pairs) {
+    const int kind = o.kind, k = ((kind == 0 ? std::max(c.rp, c.cp) : c.r8) + 63) / 64 * segments;
+    const double step[5] = {0.0, 0.24, 0.29, 0.0, 0.41};
+    int best = 4;
+    double least = 1e30;
+    for (int bn : {4, 2, 1}) {
+        o.bn = static_cast<uint8_t>(bn);
+        const double tiles = static_cast<double>(chain_tiles(c, o)) * c.count, waves = std::ceil(tiles / pairs);
+        const double mma = k * step[bn], epi = 0.5 + (kind == 2 ? 7.0 : 4.4) * bn / 4;
+        const double t = (waves - 1) * std::max(mma + 0.5, epi) + mma + epi;
+        if (t < 0.98 * least) {
+            least = t;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+ChainOp new_op(int cls, int kind, const ChainClass& c, int segments, int pairs) {
     ChainOp o;
     std::memset(&o, 0, sizeof(o));
     o.cls = static_cast<uint8_t>(cls);
     o.kind = static_cast<uint8_t>(kind);
+    o.bn = static_cast<uint8_t>(tile_width(c, o, segments, pairs));
     o.e[0] = o.e[1] = o.o[0] = o.o[1] = kPlaneNone;
     return o;
 }
@@ -469,7 +492,7 @@ muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vec
                 const double a = c.a[t], b = c.b[t];
                 const int xs = t % c.x_slots, as = t % c.a_slots;
                 const Map2 x = {kMapXk, kMapXmn, xs};
-                ChainOp o = new_op(k, stage);
+                ChainOp o = new_op(k, stage, classes[k], 1, call.sms / 2);
                 if (stage == 0) {
                     gram_seg(o, c, x, x);
                     op_out(o, 0, kPlaneA, as);
@@ -862,7 +885,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                     const StackClass& c = g.classes[k];
                     const double a = c.a[t], b = c.b[t];
                     const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t];   // t = 0: f0 comes from info
-                    ChainOp o = new_op(k, stage);
+                    ChainOp o = new_op(k, stage, classes[k], 2, call.sms / 2);
                     if (stage == 0) {          // S = (D X^T + X D^T) / 2
                         gram_seg(o, c, dd, x);
                         gram_seg(o, c, x, dd);
