@@ -41,7 +41,7 @@
 namespace muon {
 namespace {
 
-constexpr int BM = 256, BN = 256, BK = 64, STAGES = 4;
+constexpr int BM = 256, BN = 256, BK = 64, STAGES = 5;
 constexpr int HM = BM / 2, HN = BN / 2;
 constexpr int A_BYTES = HM * BK * 2, B_BYTES = HN * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -49,10 +49,10 @@ constexpr int MN_CHUNK_BYTES = 64 * BK * 2;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int BAR_BYTES = 256;
 constexpr int THREADS = 384, EPI_THREADS = 256;
-// Per epilogue warp six 32 x 32 fp16 chunks (64-byte rows): direct store, transposed mirror, and two of
-// each plane of E (the one in use and the one being fetched).
+// Per epilogue warp four 32 x 32 fp16 chunks (64-byte rows): the two planes of the output (or the output and
+// its transposed mirror) and the two of E, which is fetched again as soon as it is in registers.
 constexpr int STG_BYTES = 32 * 64;
-constexpr int STG_WARP_BYTES = 6 * STG_BYTES;
+constexpr int STG_WARP_BYTES = 4 * STG_BYTES;
 constexpr int SMEM_TOTAL = STAGES * STAGE_BYTES + BAR_BYTES + (EPI_THREADS / 32) * STG_WARP_BYTES + 1024;
 static_assert(SMEM_TOTAL <= 232448, "dynamic shared memory above the 227 KB per-CTA limit");
 
@@ -370,7 +370,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
         const int q = warp & 3;
         uint8_t* stg = smem + STAGES * STAGE_BYTES + BAR_BYTES + (warp - 4) * STG_WARP_BYTES;
         uint8_t* stg_t = stg + STG_BYTES;
-        uint8_t* stg_e = stg + 2 * STG_BYTES;          // plane 0 of E: two buffers; plane 1: the next two
+        uint8_t* stg_e = stg + 2 * STG_BYTES;          // the planes of E
         const int crow = lane >> 2, cseg = lane & 3;   // coalesced layout: rows crow + 8i, segment cseg
         uint32_t acc = 0, acc_phase = 0;
         int op = 0;
@@ -404,21 +404,19 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const int m_out = P.o[0] == kPlaneOut ? cl.rows : ti.M;
             const uint32_t t_row = tmem_base + acc * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
 
-            // E of chunk c goes by cp.async into staging slot c & 1, one commit group per chunk, so it is in
-            // flight while the previous chunk is processed.
+            // E of chunk c goes into staging by cp.async while the chunk before is packed and stored.
             auto prefetch_e = [&](int c) {
                 const int col0 = ti.n0 + c * 32;
                 if (e0 != nullptr && col0 < ti.N && !(sym && col0 + 31 < row0)) {
-                    uint8_t* dst = stg_e + (c & 1) * STG_BYTES;
                     const int cc = col0 + 8 * cseg;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int rr = row0 + crow + 8 * i;
                         const bool in = rr < ti.M && cc < ti.N;
                         const size_t at = in ? static_cast<size_t>(rr) * e_ld + cc : 0;
-                        cp_async16_zfill(dst + stg_off64(crow + 8 * i, cseg), e0 + at, in ? 16 : 0);
+                        cp_async16_zfill(stg_e + stg_off64(crow + 8 * i, cseg), e0 + at, in ? 16 : 0);
                         if (e1 != nullptr)
-                            cp_async16_zfill(dst + 2 * STG_BYTES + stg_off64(crow + 8 * i, cseg), e1 + at, in ? 16 : 0);
+                            cp_async16_zfill(stg_e + STG_BYTES + stg_off64(crow + 8 * i, cseg), e1 + at, in ? 16 : 0);
                     }
                 }
                 cp_async_commit();
@@ -437,10 +435,8 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 const bool mirror = sym && col0 > row0;   // a chunk on the diagonal holds both halves
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_row + c * 32, r);
-                if (c + 1 < c_end) prefetch_e(c + 1);
-                else cp_async_commit();
+                cp_async_wait_group<0>();   // this lane's copies of chunk c have landed
                 tmem_ld_wait();
-                cp_async_wait_group<1>();   // this lane's copies of chunk c have landed
                 __syncwarp();               // ... and every lane's
                 float v[32];
 #pragma unroll
@@ -452,7 +448,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 }
                 if (e0 != nullptr && !below) {
                     for (int pl = 0; pl < (e1 != nullptr ? 2 : 1); ++pl) {
-                        const uint8_t* src = stg_e + ((c & 1) + 2 * pl) * STG_BYTES;
+                        const uint8_t* src = stg_e + pl * STG_BYTES;
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
                             const uint4 w = *reinterpret_cast<const uint4*>(src + stg_off64(lane, s));
@@ -466,7 +462,8 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                         }
                     }
                 }
-                __syncwarp();               // slot c & 1 is free for chunk c + 2, stg for the store
+                __syncwarp();               // E's staging is free, and the output's of the chunk before
+                if (c + 1 < c_end) prefetch_e(c + 1);
                 if (!below) {
                     // rows -> staging -> 8 rows x 64 bytes per instruction; plane 1 (what plane 0 has lost) beside it
 #pragma unroll
