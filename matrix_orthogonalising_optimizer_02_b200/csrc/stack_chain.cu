@@ -42,10 +42,10 @@ namespace muon {
 namespace {
 
 constexpr int BM = 256, BN = 256, BK = 64, STAGES = 5;
-constexpr int HM = BM / 2, HN = BN / 2;
+constexpr int HM = BM / 2, HN = BN / 2;   // per CTA: rows of A, columns of B of the widest tile
 constexpr int A_BYTES = HM * BK * 2, B_BYTES = HN * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int MN_CHUNK_BYTES = 64 * BK * 2;
+constexpr int BOX_BYTES = 64 * BK * 2;    // 64 x 64 fp16, whichever way it lies
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int BAR_BYTES = 256;
 constexpr int THREADS = 384, EPI_THREADS = 256;
@@ -239,6 +239,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
         for (int i = 0;; ++i) {
             const int k = i & 1;
             int t = atomicAdd(g.ticket, 1);
+            if (!mbar_wait_cluster(&dempty_bar[k], ((i >> 1) & 1) ^ 1u, abort_flag, dev_status)) break;
             if (t >= g.tiles) {
                 t = -1;
             } else {
@@ -248,7 +249,6 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 if (!wait_done(g.cls[g.op[op].cls].done + ti.b, g.op[op].need, abort_flag, dev_status)) t = -1;
                 fence_proxy_global();
             }
-            if (!mbar_wait_cluster(&dempty_bar[k], ((i >> 1) & 1) ^ 1u, abort_flag, dev_status)) break;
             *reinterpret_cast<volatile int*>(&draw_slot[k]) = t;
             asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_slot + 4u * k), "r"(t) : "memory");
             mbar_arrive_cluster(mapa_shared(smem_u32(&dfull_bar[k]), 0));
@@ -272,8 +272,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const int am0 = ti.m0 + HM * static_cast<int>(rank);
             const int hn = ti.w / 2;                      // columns of B that this CTA uses: 128, 64 or 32
             const int bn0 = ti.n0 + hn * static_cast<int>(rank);
-            // a K-major box has 128 rows whatever the tile takes; MN-major ones come 64 columns at a time
-            const int b_chunks = (hn + 63) / 64, b_bytes = b_mn ? b_chunks * MN_CHUNK_BYTES : B_BYTES;
+            const int b_chunks = (hn + 63) / 64;          // boxes of 64 (rows or columns) x 64
             const int kblocks = (ti.K + BK - 1) / BK;
             for (int seg = 0; seg < P.nseg && ok; ++seg) {
                 const CUtensorMap* ta = &c.map[P.ma[seg]];
@@ -286,22 +285,14 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                     const int k0 = kb * BK;
                     const uint32_t fb = full_leader + stage * 8u;
                     if (rank == 0) {
-                        mbar_arrive_expect_tx(&full_bar[stage], 2u * static_cast<uint32_t>(A_BYTES + b_bytes));
+                        mbar_arrive_expect_tx(&full_bar[stage], 2u * static_cast<uint32_t>(A_BYTES + b_chunks * BOX_BYTES));
                         issued_parity[stage] = static_cast<int>(phase);
                     }
-                    if (!a_mn) {
-                        tma_load_3d_pair(sa, ta, fb, k0, am0, za);
-                    } else {
 #pragma unroll
-                        for (int h = 0; h < HM / 64; ++h)
-                            tma_load_3d_pair(sa + h * MN_CHUNK_BYTES, ta, fb, am0 + 64 * h, k0, za);
-                    }
-                    if (!b_mn) {
-                        tma_load_3d_pair(sb, tb, fb, k0, bn0, zb);
-                    } else {
-                        for (int h = 0; h < b_chunks; ++h)
-                            tma_load_3d_pair(sb + h * MN_CHUNK_BYTES, tb, fb, bn0 + 64 * h, k0, zb);
-                    }
+                    for (int h = 0; h < HM / 64; ++h)
+                        tma_load_3d_pair(sa + h * BOX_BYTES, ta, fb, a_mn ? am0 + 64 * h : k0, a_mn ? k0 : am0 + 64 * h, za);
+                    for (int h = 0; h < b_chunks; ++h)
+                        tma_load_3d_pair(sb + h * BOX_BYTES, tb, fb, b_mn ? bn0 + 64 * h : k0, b_mn ? k0 : bn0 + 64 * h, zb);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -341,9 +332,9 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 const uint32_t base_b = base_a + A_BYTES;
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k) {
-                    const uint64_t ad = a_mn ? smem_desc_sw128(base_a + k * 2048, MN_CHUNK_BYTES, 1024)
+                    const uint64_t ad = a_mn ? smem_desc_sw128(base_a + k * 2048, BOX_BYTES, 1024)
                                              : smem_desc_sw128(base_a + k * 32, 16, 1024);
-                    const uint64_t bd = b_mn ? smem_desc_sw128(base_b + k * 2048, MN_CHUNK_BYTES, 1024)
+                    const uint64_t bd = b_mn ? smem_desc_sw128(base_b + k * 2048, BOX_BYTES, 1024)
                                              : smem_desc_sw128(base_b + k * 32, 16, 1024);
                     tc_mma_bf16_pair(d_tmem, ad, bd, idesc, accumulate);   // kind::f16, types from idesc
                     accumulate = 1;
@@ -511,8 +502,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             mbar_arrive_cluster(tempty_leader + acc * 8u);
             // the block's next operation may read what this warp stored, by TMA among other ways
             fence_proxy_global();
-            __threadfence();
-            __syncwarp();
+            __syncwarp();                       // the release below covers every lane's stores
             if (lane == 0) add_done(cl.done + ti.b);
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }

@@ -28,7 +28,7 @@ constexpr uint32_t kStackOutBf16 = 8u;   // plane 0 of the output is bf16
 constexpr uint32_t kStackRowMajor = 16u; // tiles swept along the rows of a block first
 
 enum StackPlane { kPlaneX, kPlaneL, kPlaneA, kPlaneB, kPlaneOut, kPlaneD, kPlaneDL, kPlaneS, kPlaneP, kPlanes, kPlaneNone = 255 };
-enum StackMap { kMapXk, kMapXmn, kMapA, kMapB, kMapDk, kMapDmn, kMapS, kMapP, kMaps };
+enum StackMap { kMapX, kMapA, kMapB, kMapD, kMapS, kMapP, kMaps };
 
 struct ChainPlane {
     __half* p;
@@ -59,9 +59,9 @@ struct ChainOp {
 constexpr int kChainWarps = 16;          // epilogue warps of a tile: what a finished tile adds to `done`
 constexpr int kChainMaxClasses = 12, kChainMaxOps = 360;
 
-// Tensor map of `count` row-major fp16 matrices (rows x cols, dense): a box of 64 columns x
-// box_rows rows of one matrix, 128-byte swizzle, zero fill out of bounds.
-bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows);
+// Tensor map of `count` row-major fp16 matrices (rows x cols, dense): boxes of 64 x 64 of one matrix, 128-byte
+// swizzle, zero fill out of bounds.  The same box serves as a K-major and as an MN-major piece of an operand.
+bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count);
 
 // Tiles of one block of an operation: 256 rows x 64 bn columns.  Symmetric ones are those that reach the upper
 // triangle: with 4 / bn tile columns to 256, column nb has nb / (4 / bn) + 1 of them.

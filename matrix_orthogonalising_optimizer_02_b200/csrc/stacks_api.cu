@@ -331,10 +331,8 @@ bool chain_class(ChainClass& o, const StackClass& c) {
     o.plane[kPlaneB] = {c.B, sq, c.r8};
     o.plane[kPlaneOut] = {c.last, pl, c.cp};
     const int nx = c.x_slots * c.count, na = c.a_slots * c.count;
-    return encode_stack_tmap(&o.map[kMapXk], c.X, c.rp, c.cp, nx, 128) &&
-           encode_stack_tmap(&o.map[kMapXmn], c.X, c.rp, c.cp, nx, 64) &&
-           encode_stack_tmap(&o.map[kMapA], c.A, c.r8, c.r8, na, 128) &&
-           encode_stack_tmap(&o.map[kMapB], c.B, c.r8, c.r8, na, 128);
+    return encode_stack_tmap(&o.map[kMapX], c.X, c.rp, c.cp, nx) && encode_stack_tmap(&o.map[kMapA], c.A, c.r8, c.r8, na) &&
+           encode_stack_tmap(&o.map[kMapB], c.B, c.r8, c.r8, na);
 }
 
 // Tile width of an operation (in 64 columns): the one whose time is least in this model, in us measured on a
@@ -383,12 +381,12 @@ void op_seg(ChainOp& o, int ma, int sa, int mb, int sb) {
     o.sb[o.nseg] = static_cast<uint8_t>(sb);
     ++o.nseg;
 }
-struct Map2 {
-    int k, mn, slot;    // maps of a plane by box, and the slot
+struct MapSlot {
+    int map, slot;
 };
 // r x r product of two rows x cols planes over the long side: X Y^T (wide) or X^T Y (tall).
-void gram_seg(ChainOp& o, const StackClass& c, Map2 x, Map2 y) {
-    op_seg(o, c.tall ? x.mn : x.k, x.slot, c.tall ? y.mn : y.k, y.slot);
+void gram_seg(ChainOp& o, const StackClass& c, MapSlot x, MapSlot y) {
+    op_seg(o, x.map, x.slot, y.map, y.slot);
     o.flags = kStackSym | (c.tall ? kStackAMn | kStackBMn : 0u);
 }
 // r x r product of two symmetric matrices (both read along their rows).
@@ -398,9 +396,9 @@ void square_seg(ChainOp& o, int mx, int sx, int my, int sy) {
 }
 // Symmetric x plane (wide) or plane x symmetric (tall).  Neighbouring tiles share a block of the plane, so that
 // the symmetric factor stays in L2.
-void apply_seg(ChainOp& o, const StackClass& c, int ms, int ss, Map2 x) {
-    if (c.tall) op_seg(o, x.k, x.slot, ms, ss);
-    else op_seg(o, ms, ss, x.mn, x.slot);
+void apply_seg(ChainOp& o, const StackClass& c, int ms, int ss, MapSlot x) {
+    if (c.tall) op_seg(o, x.map, x.slot, ms, ss);
+    else op_seg(o, ms, ss, x.map, x.slot);
     o.flags = c.tall ? kStackRowMajor : kStackBMn;
 }
 
@@ -491,7 +489,7 @@ muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vec
                 const StackClass& c = g.classes[k];
                 const double a = c.a[t], b = c.b[t];
                 const int xs = t % c.x_slots, as = t % c.a_slots;
-                const Map2 x = {kMapXk, kMapXmn, xs};
+                const MapSlot x = {kMapX, xs};
                 ChainOp o = new_op(k, stage, classes[k], 1, call.sms / 2);
                 if (stage == 0) {
                     gram_seg(o, c, x, x);
@@ -864,10 +862,9 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             const GradPlanes& q = gp[k];
             ChainClass& o = classes[k];
             const long long pl = static_cast<long long>(c.rp) * c.cp, sq = static_cast<long long>(c.r8) * c.r8;
-            const bool ok = chain_class(o, c) && encode_stack_tmap(&o.map[kMapDk], q.D, c.rp, c.cp, 2 * c.count, 128) &&
-                            encode_stack_tmap(&o.map[kMapDmn], q.D, c.rp, c.cp, 2 * c.count, 64) &&
-                            encode_stack_tmap(&o.map[kMapS], q.S, c.r8, c.r8, c.count, 128) &&
-                            encode_stack_tmap(&o.map[kMapP], q.P, c.r8, c.r8, c.count, 128);
+            const bool ok = chain_class(o, c) && encode_stack_tmap(&o.map[kMapD], q.D, c.rp, c.cp, 2 * c.count) &&
+                            encode_stack_tmap(&o.map[kMapS], q.S, c.r8, c.r8, c.count) &&
+                            encode_stack_tmap(&o.map[kMapP], q.P, c.r8, c.r8, c.count);
             if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
             o.done = q.done;
             o.plane[kPlaneD] = {q.D, pl, c.cp};
@@ -879,7 +876,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
         double flops = 0.0;
         for (int t = T - 1; t >= 0; --t) {
             const double cc = sch.coeffs[3 * t + 2];
-            const Map2 x = {kMapXk, kMapXmn, t}, dd = {kMapDk, kMapDmn, (t + 1) & 1};
+            const MapSlot x = {kMapX, t}, dd = {kMapD, (t + 1) & 1};
             for (int stage = 0; stage < 3; ++stage) {
                 for (int k : order) {
                     const StackClass& c = g.classes[k];
@@ -1099,9 +1096,9 @@ bool encode_map(CUtensorMap* out, const void* base, CUtensorMapDataType type, in
 }
 }  // namespace
 
-bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count, int box_rows) {
+bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, int count) {
     return encode_map(out, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, count, cols,
-                      static_cast<long long>(rows) * cols, box_rows);
+                      static_cast<long long>(rows) * cols, 64);
 }
 
 void small_stack_maps(SmallStackItem& it, int rows, int cols) {
