@@ -31,6 +31,186 @@ __device__ __forceinline__ float pow2f(int k) {   // 2^k, |k| <= 126
     return __int_as_float((k + 127) << 23);
 }
 
+// Eight elements of a thread: side by side (VEC), or, for arrays that 16-byte accesses cannot reach, a warp's
+// width apart, so that the warp's accesses lie side by side (8 single accesses of neighbours took 42 us to write
+// 24 blocks of 509 x 1021 in bf16).
+template <bool VEC>
+struct Eight {
+    int i[VEC ? 1 : 8], j[VEC ? 1 : 8];   // rows and columns in the block
+    int n;                                // VEC: how many of the eight lie inside
+    unsigned in;                          // otherwise: a bit for each that does
+    unsigned padded;                      // and for each that lies in the padded block
+    size_t plane;                         // the first one's place in the workspace planes
+
+    __device__ __forceinline__ Eight(const StackItem& it, size_t plane0, int c, int q) {
+        const int rp = (it.rows + 7) & ~7, cp = (it.cols + 7) & ~7;
+        if constexpr (VEC) {
+            const int g = c * (kStackChunk / 8) + q * kStackThreads + static_cast<int>(threadIdx.x), cg = cp >> 3;
+            i[0] = g / cg;
+            j[0] = (g - i[0] * cg) * 8;
+            n = i[0] < it.rows ? min(8, it.cols - j[0]) : 0;
+            padded = i[0] < rp;
+            plane = plane0 + static_cast<size_t>(g) * 8;
+        } else {
+            const int f0 = c * kStackChunk + (q * (kStackThreads / 32) + static_cast<int>(threadIdx.x >> 5)) * 256 + (threadIdx.x & 31);
+            i[0] = f0 / cp;
+            j[0] = f0 - i[0] * cp;
+            in = padded = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e > 0) {
+                    i[e] = i[e - 1];
+                    j[e] = j[e - 1] + 32;
+                    if (cp >= 32) {
+                        if (j[e] >= cp) { ++i[e]; j[e] -= cp; }
+                    } else {
+                        while (j[e] >= cp) { ++i[e]; j[e] -= cp; }
+                    }
+                }
+                in |= (i[e] < it.rows && j[e] < it.cols) << e;
+                padded |= (i[e] < rp) << e;
+            }
+            plane = plane0 + f0;
+        }
+    }
+    __device__ __forceinline__ bool any() const {
+        if constexpr (VEC) return n > 0;
+        else return in != 0;
+    }
+    __device__ __forceinline__ void get(const void* p, int dtype, long long base, int ld, float (&x)[8]) const {
+        if constexpr (VEC) {
+            load8(p, dtype, base + static_cast<long long>(i[0]) * ld + j[0], n, true, x);
+        } else {
+            by_type(dtype, [&](auto t) {
+                using E = decltype(t);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[e] = in >> e & 1 ? widen(static_cast<const E*>(p)[base + static_cast<long long>(i[e]) * ld + j[e]]) : 0.f;
+            });
+        }
+    }
+    __device__ __forceinline__ void put(void* p, int dtype, long long base, int ld, const float (&x)[8]) const {
+        if constexpr (VEC) {
+            store8(p, dtype, base + static_cast<long long>(i[0]) * ld + j[0], n, true, x);
+        } else {
+            by_type(dtype, [&](auto t) {
+                using E = decltype(t);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (in >> e & 1) narrow(static_cast<E*>(p)[base + static_cast<long long>(i[e]) * ld + j[e]], x[e]);
+            });
+        }
+    }
+    __device__ __forceinline__ void get_plane(const __half* p, float (&x)[8]) const {
+        if constexpr (VEC) {
+            unpack8(*reinterpret_cast<const uint4*>(p + plane), MUON_F16, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = in >> e & 1 ? __half2float(p[plane + 32 * e]) : 0.f;
+        }
+    }
+    // Stores x and leaves in it what fp16 has lost.
+    __device__ __forceinline__ void put_plane(__half* p, float (&x)[8]) const {
+        if constexpr (VEC) {
+            const uint4 h = pack8(MUON_F16, x);
+            *reinterpret_cast<uint4*>(p + plane) = h;
+            float y[8];
+            unpack8(h, MUON_F16, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] -= y[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const __half h = __float2half_rn(x[e]);
+                if (padded >> e & 1) p[plane + 32 * e] = h;
+                x[e] -= __half2float(h);
+            }
+        }
+    }
+};
+
+// A CTA's chunk c of block b; returns the thread's part of the sum that kNorm and kDot form.
+template <StackPass PASS, bool VEC>
+__device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs& a, int b, int c, float gs, float up, float od,
+                                       float ox) {
+    const int rp = (it.rows + 7) & ~7, cp = (it.cols + 7) & ~7;
+    const size_t plane0 = static_cast<size_t>(b) * rp * cp;
+    const long long gb = b * it.g_stride, mb = b * it.m_stride, wb = b * it.w_stride;
+    double ss = 0.0;
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+        const Eight<VEC> at(it, plane0, c, q);
+        if (!at.padded) continue;
+        if (PASS == StackPass::kNorm) {
+            if (!at.any()) continue;
+            float x[8];
+            at.get(it.G, it.g_dtype, gb, it.g_ld, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= gs;
+            if (it.M != nullptr) {
+                float m[8];
+                at.get(it.M, MUON_F32, mb, it.m_ld, m);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    m[e] = fmaf(a.beta, m[e], x[e]);
+                    x[e] = a.nesterov ? fmaf(a.beta, m[e], x[e]) : m[e];
+                }
+                at.put(it.M, MUON_F32, mb, it.m_ld, m);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
+        } else if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (at.any()) {
+                if (it.M == nullptr || a.nesterov) {
+                    at.get(it.G, it.g_dtype, gb, it.g_ld, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= gs;
+                }
+                if (it.M != nullptr) {   // the momentum pass has updated M
+                    float m[8];
+                    at.get(it.M, MUON_F32, mb, it.m_ld, m);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = a.nesterov ? fmaf(a.beta, m[e], x[e]) : m[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= up;
+            at.put_plane(it.hi, x);
+            at.put_plane(it.lo, x);
+        } else {
+            if (!at.any()) continue;
+            float x[8];
+            at.get_plane(it.hi, x);
+            if (PASS == StackPass::kOut) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= it.step;
+                at.put(it.W, it.w_dtype, wb, it.w_ld, x);
+            } else if (PASS == StackPass::kUpdate) {
+                float w[8];
+                at.get(it.W, it.w_dtype, wb, it.w_ld, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = fmaf(it.step, x[e], it.decay * w[e]);
+                at.put(it.W, it.w_dtype, wb, it.w_ld, w);
+            } else {
+                float y[8], z[8];
+                at.get_plane(it.lo, y);
+                at.get_plane(it.hi2, z);
+                if (PASS == StackPass::kDot) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        ss = fma(static_cast<double>(x[e]) + static_cast<double>(y[e]), static_cast<double>(z[e]), ss);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(od, x[e] + y[e], ox * z[e]);
+                    at.put(it.W, it.w_dtype, wb, it.w_ld, x);
+                }
+            }
+        }
+    }
+    return ss;
+}
+
 template <StackPass PASS, int N>
 __global__ void __launch_bounds__(kStackThreads)
 stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
@@ -42,10 +222,7 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
     }
     const StackItem& it = p.item[lo];
     const int b = (chunk - it.chunk0) / it.chunks, c = (chunk - it.chunk0) - b * it.chunks;
-    const int rp = (it.rows + 7) & ~7, cg = (it.cols + 7) >> 3;   // padded rows, 8-column groups a row
-    const int groups = rp * cg;
     const float gs = p.a.gscale != nullptr ? __ldg(p.a.gscale) : 1.f;
-    const size_t plane = static_cast<size_t>(b) * groups * 8;
     float* info = it.info != nullptr ? it.info + static_cast<size_t>(b) * kStackInfo : nullptr;
     double* partials = it.partials != nullptr ? it.partials + static_cast<size_t>(b) * it.chunks : nullptr;
 
@@ -87,91 +264,10 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
 
     if (PASS == StackPass::kNorm && p.a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.a.status = 0;
 
-    double ss = 0.0;
-#pragma unroll
-    for (int q = 0; q < GROUPS; ++q) {
-        const int g = c * (kStackChunk / 8) + q * kStackThreads + static_cast<int>(threadIdx.x);
-        if (g >= groups) break;
-        const int i = g / cg, j = (g - i * cg) * 8;
-        const int n = i < it.rows ? min(8, it.cols - j) : 0;     // elements of this group inside the block
-        const long long bi = b;
-        const size_t w8 = plane + static_cast<size_t>(g) * 8;    // the group in the workspace planes
-        if (PASS == StackPass::kNorm) {
-            if (n == 0) continue;
-            float x[8];
-            load8(it.G, it.g_dtype, bi * it.g_stride + static_cast<long long>(i) * it.g_ld + j, n, it.vec & 1, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= gs;
-            if (it.M != nullptr) {
-                float m[8];
-                const long long mo = bi * it.m_stride + static_cast<long long>(i) * it.m_ld + j;
-                load8(it.M, MUON_F32, mo, n, it.vec & 2, m);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    m[e] = fmaf(p.a.beta, m[e], x[e]);
-                    x[e] = p.a.nesterov ? fmaf(p.a.beta, m[e], x[e]) : m[e];
-                }
-                store8(it.M, MUON_F32, mo, n, it.vec & 2, m);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
-        } else if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad) {
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (n > 0) {
-                if (it.M == nullptr || p.a.nesterov) {
-                    load8(it.G, it.g_dtype, bi * it.g_stride + static_cast<long long>(i) * it.g_ld + j, n, it.vec & 1, x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= gs;
-                }
-                if (it.M != nullptr) {   // the momentum pass has updated M
-                    float m[8];
-                    load8(it.M, MUON_F32, bi * it.m_stride + static_cast<long long>(i) * it.m_ld + j, n, it.vec & 2, m);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = p.a.nesterov ? fmaf(p.a.beta, m[e], x[e]) : m[e];
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= up;
-            const uint4 h = pack8(MUON_F16, x);
-            *reinterpret_cast<uint4*>(it.hi + w8) = h;
-            if (it.lo != nullptr) {
-                float y[8];
-                unpack8(h, MUON_F16, y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e] - y[e];
-                *reinterpret_cast<uint4*>(it.lo + w8) = pack8(MUON_F16, y);
-            }
-        } else {
-            if (n == 0) continue;
-            float x[8];
-            unpack8(*reinterpret_cast<const uint4*>(it.hi + w8), MUON_F16, x);
-            const long long wo = bi * it.w_stride + static_cast<long long>(i) * it.w_ld + j;
-            if (PASS == StackPass::kOut) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= it.step;
-                store8(it.W, it.w_dtype, wo, n, it.vec & 4, x);
-            } else if (PASS == StackPass::kUpdate) {
-                float w[8];
-                load8(it.W, it.w_dtype, wo, n, it.vec & 4, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = fmaf(it.step, x[e], it.decay * w[e]);
-                store8(it.W, it.w_dtype, wo, n, it.vec & 4, w);
-            } else {
-                float y[8], z[8];
-                unpack8(*reinterpret_cast<const uint4*>(it.lo + w8), MUON_F16, y);
-                unpack8(*reinterpret_cast<const uint4*>(it.hi2 + w8), MUON_F16, z);
-                if (PASS == StackPass::kDot) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        ss = fma(static_cast<double>(x[e]) + static_cast<double>(y[e]), static_cast<double>(z[e]), ss);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = fmaf(od, x[e] + y[e], ox * z[e]);
-                    store8(it.W, it.w_dtype, wo, n, it.vec & 4, x);
-                }
-            }
-        }
-    }
+    constexpr int need = PASS == StackPass::kDot ? 0 : PASS == StackPass::kNorm || PASS == StackPass::kPack ? 3 : PASS == StackPass::kPackGrad ? 1 : 4;
+    const int have = it.vec | (it.M == nullptr ? 2 : 0);
+    const double ss = (have & need) == need ? walk<PASS, true>(it, p.a, b, c, gs, up, od, ox)
+                                            : walk<PASS, false>(it, p.a, b, c, gs, up, od, ox);
     if (PASS == StackPass::kNorm || PASS == StackPass::kDot) {
         const double t = block_sum256(ss);
         if (threadIdx.x == 0) partials[c] = t;
@@ -201,7 +297,7 @@ cudaError_t launch_any(StackItem* items, int n, const StackPassArgs& a, cudaStre
         if (chunks == 0) continue;
         StackPassArgs b = a;
         if (PASS == StackPass::kNorm && i0 > 0) b.status = nullptr;   // cleared once
-        static_assert(sizeof(PassParams<kFewItems>) <= 4000, "the small form's parameters launch faster (see stack_gemm.cu)");
+        static_assert(sizeof(PassParams<kFewItems>) <= 4000, "the small form's parameters launch faster (see stack_chain.cu)");
         const cudaError_t e = m <= kFewItems ? launch<PASS, kFewItems>(items + i0, m, b, chunks, stream)
                                              : launch<PASS, kStackMaxItems>(items + i0, m, b, chunks, stream);
         if (e != cudaSuccess) return e;

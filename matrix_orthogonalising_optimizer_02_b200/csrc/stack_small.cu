@@ -282,116 +282,123 @@ __device__ __forceinline__ float sum_squares(const float (&u)[16]) {
     return s;
 }
 
-// Element j (0..15) of this thread in chunk ch, a warp along a row of the caller's.
-struct Spot {
-    int i, c;              // X's row, chunk column
-    long long at;          // place in an array with row pitch ld
-    bool ok;
-};
-__device__ __forceinline__ Spot spot(const Slab& s, int ch, int j, int ld) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Spot p;
-    int row, col;
-    if (!s.tall) {
-        p.i = row = warp + 16 * (j >> 1);
-        p.c = lane + 32 * (j & 1);
-        col = s.first(ch) + p.c;
-    } else {
-        p.c = warp + 16 * (j >> 2);
-        p.i = col = lane + 32 * (j & 3);
-        row = s.first(ch) + p.c;
+// The element-wise walk of a chunk: element (a, h) of a thread, A x H = 16 of them, a warp along the caller's
+// rows.  Offsets are a base and two steps.
+template <bool TALL>
+struct Walk {
+    static constexpr int A = TALL ? 4 : 8, H = 16 / A;
+    int row, col;              // the caller's, of element (0, 0)
+    int rows, cols;
+    long long at;              // its place in an array with row pitch ld
+    int staged;                // its place in the staging buffer
+    __device__ __forceinline__ Walk(const Slab& s, int ch, int ld) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        row = warp + (TALL ? s.first(ch) : 0);
+        col = lane + (TALL ? 0 : s.first(ch));
+        rows = s.rows;
+        cols = s.cols;
+        at = static_cast<long long>(row) * ld + col;
+        staged = TALL ? lane * STG_PITCH + warp : warp * STG_PITCH + lane;
     }
-    p.at = static_cast<long long>(row) * ld + col;
-    p.ok = row < s.rows && col < s.cols;
-    return p;
-}
-template <class F>
-__device__ __forceinline__ void by_type(int dtype, F f) {
-    if (dtype == MUON_F32) f(float());
-    else if (dtype == MUON_F16) f(__half());
-    else f(__nv_bfloat16());
-}
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void narrow(float& d, float x) { d = x; }
-__device__ __forceinline__ void narrow(__half& d, float x) { d = __float2half_rn(x); }
-__device__ __forceinline__ void narrow(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+    __device__ __forceinline__ bool ok(int a, int h) const { return row + 16 * a < rows && col + 32 * h < cols; }
+    __device__ __forceinline__ int place(int a, int h) const {
+        return staged + (TALL ? 32 * h * STG_PITCH + 16 * a : 16 * a * STG_PITCH + 32 * h);
+    }
+};
 
-// The element-wise walks, out of line: their registers and code are not the iterations'.
+// Out of line: their registers and code are not the iterations'.
+template <bool TALL>
 __device__ __noinline__ double slab_in_any(const Slab s, const SmallStackItem& item, long long b, const Momentum mo) {
-    const SmallStackItem it = item;    // by value: the stores below cannot alias it
-    const int warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
-    const uint8_t* g0 = static_cast<const uint8_t*>(it.G) + b * it.g_stride * (it.g_dtype == MUON_F32 ? 4 : 2);
-    float* m0 = it.M + b * it.m_stride;
+    using W = Walk<TALL>;
+    const int g_dtype = item.g_dtype, warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
+    const uint8_t* g0 = static_cast<const uint8_t*>(item.G) + b * item.g_stride * (g_dtype == MUON_F32 ? 4 : 2);
+    float* m0 = item.M + b * item.m_stride;
+    const int g_ld = item.g_ld, m_ld = item.m_ld;
+    const long long g16 = 16ll * g_ld, m16 = 16ll * m_ld;
     double ss = 0.0;
-#pragma unroll 1
-    for (int ch = 0; ch < s.nchunk; ++ch) {
-        float* buf = reinterpret_cast<float*>(s.buf) + (ch & 1) * STG_FLOATS;
-        float u[16], m[16];
-        by_type(it.g_dtype, [&](auto t) {
-            using E = decltype(t);
+    float u[16], m[16];
+    auto fetch = [&](int ch) {
+        const W g(s, ch, g_ld), k(s, ch, m_ld);
+        by_type(g_dtype, [&](auto t) {
+            const decltype(t)* p = reinterpret_cast<const decltype(t)*>(g0) + g.at;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const Spot p = spot(s, ch, j, it.g_ld);
-                u[j] = p.ok ? widen(reinterpret_cast<const E*>(g0)[p.at]) : 0.f;
-            }
+            for (int a = 0; a < W::A; ++a)
+#pragma unroll
+                for (int h = 0; h < W::H; ++h) u[a * W::H + h] = g.ok(a, h) ? widen(p[a * g16 + 32 * h]) : 0.f;
         });
         if (mo.on) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const Spot p = spot(s, ch, j, it.m_ld);
-                m[j] = p.ok ? m0[p.at] : 0.f;
-            }
-        }
-        mo(u, m);
-        ss += static_cast<double>(sum_squares(u));
+            for (int a = 0; a < W::A; ++a)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const Spot p = spot(s, ch, j, it.m_ld);
-            buf[p.i * STG_PITCH + p.c] = u[j];
-            if (mo.on && p.ok) m0[p.at] = m[j];
+                for (int h = 0; h < W::H; ++h) m[a * W::H + h] = k.ok(a, h) ? m0[k.at + a * m16 + 32 * h] : 0.f;
         }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 16; ++h) u[h] = buf[row * STG_PITCH + cg * 16 + h];
-        tmem_st_x16(s.t_lane + ch * 64 + cg * 16, u);
-    }
-    return ss;
-}
-__device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& item, long long b, float out) {
-    const SmallStackItem it = item;
-    const int warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
-    uint8_t* w0 = static_cast<uint8_t*>(it.W) + b * it.w_stride * (it.w_dtype == MUON_F32 ? 4 : 2);
-    const float decay = it.decay, step = it.step * out;
-    const bool update = decay != 0.f;
+    };
+    fetch(0);
 #pragma unroll 1
     for (int ch = 0; ch < s.nchunk; ++ch) {
         float* buf = reinterpret_cast<float*>(s.buf) + (ch & 1) * STG_FLOATS;
-        float z[16];
-        tmem_ld_x16(s.t_lane + ch * 64 + cg * 16, z);
+        mo(u, m);
+        ss += static_cast<double>(sum_squares(u));
+        const W k(s, ch, m_ld);
 #pragma unroll
-        for (int h = 0; h < 16; ++h) buf[row * STG_PITCH + cg * 16 + h] = z[h];
+        for (int a = 0; a < W::A; ++a)
+#pragma unroll
+            for (int h = 0; h < W::H; ++h) {
+                buf[k.place(a, h)] = u[a * W::H + h];
+                if (mo.on && k.ok(a, h)) m0[k.at + a * m16 + 32 * h] = m[a * W::H + h];
+            }
+        if (ch + 1 < s.nchunk) fetch(ch + 1);      // on its way while this chunk goes to TMEM
         __syncthreads();
-        by_type(it.w_dtype, [&](auto t) {
-            using E = decltype(t);
-            E* wt = reinterpret_cast<E*>(w0);
-            float x[16];
-            if (update) {
+        float z[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const Spot p = spot(s, ch, j, it.w_ld);
-                    x[j] = p.ok ? widen(wt[p.at]) : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const Spot p = spot(s, ch, j, it.w_ld);
-                const float v = buf[p.i * STG_PITCH + p.c];
-                if (p.ok) narrow(wt[p.at], update ? fmaf(step, v, decay * x[j]) : step * v);
-            }
-        });
+        for (int h = 0; h < 16; ++h) z[h] = buf[row * STG_PITCH + cg * 16 + h];
+        tmem_st_x16(s.t_lane + ch * 64 + cg * 16, z);
     }
+    return ss;
+}
+template <bool TALL>
+__device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& item, long long b, float out) {
+    using W = Walk<TALL>;
+    const int w_dtype = item.w_dtype, warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
+    uint8_t* w0 = static_cast<uint8_t*>(item.W) + b * item.w_stride * (w_dtype == MUON_F32 ? 4 : 2);
+    const int w_ld = item.w_ld;
+    const long long w16 = 16ll * w_ld;
+    const float decay = item.decay, step = item.step * out;
+    const bool update = decay != 0.f;
+    by_type(w_dtype, [&](auto t) {
+        using E = decltype(t);
+        E x[16];
+        auto fetch = [&](int ch) {
+            if (!update) return;
+            const W k(s, ch, w_ld);
+            const E* p = reinterpret_cast<const E*>(w0) + k.at;
+#pragma unroll
+            for (int a = 0; a < W::A; ++a)
+#pragma unroll
+                for (int h = 0; h < W::H; ++h)
+                    if (k.ok(a, h)) x[a * W::H + h] = p[a * w16 + 32 * h];
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int ch = 0; ch < s.nchunk; ++ch) {
+            float* buf = reinterpret_cast<float*>(s.buf) + (ch & 1) * STG_FLOATS;
+            float z[16];
+            tmem_ld_x16(s.t_lane + ch * 64 + cg * 16, z);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) buf[row * STG_PITCH + cg * 16 + h] = z[h];
+            __syncthreads();
+            const W k(s, ch, w_ld);
+            E* p = reinterpret_cast<E*>(w0) + k.at;
+#pragma unroll
+            for (int a = 0; a < W::A; ++a)
+#pragma unroll
+                for (int h = 0; h < W::H; ++h) {
+                    const float v = buf[k.place(a, h)];
+                    if (k.ok(a, h)) narrow(p[a * w16 + 32 * h], update ? fmaf(step, v, decay * widen(x[a * W::H + h])) : step * v);
+                }
+            if (ch + 1 < s.nchunk) fetch(ch + 1);
+        }
+    });
 }
 
 template <int N>
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         if (tid == 0) bulk_wait_read<0>();
         __syncthreads();       // the buffers are free
     } else {
-        ss = slab_in_any(slab, it, b, mo);
+        ss = tall ? slab_in_any<true>(slab, it, b, mo) : slab_in_any<false>(slab, it, b, mo);
     }
     tmem_st_wait();
     double sum = 0.0;
@@ -765,7 +772,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         }
         if (tid == 0) bulk_wait_read<0>();
     } else {
-        slab_out_any(slab, it, b, k.out);
+        if (tall) slab_out_any<true>(slab, it, b, k.out);
+        else slab_out_any<false>(slab, it, b, k.out);
     }
     tc_fence_before();
     __syncthreads();

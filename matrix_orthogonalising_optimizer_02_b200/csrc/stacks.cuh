@@ -85,7 +85,7 @@ struct alignas(16) StackItem {
     float* M;             // momentum (nullable)
     void* W;              // weights or output
     __half* hi;           // workspace planes of the first block
-    __half* lo;           // nullable
+    __half* lo;
     const __half* hi2;    // gradient of the input only: X_0
     float* info;          // per block: kStackInfo floats
     const float* ginfo;   // gradient of the input only: info of the gradient planes

@@ -45,6 +45,21 @@ __device__ __forceinline__ void store_elem(void* p, int dtype, long long e, floa
     else static_cast<__nv_bfloat16*>(p)[e] = __float2bfloat16_rn(v);
 }
 
+// Calls f with a value of the element type: code for several elements chooses the type once, so that their
+// loads are under way together.
+template <class F>
+__device__ __forceinline__ void by_type(int dtype, F f) {
+    if (dtype == MUON_F32) f(float());
+    else if (dtype == MUON_F16) f(__half());
+    else f(__nv_bfloat16());
+}
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void narrow(float& d, float x) { d = x; }
+__device__ __forceinline__ void narrow(__half& d, float x) { d = __float2half_rn(x); }
+__device__ __forceinline__ void narrow(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+
 // Elements e .. e + n - 1 (n <= 8; the rest of v is zero).  vec: e is 16-byte aligned and n == 8.
 __device__ __forceinline__ void load8(const void* p, int dtype, long long e, int n, bool vec, float (&v)[8]) {
     if (vec && n == 8) {
@@ -56,8 +71,11 @@ __device__ __forceinline__ void load8(const void* p, int dtype, long long e, int
             unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e), dtype, v);
         }
     } else {
+        by_type(dtype, [&](auto t) {
+            using E = decltype(t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? load_elem(p, dtype, e + j) : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = j < n ? widen(static_cast<const E*>(p)[e + j]) : 0.f;
+        });
     }
 }
 __device__ __forceinline__ void store8(void* p, int dtype, long long e, int n, bool vec, const float (&v)[8]) {
@@ -70,9 +88,12 @@ __device__ __forceinline__ void store8(void* p, int dtype, long long e, int n, b
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e) = pack8(dtype, v);
         }
     } else {
+        by_type(dtype, [&](auto t) {
+            using E = decltype(t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) store_elem(p, dtype, e + j, v[j]);
+            for (int j = 0; j < 8; ++j)
+                if (j < n) narrow(static_cast<E*>(p)[e + j], v[j]);
+        });
     }
 }
 
