@@ -1,5 +1,5 @@
 // Elementwise passes over stacks of blocks: what comes before and after the products of
-// stack_gemm.cu.  HBM-bound; one CTA takes 8192 elements of one block, 8 a thread at a time.
+// stack_chain.cu.  HBM-bound; one CTA takes 2048 elements of one block, 8 a thread, or four times as many.
 //
 // Norms.  A block's sum of squares is formed in fp64 (a gradient's elements, 1e-20 or 1e20, square
 // out of fp32's range), one partial per CTA; the next pass's CTAs each add up their block's partials
@@ -25,7 +25,6 @@ struct PassParams {
 };
 
 constexpr int kFewItems = 21;
-constexpr int GROUPS = kStackChunk / 8 / kStackThreads;   // 8-element groups per thread
 
 __device__ __forceinline__ float pow2f(int k) {   // 2^k, |k| <= 126
     return __int_as_float((k + 127) << 23);
@@ -42,17 +41,17 @@ struct Eight {
     unsigned padded;                      // and for each that lies in the padded block
     size_t plane;                         // the first one's place in the workspace planes
 
-    __device__ __forceinline__ Eight(const StackItem& it, size_t plane0, int c, int q) {
+    __device__ __forceinline__ Eight(const StackItem& it, size_t plane0, int c, int q) {   // q: the thread's group
         const int rp = (it.rows + 7) & ~7, cp = (it.cols + 7) & ~7;
         if constexpr (VEC) {
-            const int g = c * (kStackChunk / 8) + q * kStackThreads + static_cast<int>(threadIdx.x), cg = cp >> 3;
+            const int g = (c * it.per + q) * kStackThreads + static_cast<int>(threadIdx.x), cg = cp >> 3;
             i[0] = g / cg;
             j[0] = (g - i[0] * cg) * 8;
             n = i[0] < it.rows ? min(8, it.cols - j[0]) : 0;
             padded = i[0] < rp;
             plane = plane0 + static_cast<size_t>(g) * 8;
         } else {
-            const int f0 = c * kStackChunk + (q * (kStackThreads / 32) + static_cast<int>(threadIdx.x >> 5)) * 256 + (threadIdx.x & 31);
+            const int f0 = (c * it.per + q) * kStackGroup + static_cast<int>(threadIdx.x >> 5) * 256 + (threadIdx.x & 31);
             i[0] = f0 / cp;
             j[0] = f0 - i[0] * cp;
             in = padded = 0;
@@ -137,8 +136,7 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
     const size_t plane0 = static_cast<size_t>(b) * rp * cp;
     const long long gb = b * it.g_stride, mb = b * it.m_stride, wb = b * it.w_stride;
     double ss = 0.0;
-#pragma unroll
-    for (int q = 0; q < GROUPS; ++q) {
+    for (int q = 0; q < it.per; ++q) {
         const Eight<VEC> at(it, plane0, c, q);
         if (!at.padded) continue;
         if (PASS == StackPass::kNorm) {

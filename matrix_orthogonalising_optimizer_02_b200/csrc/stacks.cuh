@@ -93,7 +93,7 @@ struct alignas(16) StackItem {
     long long g_stride, m_stride, w_stride;
     int g_ld, m_ld, w_ld;
     int rows, cols, count;
-    int chunks;           // chunks of kStackChunk padded elements per block
+    int chunks, per;      // chunks of per * kStackGroup padded elements in a block
     int chunk0;           // first chunk of this item in the launch
     int g_dtype, w_dtype;
     int vec;              // bit 0: G, bit 1: M, bit 2: W allow 8-element vector accesses
@@ -102,7 +102,17 @@ struct alignas(16) StackItem {
 };
 constexpr int kStackMaxItems = 128;
 constexpr int kStackThreads = 256;
-constexpr int kStackChunk = 8192;        // padded elements per chunk: 256 threads x 8 x 4
+constexpr int kStackGroup = 8 * kStackThreads;
+// Groups of a CTA: one where that spreads few elements over more SMs (a pass over 2 x 320 x 257 took 13 us with
+// four), four where there is work for all (24 x 512 x 1024: 41 us for the passes, 57 with one), and where a
+// block's CTAs would add up too many partial sums.
+inline int stack_per(int rp, int cp, int count) {
+    return static_cast<long long>(rp) * cp * count > 148ll * 8 * kStackGroup ? 4 : 1;
+}
+inline int stack_chunks(int rp, int cp, int per) {
+    const long long chunk = static_cast<long long>(per) * kStackGroup;
+    return static_cast<int>((static_cast<long long>(rp) * cp + chunk - 1) / chunk);
+}
 // Per block: info[0] = f0 (X_0 = f0 * hi), info[1] = 2^k (hi = U * 2^k), info[2] = 1 / (N + eps),
 // info[3] = N
 constexpr int kStackInfo = 4;

@@ -106,7 +106,7 @@ struct StackClass {
     int rows = 0, cols = 0, count = 0;
     int rp = 0, cp = 0, r = 0, s = 0, r8 = 0;   // padded sides; true and padded shorter side
     bool tall = false;
-    int chunks = 0;
+    int chunks = 0, per = 1;                     // chunks of a block in the elementwise passes
     std::vector<double> alpha, gamma, tau;       // tau[0] unused: X_0 = f0 * plane
     std::vector<double> shift, a, b;             // l; a + bl + cl^2 and b + 2cl (a and b without a shift)
     __half* X = nullptr;                         // x_slots slots: X_t in slot t % x_slots
@@ -132,7 +132,7 @@ StackClass make_class(int rows, int cols, const muon_ns_schedule& sch, const Bou
     c.r = std::min(rows, cols);
     c.s = std::max(rows, cols);
     c.r8 = up8(c.r);
-    c.chunks = static_cast<int>((static_cast<long long>(c.rp) * c.cp + kStackChunk - 1) / kStackChunk);
+    c.chunks = stack_chunks(c.rp, c.cp, 1);   // at most
     double flat = c.r;   // 1 / (mean diagonal of A_t) for a flat spectrum
     double sigma = 1.0 / std::sqrt(static_cast<double>(c.r));
     for (int t = 0; t < sch.n_iters; ++t) {
@@ -298,6 +298,8 @@ size_t layout_forward(Group& g, int T, bool saving, Arena& ws, Arena& sv) {
     take(ws, kStackTickets * sizeof(int));
     for (StackClass& c : g.classes) {
         Arena& keep = saving ? sv : ws;
+        c.per = stack_per(c.rp, c.cp, c.count);
+        c.chunks = stack_chunks(c.rp, c.cp, c.per);
         c.info = static_cast<float*>(take(keep, static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
         c.partials = static_cast<double*>(take(ws, static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
         c.done = static_cast<int*>(take(ws, static_cast<size_t>(c.count) * sizeof(int)));
@@ -648,7 +650,8 @@ std::vector<GradPlanes> layout_backward(const Group& g, Arena& ws) {
 size_t backward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& sch, const Bounds& bd) {
     size_t most = 0;
     for (Group& g : make_groups(shapes, sch, bd, SIZE_MAX)) {
-        Arena ws;
+        Arena ws, fw, sv;
+        layout_forward(g, sch.n_iters, true, fw, sv);
         layout_backward(g, ws);
         most = std::max(most, align_up(ws.used, kAlign));
     }
@@ -662,6 +665,7 @@ StackItem base_item(const StackClass& c, const Part& p) {
     it.cols = c.cols;
     it.count = p.count;
     it.chunks = c.chunks;
+    it.per = c.per;
     it.info = c.info + static_cast<size_t>(p.at) * kStackInfo;
     it.partials = c.partials + static_cast<size_t>(p.at) * c.chunks;
     return it;
