@@ -25,7 +25,7 @@
 // pairs idle) with tcgen05.mma.cta_group::2 (K = 16 a step):
 // each stages its 128 rows of A and half the columns of B, so an SM reads half the B bytes that a
 // one-SM tile would.  Roles per CTA (384 threads): warp 0 lane 0 TMA producer, warp 1 lane 0 of the
-// leader MMA issuer, warp 2 TMEM, warp 3 lane 0 of the leader draws tiles and waits until they may start (one ahead), warps 4..11
+// leader MMA issuer, warp 2 TMEM, warp 3 lane 0 of the leader draws tiles (one ahead), warps 4..11
 // epilogue (TMEM double buffered, so the epilogue of one tile overlaps the products of the next).
 // Global accesses of the epilogue are turned through shared memory into 8 rows x 64 bytes per
 // instruction, E arrives there a chunk ahead.  Every wait is bounded (ptx_sm100.cuh); no load uses
@@ -65,27 +65,33 @@ struct ChainParams {
     unsigned* status;
 };
 
-struct Tile {
-    int b, m0, n0, M, N, K;
-    int w;                 // columns of the tile
+// A drawn tile, as the drawer hands it to the readers.
+struct alignas(16) Draw {
+    int op;                // operation, | kUnready; negative: no more tiles
+    int b, m0, n0;         // block and place
 };
+constexpr int kUnready = 1 << 20;   // the block's earlier operations were not done when the tile was drawn
+
+struct Shape {
+    int M, N, K, w;        // of the operation; w: columns of a tile
+};
+__device__ __forceinline__ Shape shape_of(const ChainClass& c, const ChainOp& o) {
+    return {o.kind < 2 ? c.r8 : c.rp, o.kind < 2 ? c.r8 : c.cp, o.kind == 0 ? max(c.rp, c.cp) : c.r8, 64 * o.bn};
+}
 // Moves `op` on to the operation of tile t (tiles come in rising order) and gives the tile's place
 // (symmetric operations list the tiles with mb <= nb, column by column).
 template <class P>
-__device__ __forceinline__ Tile tile_at(const P& g, int t, int& op) {
+__device__ __forceinline__ Draw draw_of(const P& g, int t, int& op) {
     while (op + 1 < g.n && g.op[op + 1].tile0 <= t) ++op;
     const ChainOp& o = g.op[op];
     const ChainClass& c = g.cls[o.cls];
-    Tile r;
-    const int w = 64 * o.bn;
-    r.M = o.kind < 2 ? c.r8 : c.rp;
-    r.N = o.kind < 2 ? c.r8 : c.cp;
-    r.K = o.kind == 0 ? max(c.rp, c.cp) : c.r8;
-    r.w = w;
-    const int mbs = (r.M + BM - 1) / BM, nbs = (r.N + w - 1) / w;
+    const Shape z = shape_of(c, o);
+    const int mbs = (z.M + BM - 1) / BM, nbs = (z.N + z.w - 1) / z.w;
     const int per = chain_tiles(c, o), i = t - o.tile0;
-    r.b = i / per;
-    int l = i - r.b * per, mb, nb;
+    Draw d;
+    d.op = op;
+    d.b = i / per;
+    int l = i - d.b * per, mb, nb;
     if (o.flags & kStackSym) {
         // column groups of 256: group g has 4 / bn columns of g + 1 tiles
         const int cols = 4 / o.bn, u = l / cols;
@@ -103,25 +109,28 @@ __device__ __forceinline__ Tile tile_at(const P& g, int t, int& op) {
         nb = l / mbs;
         mb = l - nb * mbs;
     }
-    r.m0 = mb * BM;
-    r.n0 = nb * w;
-    return r;
+    d.m0 = mb * BM;
+    d.n0 = nb * z.w;
+    return d;
 }
 
+__device__ __forceinline__ int load_done(const int* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 // Bounded wait until *p >= need; what the counted warps wrote is visible afterwards.
 __device__ __forceinline__ bool wait_done(const int* p, int need, volatile int* abort, unsigned* status) {
     const unsigned long long t0 = global_ns();
     while (true) {
-        int v;
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-        if (v >= need) return true;
+        if (load_done(p) >= need) return true;
         if (*abort) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
             atomicOr(status, kDevErrTimeout);
             return false;
         }
-        __nanosleep(32);
+        __nanosleep(64);
     }
 }
 __device__ __forceinline__ void add_done(int* p) {
@@ -130,22 +139,47 @@ __device__ __forceinline__ void add_done(int* p) {
 // Global data written by ordinary stores and read by TMA (on either side of a signal).
 __device__ __forceinline__ void fence_proxy_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// Tile numbers from the leader's drawer to both CTAs: a ring of two slots.
+// Tiles from the leader's drawer to both CTAs: a ring of two slots.  A tile that was not ready when it was drawn
+// is waited for by the CTA's producer alone (many more pollers would hold up the counter that they watch: 2048^2
+// took 25% longer), which tells the epilogue through a barrier of the slot.
 struct Draws {
-    int* slot;             // this CTA's two slots
-    uint64_t* full;        // this CTA's: a number is there
+    const Draw* slot;      // this CTA's two slots
+    uint64_t* full;        // this CTA's: a tile is there
+    uint64_t* ready;       // this CTA's: and its producer has seen it ready
     uint32_t empty_leader; // the leader's: all readers of both CTAs have taken it
     int i = 0;
-    // The next tile, or a negative number at the end.  By one thread per reader.
-    __device__ __forceinline__ int next(volatile int* abort, unsigned* status) {
+    uint32_t waited = 0;   // phases of `ready`, as bits
+
+    // The next tile; a negative op at the end.  By one thread per reader, which calls taken() when the slot may be
+    // filled again.
+    __device__ __forceinline__ Draw next(volatile int* abort, unsigned* status) {
         const int k = i & 1;
-        if (!mbar_wait_cluster(&full[k], (i >> 1) & 1, abort, status)) return -1;
-        const int t = *reinterpret_cast<volatile int*>(&slot[k]);
-        mbar_arrive_cluster(empty_leader + 8u * k);
-        ++i;
-        return t;
+        Draw d;
+        d.op = -1;
+        if (!mbar_wait_cluster(&full[k], (i >> 1) & 1, abort, status)) return d;
+        asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(d.op), "=r"(d.b), "=r"(d.m0), "=r"(d.n0)
+                     : "r"(smem_u32(&slot[k]))
+                     : "memory");
+        return d;
     }
+    __device__ __forceinline__ void taken() {
+        mbar_arrive_cluster(empty_leader + 8u * (i & 1));
+        ++i;
+    }
+    // For the epilogue, before taken(): the producer's word that an unready tile is ready.
+    __device__ __forceinline__ bool wait_ready(volatile int* abort, unsigned* status) {
+        const int k = i & 1;
+        const bool ok = mbar_wait(&ready[k], (waited >> k) & 1u, abort, status);
+        waited ^= 1u << k;
+        return ok;
+    }
+    __device__ __forceinline__ void tell_ready() const { mbar_arrive(&ready[i & 1]); }
 };
+__device__ __forceinline__ void put_draw(uint32_t cluster_addr, const Draw& d) {
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(d.op), "r"(d.b), "r"(d.m0), "r"(d.n0)
+                 : "memory");
+}
 constexpr int kReaders = 1 + 1 + 8 + 1 + 8;   // producer, issuer, epilogue warps; producer, epilogue warps
 
 __device__ __forceinline__ int stg_off64(int row, int seg) { return row * 64 + 16 * (seg ^ ((row >> 1) & 3)); }
@@ -199,7 +233,9 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
     uint64_t* dempty_bar = bars + 2 * STAGES + 6;   // leader: every reader has it
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* draw_slot = reinterpret_cast<int*>(tmem_slot + 2);
+    uint64_t* ready_bar = bars + 2 * STAGES + 10;   // both: the producer has seen a tile ready
+    Draw* draw_slot = reinterpret_cast<Draw*>(bars + 2 * STAGES + 12);      // 16-byte aligned
+    static_assert((2 * STAGES + 12) * 8 % 16 == 0 && (2 * STAGES + 12) * 8 + 2 * sizeof(Draw) <= BAR_BYTES, "draws' slots");
     unsigned* dev_status = g.status;
 
     const int warp = threadIdx.x >> 5;
@@ -216,6 +252,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             mbar_init(&tempty_bar[a], 2 * EPI_THREADS);
             mbar_init(&dfull_bar[a], 1);
             mbar_init(&dempty_bar[a], kReaders);
+            mbar_init(&ready_bar[a], 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -230,50 +267,61 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t full_leader = mapa_shared(smem_u32(full_bar), 0);
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty_bar), 0);
-    Draws draws = {draw_slot, dfull_bar, mapa_shared(smem_u32(dempty_bar), 0)};
+    Draws draws = {draw_slot, dfull_bar, ready_bar, mapa_shared(smem_u32(dempty_bar), 0)};
 
     if (warp == 3 && lane == 0 && rank == 0) {
         // ------------------------------------------------------------ draws tiles
-        const uint32_t peer_slot = mapa_shared(smem_u32(draw_slot), 1), peer_full = mapa_shared(smem_u32(dfull_bar), 1);
+        uint32_t slot_at[2], full_at[2];
+        for (uint32_t r = 0; r < 2; ++r) {
+            slot_at[r] = mapa_shared(smem_u32(draw_slot), r);
+            full_at[r] = mapa_shared(smem_u32(dfull_bar), r);
+        }
         int op = 0;
         for (int i = 0;; ++i) {
             const int k = i & 1;
-            int t = atomicAdd(g.ticket, 1);
+            const int t = atomicAdd(g.ticket, 1);
+            Draw d;
+            d.op = -1;
+            if (t < g.tiles) d = draw_of(g, t, op);
             if (!mbar_wait_cluster(&dempty_bar[k], ((i >> 1) & 1) ^ 1u, abort_flag, dev_status)) break;
-            if (t >= g.tiles) {
-                t = -1;
-            } else {
-                // Waiting here, a tile ahead, keeps the readers' pipelines full; what the earlier operations
-                // wrote becomes visible to them with the number.
-                const Tile ti = tile_at(g, t, op);
-                if (!wait_done(g.cls[g.op[op].cls].done + ti.b, g.op[op].need, abort_flag, dev_status)) t = -1;
-                fence_proxy_global();
+            if (d.op >= 0) {
+                // What the earlier operations wrote becomes visible to the readers with the tile.  They wait
+                // themselves only where it is not ready now: a tile ahead, it mostly is.
+                if (load_done(g.cls[g.op[op].cls].done + d.b) < g.op[op].need) d.op |= kUnready;
+                else fence_proxy_global();
             }
-            *reinterpret_cast<volatile int*>(&draw_slot[k]) = t;
-            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_slot + 4u * k), "r"(t) : "memory");
-            mbar_arrive_cluster(mapa_shared(smem_u32(&dfull_bar[k]), 0));
-            mbar_arrive_cluster(peer_full + 8u * k);
-            if (t < 0) break;
+            for (int r = 0; r < 2; ++r) {
+                put_draw(slot_at[r] + k * static_cast<uint32_t>(sizeof(Draw)), d);
+                mbar_arrive_cluster(full_at[r] + 8u * k);
+            }
+            if (d.op < 0) break;
+            // A pair that waits draws no further tiles: they would be others' to start when they all are ready.
+            if ((d.op & kUnready) && !mbar_wait_cluster(&dempty_bar[k], (i >> 1) & 1, abort_flag, dev_status)) break;
         }
     } else if (warp == 0 && lane == 0) {
         // ------------------------------------------------------------ TMA producer
         uint32_t stage = 0, phase = 0;
         bool ok = true;
-        int op = 0;
         int issued_parity[STAGES];
 #pragma unroll
         for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
-        for (int t; ok && (t = draws.next(abort_flag, dev_status)) >= 0;) {
-            const Tile ti = tile_at(g, t, op);
-            const ChainOp& P = g.op[op];
+        for (Draw ti; ok && (ti = draws.next(abort_flag, dev_status)).op >= 0;) {
+            const ChainOp& P = g.op[ti.op & (kUnready - 1)];
             const ChainClass& c = g.cls[P.cls];
+            if (ti.op & kUnready) {
+                if (!wait_done(c.done + ti.b, P.need, abort_flag, dev_status)) { ok = false; break; }
+                draws.tell_ready();
+                fence_proxy_global();
+            }
+            draws.taken();
+            const Shape z = shape_of(c, P);
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
             const int am0 = ti.m0 + HM * static_cast<int>(rank);
-            const int hn = ti.w / 2;                      // columns of B that this CTA uses: 128, 64 or 32
+            const int hn = z.w / 2;                      // columns of B that this CTA uses: 128, 64 or 32
             const int bn0 = ti.n0 + hn * static_cast<int>(rank);
             const int b_chunks = (hn + 63) / 64;          // boxes of 64 (rows or columns) x 64
-            const int kblocks = (ti.K + BK - 1) / BK;
+            const int kblocks = (z.K + BK - 1) / BK;
             for (int seg = 0; seg < P.nseg && ok; ++seg) {
                 const CUtensorMap* ta = &c.map[P.ma[seg]];
                 const CUtensorMap* tb = &c.map[P.mb[seg]];
@@ -313,14 +361,14 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
         // ------------------------------------------------------------ MMA issuer (leader)
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
         bool ok = true;
-        int op = 0;
-        for (int t; ok && (t = draws.next(abort_flag, dev_status)) >= 0;) {
-            const Tile ti = tile_at(g, t, op);
-            const ChainOp& P = g.op[op];
+        for (Draw ti; ok && (ti = draws.next(abort_flag, dev_status)).op >= 0;) {
+            draws.taken();
+            const ChainOp& P = g.op[ti.op & (kUnready - 1)];
+            const Shape z = shape_of(g.cls[P.cls], P);
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
-            const uint32_t idesc = idesc_f16_f32(BM, ti.w, a_mn, b_mn);
-            const int kblocks = (ti.K + BK - 1) / BK * P.nseg;
+            const uint32_t idesc = idesc_f16_f32(BM, z.w, a_mn, b_mn);
+            const int kblocks = (z.K + BK - 1) / BK * P.nseg;
             if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag, dev_status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
@@ -364,22 +412,31 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
         uint8_t* stg_e = stg + 2 * STG_BYTES;          // the planes of E
         const int crow = lane >> 2, cseg = lane & 3;   // coalesced layout: rows crow + 8i, segment cseg
         uint32_t acc = 0, acc_phase = 0;
-        int op = 0;
         while (true) {
-            int t = 0;
-            if (lane == 0) t = draws.next(abort_flag, dev_status);
-            t = __shfl_sync(0xffffffffu, t, 0);
-            if (t < 0) break;
-            const Tile ti = tile_at(g, t, op);
-            const ChainOp& P = g.op[op];
+            Draw ti;
+            ti.op = -1;
+            if (lane == 0) {
+                ti = draws.next(abort_flag, dev_status);
+                if (ti.op >= 0) {
+                    if (ti.op & kUnready) ti.op = draws.wait_ready(abort_flag, dev_status) ? ti.op & (kUnready - 1) : -1;
+                    draws.taken();
+                }
+            }
+            ti.op = __shfl_sync(0xffffffffu, ti.op, 0);
+            if (ti.op < 0) break;
+            ti.b = __shfl_sync(0xffffffffu, ti.b, 0);
+            ti.m0 = __shfl_sync(0xffffffffu, ti.m0, 0);
+            ti.n0 = __shfl_sync(0xffffffffu, ti.n0, 0);
+            const ChainOp& P = g.op[ti.op];
             const ChainClass& cl = g.cls[P.cls];
+            const Shape z = shape_of(cl, P);
             float f = 1.0f;
             if (P.pow != 0) {
                 const float x = cl.info[static_cast<size_t>(ti.b) * kStackInfo];
                 f = P.pow == 1 ? x : x * x;
             }
             const float alpha = P.alpha * f, beta = P.beta * f;
-            const int c_beg = ((warp - 4) >> 2) * (ti.w / 64), c_end = c_beg + ti.w / 64;   // this warp's chunks of 32 columns
+            const int c_beg = ((warp - 4) >> 2) * (z.w / 64), c_end = c_beg + z.w / 64;   // this warp's chunks of 32 columns
             const bool sym = (P.flags & kStackSym) != 0;
             const bool bf = (P.flags & kStackOutBf16) != 0;
             const int row0 = ti.m0 + HM * static_cast<int>(rank) + q * 32;
@@ -391,19 +448,19 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const __half* e1 = plane_of(P.e[1], P.es[1]);
             __half* o_plane[2] = {plane_of(P.o[0], P.os[0]), plane_of(P.o[1], P.os[1])};
             const int planes = o_plane[1] != nullptr ? 2 : 1;
-            const int e_ld = ti.N, o_ld = cl.plane[P.o[0]].ld;
-            const int m_out = P.o[0] == kPlaneOut ? cl.rows : ti.M;
+            const int e_ld = z.N, o_ld = cl.plane[P.o[0]].ld;
+            const int m_out = P.o[0] == kPlaneOut ? cl.rows : z.M;
             const uint32_t t_row = tmem_base + acc * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
 
             // E of chunk c goes into staging by cp.async while the chunk before is packed and stored.
             auto prefetch_e = [&](int c) {
                 const int col0 = ti.n0 + c * 32;
-                if (e0 != nullptr && col0 < ti.N && !(sym && col0 + 31 < row0)) {
+                if (e0 != nullptr && col0 < z.N && !(sym && col0 + 31 < row0)) {
                     const int cc = col0 + 8 * cseg;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int rr = row0 + crow + 8 * i;
-                        const bool in = rr < ti.M && cc < ti.N;
+                        const bool in = rr < z.M && cc < z.N;
                         const size_t at = in ? static_cast<size_t>(rr) * e_ld + cc : 0;
                         cp_async16_zfill(stg_e + stg_off64(crow + 8 * i, cseg), e0 + at, in ? 16 : 0);
                         if (e1 != nullptr)
@@ -421,7 +478,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
 #pragma unroll 1
             for (int c = c_beg; c < c_end; ++c) {
                 const int col0 = ti.n0 + c * 32;
-                if (col0 >= ti.N) break;  // uniform across the warp
+                if (col0 >= z.N) break;  // uniform across the warp
                 const bool below = sym && col0 < row0;    // its mirror image is stored instead
                 const bool mirror = sym && col0 > row0;   // a chunk on the diagonal holds both halves
                 uint32_t r[32];
@@ -474,7 +531,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int rr = row0 + crow + 8 * i, cc = col0 + 8 * cseg;
-                        if (rr < m_out && cc < ti.N) {
+                        if (rr < m_out && cc < z.N) {
                             const size_t at = static_cast<size_t>(rr) * o_ld + cc;
                             *reinterpret_cast<uint4*>(o_plane[0] + at) =     // bf16: the same 2 bytes
                                 *reinterpret_cast<const uint4*>(stg + stg_off64(crow + 8 * i, cseg));
@@ -489,7 +546,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int rr = col0 + crow + 8 * i, cc = row0 + 8 * cseg;
-                            if (rr < ti.N && cc < ti.M)
+                            if (rr < z.N && cc < z.M)
                                 *reinterpret_cast<uint4*>(o_plane[0] + static_cast<size_t>(rr) * o_ld + cc) =
                                     *reinterpret_cast<const uint4*>(stg_t + stg_off64(crow + 8 * i, cseg));
                         }
