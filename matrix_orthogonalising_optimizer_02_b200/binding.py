@@ -558,6 +558,29 @@ def ns_orthogonalize_stacks_backward(grads: Sequence[Stack], schedule: Schedule,
                                                        ws_bytes, st), "ns_orthogonalize_stacks_backward")
 
 
+def orthogonalize_alloc(stacks: Sequence[Stack], schedule: Schedule, keep: bool = False):
+    """ns_orthogonalize_stacks on torch's current stream with buffers of its own; returns the `saved`
+    buffer if `keep`, else None."""
+    arr, device = _stack_descs(stacks)
+    lib, n, sch = _lib(), len(stacks), ctypes.byref(schedule.c)
+    with _On(device, None) as st:
+        ws = workspace(lib.ns_stacks_workspace_size(arr, n, sch, int(keep)), device=device)
+        saved = workspace(lib.ns_stacks_saved_size(arr, n, sch), device=device) if keep else None
+        _check(lib.ns_orthogonalize_stacks(arr, n, sch, saved.data_ptr() if keep else None, saved.numel() if keep else 0,
+                                           ws.data_ptr(), ws.numel(), st), "ns_orthogonalize_stacks")
+    return saved
+
+
+def orthogonalize_backward_alloc(grads: Sequence[Stack], schedule: Schedule, saved):
+    """ns_orthogonalize_stacks_backward on torch's current stream with a workspace of its own."""
+    arr, device = _stack_descs(grads)
+    lib, n, sch = _lib(), len(grads), ctypes.byref(schedule.c)
+    with _On(device, None) as st:
+        ws = workspace(lib.ns_stacks_backward_workspace_size(arr, n, sch), device=device)
+        _check(lib.ns_orthogonalize_stacks_backward(arr, n, sch, saved.data_ptr(), saved.numel(), ws.data_ptr(), ws.numel(),
+                                                    st), "ns_orthogonalize_stacks_backward")
+
+
 def muon_stacks_workspace_size(stacks: Sequence[MuonStack], hp) -> int:
     return int(_lib().muon_stacks_workspace_size(_muon_stack_descs(stacks)[0], len(stacks), ctypes.byref(hp[0])))
 

@@ -33,13 +33,9 @@ def _unit_last(t):
 class _Orthogonalize(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, schedule, dtype):
-        x3 = _unit_last(x.detach())
         y = torch.empty(x.shape, dtype=dtype, device=x.device)
-        st = [mb.Stack(x3, y)]
         need = ctx.needs_input_grad[0]
-        ws = mb.workspace(mb.ns_stacks_workspace_size(st, schedule, need), device=x.device)
-        saved = mb.workspace(mb.ns_stacks_saved_size(st, schedule), device=x.device) if need else None
-        mb.ns_orthogonalize_stacks(st, schedule, ws, saved=saved)
+        saved = mb.orthogonalize_alloc([mb.Stack(_unit_last(x.detach()), y)], schedule, keep=need)
         ctx.schedule, ctx.dtype = schedule, x.dtype
         if need:
             ctx.save_for_backward(saved)
@@ -52,9 +48,7 @@ class _Orthogonalize(torch.autograd.Function):
         if dy.dtype not in (torch.bfloat16, torch.float16, torch.float32):
             dy = dy.float()
         dx = torch.empty(dy.shape, dtype=ctx.dtype, device=dy.device)
-        st = [mb.Stack(_unit_last(dy), dx)]
-        ws = mb.workspace(mb.ns_stacks_backward_workspace_size(st, ctx.schedule), device=dy.device)
-        mb.ns_orthogonalize_stacks_backward(st, ctx.schedule, saved, ws)
+        mb.orthogonalize_backward_alloc([mb.Stack(_unit_last(dy), dx)], ctx.schedule, saved)
         return dx, None, None
 
 
