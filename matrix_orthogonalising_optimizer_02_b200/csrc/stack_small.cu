@@ -407,7 +407,7 @@ struct SmallParams {
     SmallStackClass k;
     int n;
 };
-constexpr int kFewItems = 6;
+constexpr int kFewItems = 5;
 static_assert(sizeof(SmallParams<kFewItems>) <= 4096, "the small form's parameters launch faster");
 
 template <int N>
@@ -566,6 +566,37 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     __syncthreads();
     if (C > 1) cluster_arrive();      // staging is over: peers may write into this CTA's buffers
 
+    // What the reverse pass reads, kept as it lies in shared memory (thread 0): X^_t from every CTA, A_t and
+    // B~_t from the first.
+    const bool keep = k.saved != 0;
+    const int keep_z = keep ? it.at + static_cast<int>(b) : 0;
+    auto keep_x = [&](int t) {
+        for (int j = 0; j < nchunk; ++j) {
+            const int x = slab.first(j);
+            if (x >= k.cols) break;
+            for (int y = 0; y < k.rows; y += 64)
+                tma_store_3d(&k.x, smem_u32(panels) + j * PANEL + y * 128, x, y, t * k.saved + keep_z);
+        }
+        bulk_commit();
+    };
+    auto keep_square = [&](const CUtensorMap* m, const uint8_t* src, int t) {
+        if (rank != 0) return;
+        for (int x = 0; x < k.rows; x += 64)
+            for (int y = 0; y < k.rows; y += 64)
+                tma_store_3d(m, smem_u32(src) + (x >> 6) * PANEL + y * 128, x, y, t * k.saved + keep_z);
+        bulk_commit();
+    };
+    if (keep && tid == 0) {
+        keep_x(0);
+        if (rank == 0) {
+            float* info = k.info + static_cast<size_t>(keep_z) * kStackInfo;
+            info[0] = !fin ? NAN : norm > 0.0 ? k.f0 : 0.f;
+            info[1] = 1.f;
+            info[2] = static_cast<float>(1.0 / (norm + static_cast<double>(k.eps)));
+            info[3] = static_cast<float>(norm);
+        }
+    }
+
     // ---------------------------------------------------------------- iterations
     const bool spill = w > ACC;
     const int rc = 128 / C;                        // rows of the Gram matrix that a CTA owns
@@ -671,6 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                 tc_mma_bf16(tmem + ACC, d, d, idesc, s > 0);
             }
             tc_commit(&bar_square);
+            if (keep) keep_square(&k.a, Am, t);
         }
         mbar_wait(&bar_square, phase, abort, status);
         __syncwarp();
@@ -695,6 +727,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         tc_fence_before();
         __syncthreads();
         if (tid == 0) {
+            if (keep) keep_square(&k.b, Bm, t);
             tc_fence_after();
             for (int n0 = 0; n0 < w; n0 += 256) {
                 const int n = min(256, w - n0);
@@ -715,6 +748,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             mbar_wait(&bar_apply[n0 >> 8], phase, abort, status);
             __syncwarp();
             tc_fence_after();
+            if (keep && n0 == 0) {     // nothing is overwritten before it has been kept
+                if (tid == 0) bulk_wait_read<0>();
+                __syncthreads();
+            }
             if (!last && n0 + 256 >= w && C > 1) cluster_arrive();   // this CTA's A, B~ and partial rows are done with
             const int nq = min(256, w - n0) >> 2;
             if (!last)
@@ -728,6 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             fence_async_proxy();
             tc_fence_before();
             __syncthreads();
+            if (keep && tid == 0) keep_x(t + 1);
         }
     }
 

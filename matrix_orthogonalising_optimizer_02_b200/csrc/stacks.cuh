@@ -151,6 +151,7 @@ struct alignas(64) SmallStackItem {
     long long g_stride, m_stride, w_stride;
     int g_ld, m_ld, w_ld;
     int count, block0;
+    int at;               // place of the first block in the class's saved planes
     int g_dtype, w_dtype;
     int vec;              // bit 0: G, bit 1: M, bit 2: W go by TMA
     float decay, step;
@@ -160,7 +161,11 @@ struct SmallStackIter {
     float ga, diag;       // fp16 A = ga * Gram - diag on the diagonal
     float pb, pc;         // B~ = pb * A + pc * A^2
 };
-struct SmallStackClass {
+struct alignas(64) SmallStackClass {
+    CUtensorMap x, a, b;  // saved planes of wide blocks: X^_t, A_t and B~_t in slot t of `saved` blocks
+    float* info;          // kStackInfo floats per saved block
+    int saved;            // 0: nothing is kept
+    float f0;             // X_0 = f0 * X^_0
     SmallStackIter it[32];
     int rows, cols, cluster, slab, iters;   // slab: a multiple of 64, cluster * slab >= long side
     float unit, out;      // Z_0 = unit * X_0; X_T = out * Z

@@ -106,6 +106,7 @@ struct StackClass {
     int rows = 0, cols = 0, count = 0;
     int rp = 0, cp = 0, r = 0, s = 0, r8 = 0;   // padded sides; true and padded shorter side
     bool tall = false;
+    bool chip = false;                           // iterates on chip, also where its iterates are kept
     int chunks = 0, per = 1;                     // chunks of a block in the elementwise passes
     std::vector<double> alpha, gamma, tau;       // tau[0] unused: X_0 = f0 * plane
     std::vector<double> shift, a, b;             // l; a + bl + cl^2 and b + 2cl (a and b without a shift)
@@ -156,7 +157,8 @@ StackClass make_class(int rows, int cols, const muon_ns_schedule& sch, const Bou
 // The scales of a class whose blocks run in one cluster each (stack_small.cu), or false where they do not:
 // a long side above 8 slabs, or a schedule whose product of coefficients a leaves the range in which the
 // state's unit keeps X^ and B~ inside fp16.
-bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, const Bounds& bd, SmallStackClass& k) {
+bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, const Bounds& bd, SmallStackClass& k,
+                 std::vector<double>* kappas = nullptr) {
     const int r = std::min(rows, cols), s = std::max(rows, cols);
     if (r > kSmallStackSide || s > 8 * kSmallStackSlab) return false;
     const StackClass c = make_class(rows, cols, sch, bd);
@@ -181,6 +183,7 @@ bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, co
         pa *= c.a[t];
         const double kappa = unit / (pa * tau);
         if (!(kappa >= 0.0625 && kappa * 2.0 * bd.bmax[t] <= 2.0 * kTop)) return false;
+        if (kappas) kappas->push_back(kappa);
         f.pb = static_cast<float>(kappa * c.b[t] / c.alpha[t]);
         f.pc = static_cast<float>(kappa * sch.coeffs[3 * t + 2] / (c.alpha[t] * c.alpha[t]));
     }
@@ -190,6 +193,7 @@ bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, co
     k.unit = static_cast<float>(unit);
     k.out = static_cast<float>(pa / unit);
     k.eps = sch.eps;
+    k.f0 = static_cast<float>(1.0 / tau0);
     // As few CTAs as hold the block; more while all blocks' CTAs still run at once.  Up to 256 columns
     // one CTA is faster than several that have to exchange their sums.
     const int pieces = (s + 63) / 64;
@@ -455,9 +459,10 @@ muon_status launch_pass(StackPass pass, std::vector<StackItem>& items, const Sta
 }
 
 // Class order of the launches: the longest sums first, so that the last tiles are short ones.
-std::vector<int> class_order(const Group& g) {
-    std::vector<int> o(g.classes.size());
-    for (size_t i = 0; i < o.size(); ++i) o[i] = static_cast<int>(i);
+std::vector<int> class_order(const Group& g, bool on_chip_too) {
+    std::vector<int> o;
+    for (size_t i = 0; i < g.classes.size(); ++i)
+        if (on_chip_too || !g.classes[i].chip) o.push_back(static_cast<int>(i));
     std::stable_sort(o.begin(), o.end(), [&](int x, int y) { return g.classes[x].s > g.classes[y].s; });
     return o;
 }
@@ -472,7 +477,7 @@ struct Direct {
 muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vector<Direct>& direct, int* tickets,
                            const Call& call) {
     const int T = sch.n_iters;
-    const std::vector<int> order = class_order(g);
+    const std::vector<int> order = class_order(g, false);
     std::vector<ChainClass> classes(g.classes.size());
     for (size_t k = 0; k < classes.size(); ++k) {
         if (!chain_class(classes[k], g.classes[k]))
@@ -532,7 +537,7 @@ muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vec
             }
         }
     }
-    return launch_chain(classes, ops, 3 * static_cast<int>(classes.size()), flops, tickets, call);
+    return launch_chain(classes, ops, 3 * static_cast<int>(order.size()), flops, tickets, call);
 }
 
 // ---------------------------------------------------------------- arguments
@@ -679,6 +684,59 @@ const uint8_t* bytes_at(const void* p, long long blocks, long long stride, int d
 }
 
 // ---------------------------------------------------------------- forward
+// Where iterates are kept for the reverse pass: wide blocks that run on chip keep them from there, with B_t
+// scaled as it is there (a tall block's X^ lies the wrong way for that).
+void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
+    for (StackClass& c : g.classes) {
+        SmallStackClass k;
+        std::vector<double> kappas;
+        if (c.tall || !small_class(c.rows, c.cols, c.count, sch, bd, k, &kappas)) continue;
+        c.chip = true;
+        c.gamma = kappas;
+    }
+}
+SmallStackItem small_item(const ns_stack_desc& s, int first, int count) {
+    SmallStackItem it;
+    std::memset(&it, 0, sizeof(it));
+    it.G = bytes_at(s.X, first, s.x_stride, s.x_dtype);
+    it.W = const_cast<uint8_t*>(bytes_at(s.Y, first, s.y_stride, s.y_dtype));
+    it.g_stride = s.x_stride;
+    it.w_stride = s.y_stride;
+    it.g_ld = s.x_ld;
+    it.w_ld = s.y_ld;
+    it.g_dtype = s.x_dtype;
+    it.w_dtype = s.y_dtype;
+    it.count = count;
+    it.step = 1.f;
+    small_stack_maps(it, s.rows, s.cols);
+    return it;
+}
+// The on-chip classes of a group whose iterates are kept.
+muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedule& sch, const Bounds& bd, const Call& call) {
+    for (size_t k = 0; k < g.classes.size(); ++k) {
+        const StackClass& c = g.classes[k];
+        if (!c.chip) continue;
+        SmallStackClass q;
+        if (!small_class(c.rows, c.cols, c.count, sch, bd, q)) return MUON_ERR_INVALID_ARG;
+        const int n = sch.n_iters * c.count;
+        if (!encode_stack_tmap(&q.x, c.X, c.rp, c.cp, n) || !encode_stack_tmap(&q.a, c.A, c.r8, c.r8, n) ||
+            !encode_stack_tmap(&q.b, c.B, c.r8, c.r8, n))
+            return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        q.info = c.info;
+        q.saved = c.count;
+        q.status = call.status;
+        std::vector<SmallStackItem> items;
+        for (const Part& p : g.parts) {
+            if (p.cls != static_cast<int>(k)) continue;
+            items.push_back(small_item(d[p.stack], p.first, p.count));
+            items.back().at = p.at;
+        }
+        const muon_status st = launch_small(items, q, small_flops(q, c.count), call);
+        if (st != MUON_OK) return st;
+    }
+    return MUON_OK;
+}
+
 muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shapes, std::vector<SmallSet>& small,
                           const muon_ns_schedule& sch, const Bounds& bd, void* saved, void* workspace, const Call& call) {
     const bool saving = saved != nullptr;
@@ -694,22 +752,8 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
         std::vector<SmallStackItem> items;
         double blocks = 0.0;
         for (int i : set.stacks) {
-            const ns_stack_desc& s = d[i];
-            SmallStackItem it;
-            std::memset(&it, 0, sizeof(it));
-            it.G = s.X;
-            it.W = s.Y;
-            it.g_stride = s.x_stride;
-            it.w_stride = s.y_stride;
-            it.g_ld = s.x_ld;
-            it.w_ld = s.y_ld;
-            it.g_dtype = s.x_dtype;
-            it.w_dtype = s.y_dtype;
-            it.count = s.count;
-            it.step = 1.f;
-            small_stack_maps(it, s.rows, s.cols);
-            items.push_back(it);
-            blocks += s.count;
+            items.push_back(small_item(d[i], 0, d[i].count));
+            blocks += d[i].count;
         }
         set.k.status = call.status;
         const muon_status st = launch_small(items, set.k, small_flops(set.k, blocks), call);
@@ -722,6 +766,16 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
         sv.used = kept;
         layout_forward(g, T, saving, ws, sv);
         kept = align_up(sv.used, kAlign);
+        if (saving) mark_chip(g, sch, bd);
+        bool any_chip = false;
+        for (const StackClass& c : g.classes) any_chip = any_chip || c.chip;
+        if (any_chip) {
+            muon_status st = MUON_OK;
+            if (first) st = clear_status(call);
+            first = false;
+            if (st == MUON_OK) st = keep_on_chip(g, d, sch, bd, call);
+            if (st != MUON_OK) return st;
+        }
         std::vector<Direct> direct(g.classes.size());
         std::vector<int> parts_of(g.classes.size(), 0);
         for (const Part& p : g.parts) ++parts_of[p.cls];
@@ -729,6 +783,7 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
         double read = 0.0, written = 0.0;
         for (const Part& p : g.parts) {
             const StackClass& c = g.classes[p.cls];
+            if (c.chip) continue;
             const ns_stack_desc& s = d[p.stack];
             StackItem it = base_item(c, p);
             const double n = static_cast<double>(p.count) * c.rows * c.cols;
@@ -759,6 +814,7 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
                 written += n * elem_size(s.y_dtype);
             }
         }
+        if (in.empty()) continue;
         StackPassArgs args = {};
         args.eps = sch.eps;
         args.status = first ? call.status : nullptr;
@@ -791,9 +847,10 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
         sv.base = static_cast<uint8_t*>(const_cast<void*>(saved));
         sv.used = kept;
         layout_forward(g, T, true, fw, sv);   // the saved planes' places
+        mark_chip(g, sch, bd);
         kept = align_up(sv.used, kAlign);
         std::vector<GradPlanes> gp = layout_backward(g, ws);
-        const std::vector<int> order = class_order(g);
+        const std::vector<int> order = class_order(g, true);
         const size_t nc = g.classes.size();
 
         // delta[k][t]: D_t's planes hold D_t * 2^k * delta_t
