@@ -134,7 +134,20 @@ def clip_scale(params, max_norm: float, workspaces=None):
     return out
 
 
-class StackedMuon(torch.optim.Optimizer):
+class _Fp32State(torch.optim.Optimizer):
+    """Keeps its state in fp32 through load_state_dict, which casts it to the parameter's type otherwise."""
+
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        saved = [i for g in state_dict["param_groups"] for i in g["params"]]
+        params = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(saved, params):
+            for k, v in state_dict["state"].get(i, {}).items():
+                if torch.is_tensor(v):
+                    self.state[p][k] = v.to(device=p.device, dtype=torch.float32, copy=True)
+
+
+class StackedMuon(_Fp32State):
     """The Muon step on blocks of parameters: a 3-D parameter [count, rows, cols] is a stack of blocks
     (experts); a 2-D one is a block, or, with the group option ``row_block`` or ``col_block``, a stack
     of blocks of that many rows or columns (heads of a fused QKV weight, the halves of a fused gate/up
@@ -152,6 +165,10 @@ class StackedMuon(torch.optim.Optimizer):
                 if p.dtype not in (torch.bfloat16, torch.float16, torch.float32):
                     raise ValueError(f"unsupported parameter dtype {p.dtype}")
                 self._blocks(p, g)
+        self._ws = _Workspaces()
+
+    def __setstate__(self, state):     # copies and pickles carry the state alone
+        super().__setstate__(state)
         self._ws = _Workspaces()
 
     @staticmethod
@@ -193,7 +210,7 @@ class StackedMuon(torch.optim.Optimizer):
         return loss
 
 
-class AdamW(torch.optim.Optimizer):
+class AdamW(_Fp32State):
     """AdamW for what Muon does not take, one grouped call per param group.  Parameters of any shape,
     dense, bf16, fp16 or fp32; moments in fp32."""
 
