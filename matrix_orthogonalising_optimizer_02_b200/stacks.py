@@ -34,11 +34,9 @@ class _Orthogonalize(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, schedule, dtype):
         y = torch.empty(x.shape, dtype=dtype, device=x.device)
-        need = ctx.needs_input_grad[0]
-        saved = mb.orthogonalize_alloc([mb.Stack(_unit_last(x.detach()), y)], schedule, keep=need)
+        saved = mb.orthogonalize_alloc([mb.Stack(_unit_last(x.detach()), y)], schedule, keep=True)
         ctx.schedule, ctx.dtype = schedule, x.dtype
-        if need:
-            ctx.save_for_backward(saved)
+        ctx.save_for_backward(saved)
         return y
 
     @staticmethod
@@ -55,7 +53,10 @@ class _Orthogonalize(torch.autograd.Function):
 def orthogonalize(x, steps: int = 5, coeffs=KJ_COEFFS, eps: float = 1e-7, dtype=None):
     """Every [rows, cols] block of x ([rows, cols] or [count, rows, cols]; bf16, fp16 or fp32) after
     `steps` Newton-Schulz iterations with `coeffs` ((a, b, c), or a sequence of `steps` of them), in
-    `dtype` (x's own if None).  Differentiable with respect to x, once.
+    `dtype` (x's own if None).  Differentiable with respect to x, once; without a gradient to come (no
+    grad mode, an input that needs none) no iterates are kept.  Forward and backward can be captured in
+    a CUDA graph; as for any backward pass, no graph of the same leaves made outside the capture may
+    still be alive then.
 
     With the optimizer's coefficients the singular values of the result lie near 1 (0.7 to 1.2); a
     parametrisation that needs orthonormal blocks takes converging ones, such as (1.875, -1.25, 0.375).
@@ -65,4 +66,9 @@ def orthogonalize(x, steps: int = 5, coeffs=KJ_COEFFS, eps: float = 1e-7, dtype=
     per_step = [tuple(coeffs)] * steps if not isinstance(coeffs[0], (tuple, list)) else coeffs
     if len(per_step) != steps:
         raise ValueError(f"{len(per_step)} coefficient triples for {steps} steps")
-    return _Orthogonalize.apply(x, mb.Schedule(per_step, eps=eps), dtype if dtype is not None else x.dtype)
+    schedule, dtype = mb.Schedule(per_step, eps=eps), dtype if dtype is not None else x.dtype
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _Orthogonalize.apply(x, schedule, dtype)
+    y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    mb.orthogonalize_alloc([mb.Stack(_unit_last(x.detach()), y)], schedule)
+    return y
