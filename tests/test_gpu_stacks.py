@@ -473,3 +473,193 @@ def test_a_training_step_of_all_of_them():
                 w, m, v = ref.adamw(old[n], p.grad, s[0], s[1], t, 1e-2, 0.9, 0.95, 1e-8, 0.01, gs=gs)
                 assert ref.rel(p, w) <= 1e-5, n
                 s[0], s[1] = m, v
+
+
+# ---------------------------------------------------------------- how calls are made
+_FRESH = """
+import torch
+from matrix_orthogonalising_optimizer_02_b200 import binding as mb, stacks as ms
+x = torch.randn({shape}, device="cuda")
+dy = torch.randn_like(x)
+leaf = x.clone().requires_grad_(True)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = ms.orthogonalize(leaf)
+    (dx,) = torch.autograd.grad(y, leaf, dy)
+for seed in range(3):
+    with torch.no_grad():
+        leaf.copy_(torch.randn_like(x))
+    g.replay()
+    torch.cuda.synchronize()
+    got = y.detach().clone(), dx.clone()
+    twin = leaf.detach().clone().requires_grad_(True)
+    z = ms.orthogonalize(twin)
+    (dz,) = torch.autograd.grad(z, twin, dy)
+    assert torch.equal(got[0], z.detach()) and torch.equal(got[1], dz)
+print("equal")
+"""
+
+
+@pytest.mark.parametrize("shape", [(2, 300, 200), (3, 64, 200), (2, 200, 64)], ids=str)
+def test_first_call_of_a_process_is_a_captured_forward_and_backward(shape):
+    import pathlib
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", _FRESH.format(shape=shape)], capture_output=True, text=True, timeout=300,
+                         cwd=pathlib.Path(__file__).resolve().parents[1])
+    assert out.returncode == 0 and "equal" in out.stdout, out.stderr[-2000:]
+
+
+def test_streams_run_chains_side_by_side():
+    """Two streams, several calls each, workspaces of their own; each equals the call alone."""
+    sch = mb.Schedule.fixed(T)
+    xs = [blocks(90 + i, 4, 320, 400 + 64 * i, BF) for i in range(2)]
+    want = [torch.empty_like(x) for x in xs]
+    for x, y in zip(xs, want):
+        run([mb.Stack(x, y)], sch)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    ys = [[torch.empty_like(x) for _ in range(6)] for x in xs]
+    torch.cuda.synchronize()
+    keep = [run([mb.Stack(xs[i], ys[i][k])], sch, stream=streams[i]) for k in range(6) for i in range(2)]
+    torch.cuda.synchronize()
+    assert all(mb.device_status(ws) == mb.MUON_OK for ws in keep)
+    assert all(torch.equal(y, w) for per, w in zip(ys, want) for y in per)
+
+
+def test_backward_twice_and_many_graphs_alive():
+    x = blocks(100, 3, 150, 222, FP).requires_grad_(True)
+    dy = [blocks(101 + i, 3, 150, 222, FP, std=1.0) for i in range(2)]
+    ys = [ms.orthogonalize(x) for _ in range(2)]
+    first = [torch.autograd.grad(y, x, d, retain_graph=True)[0] for y, d in zip(ys, dy)]
+    again = [torch.autograd.grad(y, x, d)[0] for y, d in zip(ys, dy)]
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    assert ref.rel(first[1][2], ref.ns_grad(x[2].detach(), dy[1][2], [ref.KJ] * T)) <= 2 * ref.tol_kj(FP)
+
+
+def test_no_iterates_are_kept_without_a_gradient(monkeypatch):
+    kept, call = [], mb.orthogonalize_alloc
+    monkeypatch.setattr(mb, "orthogonalize_alloc", lambda s, sch, keep=False: kept.append(keep) or call(s, sch, keep))
+    x = blocks(110, 2, 40, 60, FP).requires_grad_(True)
+    y = ms.orthogonalize(x)
+    with torch.no_grad():
+        z = ms.orthogonalize(x)
+    w = ms.orthogonalize(x.detach())
+    assert kept == [True, False, False] and y.requires_grad and not z.requires_grad and not w.requires_grad
+    for v in (y, z, w):
+        assert ref.rel(v[1], ref.ns(x[1].detach(), [ref.KJ] * T)) <= ref.tol_kj(FP)
+
+
+def test_many_classes_and_iterations():
+    """More classes than one launch of a chain takes, and more operations."""
+    shapes = [(1, 136 + 8 * i, 300 - 4 * i) for i in range(14)] + [(2, 20 + i, 50) for i in range(3)]
+    coeffs = [ref.STABLE] * 32
+    xs = [blocks(120 + i, *s, FP) for i, s in enumerate(shapes)]
+    ys = [torch.empty_like(x) for x in xs]
+    run([mb.Stack(x, y) for x, y in zip(xs, ys)], mb.Schedule(coeffs))
+    for x, y in zip(xs, ys):   # converging iterations: the last ones contract what went before
+        assert ref.rel(y[-1], ref.ns(x[-1], coeffs)) <= ref.tol_stable(FP)
+
+
+def test_many_stacks_of_longer_sides():
+    """More stacks than one launch of a pass takes, through every pass."""
+    n = 135
+    x = blocks(140, n, 136, 144, FP)
+    xs = [x[i:i + 1] for i in range(n)]
+    dy = blocks(141, n, 136, 144, FP, std=1.0)
+    ys, dx = [torch.empty_like(v) for v in xs], [torch.empty_like(v) for v in xs]
+    sch = mb.Schedule.fixed(T)
+    stacks = [mb.Stack(a, b) for a, b in zip(xs, ys)]
+    saved = mb.workspace(mb.ns_stacks_saved_size(stacks, sch))
+    run(stacks, sch, saved=saved)
+    grads = [mb.Stack(dy[i:i + 1], dx[i]) for i in range(n)]
+    ws = mb.workspace(mb.ns_stacks_backward_workspace_size(grads, sch))
+    mb.ns_orthogonalize_stacks_backward(grads, sch, saved, ws)
+    w = [torch.zeros_like(v) for v in xs]
+    hp = mb.hyper(1.0, 0.0, 0.0, False, "naive", sch)
+    muon = [mb.MuonStack(a, b, torch.zeros_like(b)) for a, b in zip(w, xs)]
+    mb.muon_step_stacks(muon, hp, mb.workspace(mb.muon_stacks_workspace_size(muon, hp)))
+    for i in (0, 63, 127, 128, 134):
+        want = ref.ns(x[i], [ref.KJ] * T)
+        assert ref.rel(ys[i][0], want) <= ref.tol_kj(FP), i
+        assert ref.rel(-w[i][0], want) <= ref.tol_kj(FP), i
+        assert ref.rel(dx[i][0], ref.ns_grad(x[i], dy[i], [ref.KJ] * T)) <= 2 * ref.tol_kj(FP), i
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 96), (150, 200)])
+def test_offsets_beyond_32_bits(rows, cols):
+    """Blocks, and rows, that lie further apart than 2^32 bytes or 2^31 elements reach."""
+    far = 2 ** 32 + 24
+    buf = torch.empty(far + rows * cols, dtype=BF, device="cuda")
+    x = buf.as_strided((2, rows, cols), (far, cols, 1))
+    x.copy_(blocks(150, 2, rows, cols, BF))
+    y = torch.empty((2, rows, cols), device="cuda")
+    run([mb.Stack(x, y)], mb.Schedule.fixed(T))
+    want = [ref.ns(b, [ref.KJ] * T) for b in x]
+    assert all(ref.rel(a, b) <= ref.tol_kj(FP) for a, b in zip(y, want))
+    run([mb.Stack(x, x)], mb.Schedule.fixed(T))
+    assert all(ref.rel(a, b) <= ref.tol_kj(BF) for a, b in zip(x, want))
+    pitch = 2 ** 32 // (rows - 1) & ~7       # the last row begins beyond 2^31 elements
+    z = buf.as_strided((rows, cols), (pitch, 1))
+    z.copy_(blocks(151, 1, rows, cols, BF)[0])
+    y = torch.empty((rows, cols), device="cuda")
+    run([mb.Stack(z, y)], mb.Schedule.fixed(T))
+    assert ref.rel(y, ref.ns(z, [ref.KJ] * T)) <= ref.tol_kj(FP)
+
+
+def test_more_blocks_than_a_group_takes():
+    """The call goes through its blocks in groups of some 5 GiB of workspace."""
+    n = 9000
+    x = blocks(160, n, 200, 264, BF)
+    y = torch.empty_like(x)
+    ws = run([mb.Stack(x, y)], mb.Schedule.fixed(T))
+    assert ws.numel() < 6 * 2 ** 30 and mb.device_status(ws) == mb.MUON_OK
+    for b in list(range(0, n, 1500)) + [n - 1]:
+        assert ref.rel(y[b], ref.ns(x[b], [ref.KJ] * T)) <= ref.tol_kj(BF), b
+    # every block was done: none is left as it was allocated, and all have a full block's norm
+    norms = torch.linalg.vector_norm(y.float(), dim=(1, 2))
+    assert float(norms.min()) > 0.6 * 200 ** 0.5 and float(norms.max()) < 1.3 * 200 ** 0.5
+
+
+def test_a_tensor_beyond_31_bits_of_elements():
+    n = 2 ** 31 + 9
+    w, g = torch.zeros(n, dtype=BF, device="cuda"), torch.zeros(n, dtype=BF, device="cuda")
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    g[-5:] = 3.0
+    g[:4] = 4.0
+    out = torch.empty(2, device="cuda")
+    mb.grad_norm_batched([g], 1.0, out, mb.workspace(mb.grad_norm_workspace_size([g])))
+    assert abs(float(out[0]) - 109 ** 0.5) <= 2.0 ** -22 * 109 ** 0.5
+    mb.adamw_step_batched([mb.AdamWTensor(w, g, m, v)], mb.adamw_hyper(lr=0.5, weight_decay=0.0), 1)
+    # the first step moves every element with a gradient by lr
+    assert bool((w[:4] == -0.5).all()) and bool((w[-5:] == -0.5).all()) and float(w.float().sum()) == -4.5
+
+
+def test_optimizers_carry_their_state_in_fp32():
+    """State dicts, and copies, of bf16 parameters' optimizers go on as the original does."""
+    import copy
+    p = [torch.nn.Parameter(blocks(170, 2, 24, 40, BF, std=0.1)), torch.nn.Parameter(blocks(171, 1, 5, 7, BF, std=0.1)[0])]
+    q = [torch.nn.Parameter(x.detach().clone()) for x in p]
+
+    def make(x):
+        return StackedMuon(x[:1], lr=0.02), AdamW(x[1:], lr=1e-2)
+
+    def step(x, opts, seed):
+        for i, t in enumerate(x):
+            t.grad = blocks(seed + i, *t.shape, BF) if t.dim() == 3 else blocks(seed + i, 1, *t.shape, BF)[0]
+        for o in opts:
+            o.step()
+    a, b = make(p), make(q)
+    step(p, a, 180)
+    for x, y in zip(p, q):
+        y.data.copy_(x.data)
+    for o, n in zip(a, b):
+        n.load_state_dict(copy.deepcopy(o.state_dict()))
+        assert all(v.dtype == FP for s in n.state.values() for v in s.values() if torch.is_tensor(v))
+    step(p, a, 190)
+    step(q, b, 190)
+    assert all(torch.equal(x, y) for x, y in zip(p, q))
+    twin = copy.deepcopy(a[0])
+    for t in twin.param_groups[0]["params"]:
+        t.grad = blocks(200, 2, 24, 40, BF)
+    twin.step()
