@@ -74,6 +74,8 @@ constexpr int kUnready = 1 << 20;   // the block's earlier operations were not d
 
 struct Shape {
     int M, N, K, w;        // of the operation; w: columns of a tile
+    // Columns of the tile at column n0: the last ones of a row take as many 64s as are left.
+    __device__ __forceinline__ int width(int n0) const { return min(w, (N - n0 + 63) & ~63); }
 };
 __device__ __forceinline__ Shape shape_of(const ChainClass& c, const ChainOp& o) {
     return {o.kind < 2 ? c.r8 : c.rp, o.kind < 2 ? c.r8 : c.cp, o.kind == 0 ? max(c.rp, c.cp) : c.r8, 64 * o.bn};
@@ -318,7 +320,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
             const int am0 = ti.m0 + HM * static_cast<int>(rank);
-            const int hn = z.w / 2;                      // columns of B that this CTA uses: 128, 64 or 32
+            const int hn = z.width(ti.n0) / 2;           // columns of B that this CTA uses: 128, 96, 64 or 32
             const int bn0 = ti.n0 + hn * static_cast<int>(rank);
             const int b_chunks = (hn + 63) / 64;          // boxes of 64 (rows or columns) x 64
             const int kblocks = (z.K + BK - 1) / BK;
@@ -367,7 +369,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             const Shape z = shape_of(g.cls[P.cls], P);
             const bool a_mn = (P.flags & kStackAMn) != 0;
             const bool b_mn = (P.flags & kStackBMn) != 0;
-            const uint32_t idesc = idesc_f16_f32(BM, z.w, a_mn, b_mn);
+            const uint32_t idesc = idesc_f16_f32(BM, z.width(ti.n0), a_mn, b_mn);
             const int kblocks = (z.K + BK - 1) / BK * P.nseg;
             if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag, dev_status)) { ok = false; break; }
             tc_fence_after();
@@ -436,7 +438,8 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 f = P.pow == 1 ? x : x * x;
             }
             const float alpha = P.alpha * f, beta = P.beta * f;
-            const int c_beg = ((warp - 4) >> 2) * (z.w / 64), c_end = c_beg + z.w / 64;   // this warp's chunks of 32 columns
+            const int chunks = z.width(ti.n0) / 64;
+            const int c_beg = ((warp - 4) >> 2) * chunks, c_end = c_beg + chunks;   // this warp's chunks of 32 columns
             const bool sym = (P.flags & kStackSym) != 0;
             const bool bf = (P.flags & kStackOutBf16) != 0;
             const int row0 = ti.m0 + HM * static_cast<int>(rank) + q * 32;
