@@ -865,6 +865,39 @@ cudaError_t launch(const SmallStackItem* items, int n, const SmallStackClass& k,
 
 }  // namespace
 
+int stack_small_resident(int cluster) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> of[kMaxDevices][4];
+    const int k = cluster >= 8 ? 3 : cluster >= 4 ? 2 : cluster >= 2 ? 1 : 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return 112 / cluster;
+    }
+    int n = of[dev][k].load();
+    if (n == 0) {
+        const auto kernel = stack_small_kernel<kFewItems>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cluster) * 148, 1, 1);
+        cfg.blockDim = dim3(THREADS, 1, 1);
+        cfg.dynamicSmemBytes = smem_bytes(kSmallStackSlab);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = cluster;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kSmallStackSlab)) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            n = 112 / cluster;
+        }
+        of[dev][k].store(n);
+    }
+    return n;
+}
+
 cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
     return n <= kFewItems ? launch<kFewItems>(items, n, k, stream) : launch<kSmallStackItems>(items, n, k, stream);
 }

@@ -142,7 +142,6 @@ cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const Sta
 constexpr int kSmallStackSide = 128;     // longest short side
 constexpr int kSmallStackSlab = 512;     // columns of a CTA's slab at most
 constexpr int kSmallStackItems = 48;    // of a launch: parameters are limited to 32 KB
-constexpr int kSmallStackCtas = 148;     // CTAs (one per SM) that run at once
 struct alignas(64) SmallStackItem {
     CUtensorMap map_g, map_m, map_w;   // where `vec` says that TMA moves the array
     const void* G;
@@ -176,6 +175,8 @@ struct alignas(64) SmallStackClass {
 };
 // Fills the item's maps and `vec` from its arrays.
 void small_stack_maps(SmallStackItem& it, int rows, int cols);
+// Clusters of 1, 2, 4 or 8 CTAs that run at once on the current device (they do not fill it: 14 of 8, not 18).
+int stack_small_resident(int cluster);
 cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream);
 
 }  // namespace muon

@@ -194,12 +194,13 @@ bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, co
     k.out = static_cast<float>(pa / unit);
     k.eps = sch.eps;
     k.f0 = static_cast<float>(1.0 / tau0);
-    // As few CTAs as hold the block; more while all blocks' CTAs still run at once.  Up to 256 columns
-    // one CTA is faster than several that have to exchange their sums.
+    // As few CTAs as hold the block; more while all blocks' clusters still run at once (16 blocks of 96 x 641: 57 us
+    // with 4 CTAs each, 98 with 8, of which two do not start before others end; 12 blocks: 57 and 53).  Up to 256
+    // columns one CTA is faster than several that have to exchange their sums.
     const int pieces = (s + 63) / 64;
     int C = 1;
     while (C * kSmallStackSlab < s) C *= 2;
-    while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && 2ll * C * blocks <= kSmallStackCtas) C *= 2;
+    while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && blocks <= stack_small_resident(2 * C)) C *= 2;
     k.cluster = C;
     k.slab = (pieces + C - 1) / C * 64;
     return true;

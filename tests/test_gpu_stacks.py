@@ -500,7 +500,7 @@ print("equal")
 """
 
 
-@pytest.mark.parametrize("shape", [(2, 300, 200), (3, 64, 200), (2, 200, 64)], ids=str)
+@pytest.mark.parametrize("shape", [(2, 300, 200), (3, 64, 400), (2, 200, 64)], ids=str)
 def test_first_call_of_a_process_is_a_captured_forward_and_backward(shape):
     import pathlib
     import subprocess
