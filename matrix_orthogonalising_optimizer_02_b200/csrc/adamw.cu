@@ -3,6 +3,8 @@
 // Both are HBM-bound: the norm reads each gradient once; AdamW reads W, G, m, v and writes W, m, v
 // once, all arithmetic in fp32 registers.  Descriptors travel as kernel parameters (up to 256 tensors
 // a launch).  A persistent grid walks chunks of 4096 elements, 8 elements a thread at a time.
+// Measured: AdamW on 33e6 bf16 elements 116 us (0.96 of the measured copy rate); the norm of 83e6 45 us (0.57:
+// the conversions to fp64, which keep squares of 1e-20 and 1e30 in range, bind it).
 #include <cmath>
 
 #include "../../include/muon_b200.h"

@@ -28,7 +28,15 @@
 // conflicts, zero-filled and clipped at the block's edges.  (Loads through registers took twice as long,
 // 26 us for a slab of 128 x 512: a quarter of the stalls were instruction fetches of the code for every
 // type and edge, another the loads' latency.  Row by row, bulk copies took 42 us: about 20 ns each.)
-// Arrays whose rows TMA cannot address go element by element through shared memory.
+// Arrays whose rows TMA cannot address go element by element through shared memory.  (TMA clips a store at
+// 16 bytes, no finer, so rows of a broken number of 16-byte pieces are among them.)
+//
+// Where the reverse pass is to follow, the panels of X^_t and the matrices A_t and B~_t leave by TMA as they lie in
+// shared memory, behind the products that read them (16 blocks of 96 x 641: 55 us without, 63 with).
+//
+// Bound: latency of the chain Gram, exchange, A^2, apply (12 blocks of 64 x 768: 50 us for five iterations, the
+// tensor pipe 12% busy).  A cluster of 8 leaves 36 SMs idle (14 run at once); 96 steps of 128 x 4096 are 7 rounds
+// of them, 549 us against 109 for their bytes.
 #include <atomic>
 #include <cmath>
 
