@@ -829,8 +829,402 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     }
 }
 
+// ---------------------------------------------------------------- reverse pass
+// D <- aD + BD + 2PX with S = sym(D X^T), P = bS + c(SA + AS), from the kept X^_t, A_t and B~_t, t falling.
+// The state V = 2^k D stays in TMEM in fp32 (columns 0 ..), the products go to the columns from ACC_G on; X^_t and
+// D^ = fp16(V) lie in panels as above.  S's partial rows are exchanged as the Gram matrix's are; A and B~ come in by
+// TMA over the partial rows when those have been summed, P^ takes S^'s place.  (As a chain of launches' tiles the
+// reverse pass of 16 blocks of 96 x 641 took 160 us.)
+constexpr int ACC_G = 256;
+__host__ __device__ constexpr int grad_smem_bytes(int w) { return 2 * (w / 64) * PANEL + A_BYTES + RED_BYTES + 1024; }
+static_assert(grad_smem_bytes(kSmallGradSlab) + 512 <= 232448, "shared memory above the 227 KB per-CTA limit");
+static_assert(2 * STG_FLOATS * 4 <= PANEL + A_BYTES + RED_BYTES, "two staging buffers fit beside the X panels");
+static_assert(2 * A_BYTES <= RED_BYTES, "A and B~ over the partial rows");
+
 template <int N>
-cudaError_t launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
+struct SmallGradParams {
+    SmallStackItem item[N];
+    SmallGradClass k;
+    int n;
+};
+static_assert(sizeof(SmallGradParams<kFewItems>) <= 4096, "the small form's parameters launch faster");
+
+template <int N>
+__global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __grid_constant__ SmallGradParams<N> p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t bar_s, bar_p, bar_apply, bar_rows, bar_all, bar_ab, bar_x, bar_ring[kRing];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ double red_sum[THREADS / 32];
+    __shared__ double parts[16];
+
+    const SmallGradClass& k = p.k;
+    const int C = k.cluster, w = k.slab, nchunk = w >> 6;
+    uint8_t* Xp = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* Dp = Xp + nchunk * PANEL;
+    uint8_t* Sm = Dp + nchunk * PANEL;             // S^, then P^
+    uint8_t* red = Sm + A_BYTES;                   // partial rows, then A and B~
+    uint8_t* Am = red;
+    uint8_t* Bm = red + A_BYTES;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int blk = static_cast<int>(blockIdx.x) / C;
+    int lo = 0, hi = p.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.item[mid].block0 <= blk) lo = mid; else hi = mid - 1;
+    }
+    const SmallStackItem& it = p.item[lo];
+    const long long b = blk - it.block0;
+    const int kept = it.at + static_cast<int>(b);
+    const int q = warp & 3, cg = warp >> 2, row = 32 * q + lane;
+
+    if (tid == 0) {
+        for (uint64_t* x : {&bar_s, &bar_p, &bar_apply, &bar_rows, &bar_all, &bar_ab, &bar_x}) mbar_init(x, 1);
+        for (uint64_t& x : bar_ring) mbar_init(&x, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    volatile int* abort = &abort_flag;
+    unsigned* status = k.status;
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, false, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
+    const bool tma_in = (it.vec & 1) != 0, tma_out = (it.vec & 4) != 0;
+
+    auto load_x = [&](int t) {     // thread 0
+        mbar_arrive_expect_tx(&bar_x, static_cast<uint32_t>(nchunk * PANEL));
+        for (int j = 0; j < nchunk; ++j)
+            for (int y = 0; y < 128; y += 64)
+                tma_load_3d(smem_u32(Xp) + j * PANEL + y * 128, &k.x, smem_u32(&bar_x), slab.first(j), y, t * k.saved + kept);
+    };
+    auto load_ab = [&](int t) {    // thread 0
+        mbar_arrive_expect_tx(&bar_ab, 2 * A_BYTES);
+        for (int x = 0; x < 128; x += 64)
+            for (int y = 0; y < 128; y += 64) {
+                const uint32_t at = (x >> 6) * PANEL + y * 128;
+                tma_load_3d(smem_u32(Am) + at, &k.a, smem_u32(&bar_ab), x, y, t * k.saved + kept);
+                tma_load_3d(smem_u32(Bm) + at, &k.b, smem_u32(&bar_ab), x, y, t * k.saved + kept);
+            }
+    };
+    // The cluster's sum, in rank order, in every thread of every CTA.
+    auto cluster_sum = [&](double v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) red_sum[warp] = v;
+        __syncthreads();
+        cluster_arrive();      // every CTA of the cluster runs, and is past its last read of `parts`
+        cluster_wait();
+        if (tid < C) {
+            double s = 0.0;
+            for (int i = 0; i < THREADS / 32; ++i) s += red_sum[i];
+            st_cluster_f64(mapa_shared(smem_u32(&parts[rank]), tid), s);
+        }
+        cluster_arrive();
+        cluster_wait();
+        double s = 0.0;
+        for (int i = 0; i < C; ++i) s += parts[i];
+        return s;
+    };
+
+    // ---------------------------------------------------------------- gradient of the output -> TMEM, its norm
+    if (tid == 0) load_x(k.iters - 1);
+    uint32_t turns = 0;
+    double ss = 0.0;
+    if (tma_in) {
+        Ring<1> ring;
+        ring.a[0] = {&it.map_g, it.g_dtype, it.g_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+        ring.n = 1;
+        ring.shape(slab);
+        if (tid == 0)
+            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch);
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+            ring.wait(slab, ch, turns);
+            float u[16];
+            ring.a[0].get(slab, ring.buf(slab, ch), row, cg, u);
+            ss += static_cast<double>(sum_squares(u));
+            tmem_st_x16(t_lane + ch * 64 + cg * 16, u);
+            __syncthreads();
+            if (tid == 0) ring.refill(slab, ch);
+        }
+    } else {
+        const Momentum mo = {1.f, 0.f, false, false};
+        ss = slab_in_any<false>(slab, it, b, mo);
+    }
+    tmem_st_wait();
+    double sum = cluster_sum(ss);
+    if (!(sum > 1e-25 && sum < 1e36)) {     // squares outside fp32's range: once more in fp64 (all CTAs alike)
+        ss = 0.0;
+        for (int c = cg * 16; c < w; c += 64) {
+            float z[16];
+            tmem_ld_x16(t_lane + c, z);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) ss = fma(static_cast<double>(z[h]), static_cast<double>(z[h]), ss);
+        }
+        sum = cluster_sum(ss);
+    }
+    const double norm = sqrt(sum);
+    const bool fin = isfinite(norm);
+    if (tid == 0 && rank == 0 && !fin) atomicOr(status, kDevErrNonfinite);
+    int ex = 0;
+    if (fin && norm > 0.0) ex = max(-126, min(126, -(ilogb(norm) + 1)));
+    const float up = __int_as_float((ex + 127) << 23);
+    const float* info = k.info + static_cast<size_t>(kept) * kStackInfo;
+    const float f0 = info[0];
+    {
+        const float d = k.it[k.iters - 1].d;
+        for (int c = cg * 16; c < w; c += 64) {
+            float z[16];
+            tmem_ld_x16(t_lane + c, z);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) z[h] *= up;
+            tmem_st_x16(t_lane + c, z);
+            put_panel16(Dp, row, c, z, d);
+        }
+        tmem_st_wait();
+    }
+    fence_async_proxy();
+    tc_fence_before();
+    __syncthreads();
+    if (C > 1) cluster_arrive();      // staging is over: peers may write into this CTA's buffers
+
+    // ---------------------------------------------------------------- iterations
+    const int rc = 128 / C;                        // rows of S that a CTA owns
+    const int own = row / rc, orow = row - own * rc, rmask = min(rc, 8) - 1;
+    const uint32_t idesc = idesc_f16_f32(128, 128, 0, 0);
+    const uint32_t x0 = smem_u32(Xp), d0 = smem_u32(Dp), s0 = smem_u32(Sm), a0 = smem_u32(Am), b0 = smem_u32(Bm);
+    const int pn = cg >> 1, ps = (cg & 1) * 4;     // panel and first 16-byte piece of columns 32 cg ...
+    for (int i = 0; i < k.iters; ++i) {
+        const int t = k.iters - 1 - i;
+        const SmallGradIter& f = k.it[t];
+        const uint32_t phase = i & 1;
+        const float f0t = t == 0 ? f0 : 1.f;       // X_0 = f0 X^_0
+        if (tid == 0) {
+            if (C > 1) {
+                mbar_arrive_expect_tx(&bar_rows, RED_BYTES);
+                mbar_arrive_expect_tx(&bar_all, A_BYTES);
+            } else {
+                load_ab(t);
+            }
+            mbar_wait(&bar_x, phase, abort, status);
+            tc_fence_after();
+            fence_async_proxy();
+            for (int j = 0; j < nchunk; ++j)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint64_t dd = smem_desc_sw128(d0 + j * PANEL + s * 32, 16, 1024);
+                    const uint64_t xd = smem_desc_sw128(x0 + j * PANEL + s * 32, 16, 1024);
+                    tc_mma_bf16(tmem + ACC_G, dd, xd, idesc, j + s > 0);   // kind::f16, types from idesc
+                    tc_mma_bf16(tmem + ACC_G, xd, dd, idesc, 1);
+                }
+            tc_commit(&bar_s);
+        }
+        mbar_wait(&bar_s, phase, abort, status);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t_lane + ACC_G + 32 * cg, r);
+        tmem_ld_wait();
+        tc_fence_before();
+        const float fs = f.s * f0t;
+        if (C > 1) {
+            // as the Gram matrix's rows
+            cluster_wait();        // every CTA's buffers are free
+            const uint32_t dst = mapa_shared(smem_u32(red), own) + static_cast<uint32_t>(rank * rc * 512);
+            const uint32_t bar = mapa_shared(smem_u32(&bar_rows), own);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int seg = 8 * cg + s;
+                st_async_v4(dst + ((seg * rc + (orow ^ (seg & rmask))) << 4), bar, r[4 * s], r[4 * s + 1], r[4 * s + 2], r[4 * s + 3]);
+            }
+            mbar_wait(&bar_rows, phase, abort, status);
+            __syncwarp();
+            for (int g = tid; g < rc * 16; g += THREADS) {
+                const int rr = g >> 4, pc = g & 15, ar = rank * rc + rr;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int seg = 2 * pc + h;
+                    const uint8_t* src = red + ((seg * rc + (rr ^ (seg & rmask))) << 4);
+                    for (int j = 0; j < C; ++j) {
+                        const float4 x = *reinterpret_cast<const float4*>(src + j * rc * 512);
+                        v[4 * h] += x.x; v[4 * h + 1] += x.y; v[4 * h + 2] += x.z; v[4 * h + 3] += x.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= fs;
+                const uint4 x = pack8(MUON_F16, v);
+                const uint32_t off = (pc >> 3) * PANEL + ar * 128 + (((pc & 7) ^ (ar & 7)) << 4);
+                for (int j = 0; j < C; ++j) {
+                    const int to = (rank + j) & (C - 1);
+                    st_async_v4(mapa_shared(s0 + off, to), mapa_shared(smem_u32(&bar_all), to), x.x, x.y, x.z, x.w);
+                }
+            }
+            __syncthreads();       // the partial rows have been read
+            if (tid == 0) {
+                fence_async_proxy();
+                load_ab(t);
+            }
+            mbar_wait(&bar_all, phase, abort, status);
+            __syncwarp();
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * s + e]) * fs;
+                *reinterpret_cast<uint4*>(Sm + pn * PANEL + row * 128 + (((ps + s) ^ (row & 7)) << 4)) = pack8(MUON_F16, v);
+            }
+        }
+        fence_async_proxy();
+        __syncthreads();
+        if (tid == 0) {
+            mbar_wait(&bar_ab, phase, abort, status);
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const uint32_t o = (s >> 2) * PANEL + (s & 3) * 32;
+                const uint64_t sd = smem_desc_sw128(s0 + o, 16, 1024), ad = smem_desc_sw128(a0 + o, 16, 1024);
+                tc_mma_bf16(tmem + ACC_G + 128, sd, ad, idesc, s > 0);
+                tc_mma_bf16(tmem + ACC_G + 128, ad, sd, idesc, 1);
+            }
+            tc_commit(&bar_p);
+        }
+        mbar_wait(&bar_p, phase, abort, status);
+        __syncwarp();
+        tc_fence_after();
+        tmem_ld_32x32b_x32(t_lane + ACC_G + 128 + 32 * cg, r);
+        tmem_ld_wait();
+        const float pa = f.pa * f0t, pb = f.pb * f0t;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            uint4* at = reinterpret_cast<uint4*>(Sm + pn * PANEL + row * 128 + (((ps + s) ^ (row & 7)) << 4));
+            float v[8];
+            unpack8(*at, MUON_F16, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(pb, v[e], pa * __uint_as_float(r[8 * s + e]));
+            *at = pack8(MUON_F16, v);
+        }
+        fence_async_proxy();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tc_fence_after();
+            const uint32_t id = idesc_f16_f32(128, w, 0, 1);
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint64_t ad = smem_desc_sw128((g ? s0 : b0) + (s >> 2) * PANEL + (s & 3) * 32, 16, 1024);
+                    const uint64_t xd = smem_desc_sw128((g ? x0 : d0) + s * 2048, PANEL, 1024);
+                    tc_mma_bf16(tmem + ACC_G, ad, xd, id, g + s > 0);
+                }
+            tc_commit(&bar_apply);
+        }
+        mbar_wait(&bar_apply, phase, abort, status);
+        __syncwarp();
+        tc_fence_after();
+        const bool last = t == 0;
+        if (!last) {
+            if (tid == 0) load_x(t - 1);
+            if (C > 1) cluster_arrive();           // this CTA's partial rows, A, B~ and P^ are done with
+        }
+        const float d = last ? 0.f : k.it[t - 1].d;
+        for (int c = cg * 16; c < w; c += 64) {
+            float z[16], u[16];
+            tmem_ld_x16(t_lane + c, z);
+            tmem_ld_x16(t_lane + ACC_G + c, u);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) z[h] = fmaf(f.va, z[h], f.vb * u[h]);
+            tmem_st_x16(t_lane + c, z);
+            if (!last) put_panel16(Dp, row, c, z, d);
+        }
+        tmem_st_wait();
+        fence_async_proxy();
+        tc_fence_before();
+        __syncthreads();
+    }
+
+    // ---------------------------------------------------------------- gradient of the input
+    // dU = [D - X_0 <D, X_0> (N + eps) / N] / (N + eps), D = V / 2^k, X_0 = f0 X^_0 (whose panels are still here)
+    mbar_wait(&bar_x, (k.iters - 1) & 1, abort, status);
+    __syncwarp();
+    auto x_at = [&](int c, float (&x)[16]) {
+        const uint8_t* src = Xp + (c >> 6) * PANEL + row * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            unpack8(*reinterpret_cast<const uint4*>(src + (((((c & 63) >> 3) + h) ^ (row & 7)) << 4)), MUON_F16, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[8 * h + e] = v[e];
+        }
+    };
+    double dot = 0.0;
+    for (int c = cg * 16; c < w; c += 64) {
+        float z[16], x[16];
+        tmem_ld_x16(t_lane + c, z);
+        x_at(c, x);
+        float s = 0.f;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) s = fmaf(z[h], x[h], s);
+        dot += static_cast<double>(s);
+    }
+    dot = cluster_sum(dot);
+    const double n = info[3], eps = static_cast<double>(k.eps), sd = 1.0 / static_cast<double>(up);
+    const double corr = n > 0.0 ? dot * sd * f0 * (n + eps) / n : (isnan(f0) ? static_cast<double>(f0) : 0.0);
+    const float od = static_cast<float>(sd / (n + eps)), ox = static_cast<float>(-corr * f0 / (n + eps));
+    for (int c = cg * 16; c < w; c += 64) {
+        float z[16], x[16];
+        tmem_ld_x16(t_lane + c, z);
+        x_at(c, x);
+#pragma unroll
+        for (int h = 0; h < 16; ++h) z[h] = fmaf(od, z[h], ox * x[h]);
+        tmem_st_x16(t_lane + c, z);
+    }
+    tmem_st_wait();
+    __syncthreads();
+    if (tma_out) {
+        const Boxes boxes = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+        const int size = boxes.bytes(), bufs = min(nchunk, slab.bytes / size);
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+            uint8_t* buf = slab.buf + (ch % bufs) * size;
+            if (ch >= bufs) {          // the buffer's last store has been read out
+                if (tid == 0) bulk_wait_read<0>();
+                __syncthreads();
+            }
+            float z[16];
+            tmem_ld_x16(t_lane + ch * 64 + cg * 16, z);
+            boxes.put(slab, buf, row, cg, z);
+            fence_async_proxy();
+            __syncthreads();
+            if (tid == 0) {
+                boxes.store(slab, slab.first(ch), smem_u32(buf));
+                bulk_commit();
+            }
+        }
+        if (tid == 0) bulk_wait_read<0>();
+    } else {
+        slab_out_any<false>(slab, it, b, 1.f);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <class P, class K, int N>
+cudaError_t launch(void (*kernel)(P), int most_smem, int smem, const SmallStackItem* items, int n, const K& k, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
@@ -838,12 +1232,12 @@ cudaError_t launch(const SmallStackItem* items, int n, const SmallStackClass& k,
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!ready[dev].load()) {
-        e = cudaFuncSetAttribute(stack_small_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kSmallStackSlab));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
     for (int i0 = 0; i0 < n; i0 += N) {
-        SmallParams<N> p;
+        P p;
         p.n = n - i0 < N ? n - i0 : N;
         p.k = k;
         int blocks = 0;
@@ -855,7 +1249,7 @@ cudaError_t launch(const SmallStackItem* items, int n, const SmallStackClass& k,
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(k.cluster) * blocks, 1, 1);
         cfg.blockDim = dim3(THREADS, 1, 1);
-        cfg.dynamicSmemBytes = smem_bytes(k.slab);
+        cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -864,11 +1258,22 @@ cudaError_t launch(const SmallStackItem* items, int n, const SmallStackClass& k,
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, stack_small_kernel<N>, p);
+        e = cudaLaunchKernelEx(&cfg, kernel, p);
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+template <int N>
+cudaError_t run_step(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
+    return launch<SmallParams<N>, SmallStackClass, N>(stack_small_kernel<N>, smem_bytes(kSmallStackSlab), smem_bytes(k.slab), items, n,
+                                                      k, stream);
+}
+template <int N>
+cudaError_t run_grad(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream) {
+    return launch<SmallGradParams<N>, SmallGradClass, N>(stack_small_grad_kernel<N>, grad_smem_bytes(kSmallGradSlab),
+                                                         grad_smem_bytes(k.slab), items, n, k, stream);
 }
 
 }  // namespace
@@ -907,7 +1312,11 @@ int stack_small_resident(int cluster) {
 }
 
 cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
-    return n <= kFewItems ? launch<kFewItems>(items, n, k, stream) : launch<kSmallStackItems>(items, n, k, stream);
+    return n <= kFewItems ? run_step<kFewItems>(items, n, k, stream) : run_step<kSmallStackItems>(items, n, k, stream);
+}
+
+cudaError_t stack_small_grad_launch(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream) {
+    return n <= kFewItems ? run_grad<kFewItems>(items, n, k, stream) : run_grad<kSmallStackItems>(items, n, k, stream);
 }
 
 }  // namespace muon

@@ -173,6 +173,25 @@ struct alignas(64) SmallStackClass {
     const float* gscale;
     unsigned* status;
 };
+// The reverse pass of wide blocks whose iterates were kept, on chip as well: G is the gradient of the output, W
+// receives that of the input (decay = 0, step = 1).
+constexpr int kSmallGradSlab = 256;      // columns of a CTA's slab at most
+struct SmallGradIter {
+    float d;              // D^ = fp16(d * V), V = 2^k dL/dX_{t+1}
+    float s;              // S^ = s * (D^ X^T + X^ D^T)
+    float pa, pb;         // P^ = pa * (S^ A + A S^) + pb * S^
+    float va, vb;         // V <- va * V + vb * (B D^ + P^ X^)
+};
+struct alignas(64) SmallGradClass {
+    CUtensorMap x, a, b;
+    const float* info;
+    int saved;
+    SmallGradIter it[32];
+    int rows, cols, cluster, slab, iters;
+    float eps;
+    unsigned* status;
+};
+cudaError_t stack_small_grad_launch(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream);
 // Fills the item's maps and `vec` from its arrays.
 void small_stack_maps(SmallStackItem& it, int rows, int cols);
 // Clusters of 1, 2, 4 or 8 CTAs that run at once on the current device (they do not fill it: 14 of 8, not 18).

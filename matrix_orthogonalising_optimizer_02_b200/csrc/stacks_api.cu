@@ -107,6 +107,7 @@ struct StackClass {
     int rp = 0, cp = 0, r = 0, s = 0, r8 = 0;   // padded sides; true and padded shorter side
     bool tall = false;
     bool chip = false;                           // iterates on chip, also where its iterates are kept
+    bool chip_grad = false;                      // and so does its reverse pass
     int chunks = 0, per = 1;                     // chunks of a block in the elementwise passes
     std::vector<double> alpha, gamma, tau;       // tau[0] unused: X_0 = f0 * plane
     std::vector<double> shift, a, b;             // l; a + bl + cl^2 and b + 2cl (a and b without a shift)
@@ -460,10 +461,10 @@ muon_status launch_pass(StackPass pass, std::vector<StackItem>& items, const Sta
 }
 
 // Class order of the launches: the longest sums first, so that the last tiles are short ones.
-std::vector<int> class_order(const Group& g, bool on_chip_too) {
+std::vector<int> class_order(const Group& g, bool reverse) {
     std::vector<int> o;
     for (size_t i = 0; i < g.classes.size(); ++i)
-        if (on_chip_too || !g.classes[i].chip) o.push_back(static_cast<int>(i));
+        if (!(reverse ? g.classes[i].chip_grad : g.classes[i].chip)) o.push_back(static_cast<int>(i));
     std::stable_sort(o.begin(), o.end(), [&](int x, int y) { return g.classes[x].s > g.classes[y].s; });
     return o;
 }
@@ -693,6 +694,7 @@ void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
         std::vector<double> kappas;
         if (c.tall || !small_class(c.rows, c.cols, c.count, sch, bd, k, &kappas)) continue;
         c.chip = true;
+        c.chip_grad = c.cols <= 8 * kSmallGradSlab;
         c.gamma = kappas;
     }
 }
@@ -734,6 +736,57 @@ muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedul
         }
         const muon_status st = launch_small(items, q, small_flops(q, c.count), call);
         if (st != MUON_OK) return st;
+    }
+    return MUON_OK;
+}
+
+// The reverse pass of the on-chip classes of a group; delta as in backward().
+muon_status reverse_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedule& sch,
+                            const std::vector<std::vector<double>>& delta, const Call& call) {
+    for (size_t k = 0; k < g.classes.size(); ++k) {
+        const StackClass& c = g.classes[k];
+        if (!c.chip_grad) continue;
+        const int T = sch.n_iters, n = T * c.count;
+        SmallGradClass q;
+        std::memset(&q, 0, sizeof(q));
+        if (!encode_stack_tmap(&q.x, c.X, c.rp, c.cp, n) || !encode_stack_tmap(&q.a, c.A, c.r8, c.r8, n) ||
+            !encode_stack_tmap(&q.b, c.B, c.r8, c.r8, n))
+            return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        for (int t = 0; t < T; ++t) {
+            const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t], p = 2.0 * c.gamma[t] * inv_tau;   // t = 0: f0 comes from info
+            SmallGradIter& f = q.it[t];
+            f.d = static_cast<float>(delta[k][t + 1]);
+            f.s = static_cast<float>(0.5 * inv_tau);
+            f.pa = static_cast<float>(sch.coeffs[3 * t + 2] * p / c.alpha[t]);
+            f.pb = static_cast<float>(c.b[t] * p);
+            f.va = static_cast<float>(c.a[t]);
+            f.vb = static_cast<float>(1.0 / (c.gamma[t] * delta[k][t + 1]));
+        }
+        q.info = c.info;
+        q.saved = c.count;
+        q.rows = c.rows;
+        q.cols = c.cols;
+        q.iters = T;
+        q.eps = sch.eps;
+        q.status = call.status;
+        // as in small_class
+        const int pieces = (c.cols + 63) / 64;
+        int C = 1;
+        while (C * kSmallGradSlab < c.cols) C *= 2;
+        while (c.cols > 256 && 2 * C <= 8 && 2 * C <= pieces && c.count <= stack_small_resident(2 * C)) C *= 2;
+        q.cluster = C;
+        q.slab = (pieces + C - 1) / C * 64;
+        std::vector<SmallStackItem> items;
+        for (const Part& p : g.parts) {
+            if (p.cls != static_cast<int>(k)) continue;
+            items.push_back(small_item(d[p.stack], p.first, p.count));
+            items.back().at = p.at;
+        }
+        const double flops = static_cast<double>(c.count) * T * (6.0 * c.r * c.r * c.s + 2.0 * c.r * c.r * c.r);
+        const cudaError_t e = launch_timed(MUON_KERNEL_NS_GEMM, flops, call.stream, [&](cudaStream_t st) {
+            return stack_small_grad_launch(items.data(), static_cast<int>(items.size()), q, st);
+        });
+        if (e != cudaSuccess) return cuda_error(e, "small-block reverse launch");
     }
     return MUON_OK;
 }
@@ -874,10 +927,21 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             }
         }
 
+        bool any_chip = false;
+        for (const StackClass& c : g.classes) any_chip = any_chip || c.chip_grad;
+        if (any_chip) {
+            muon_status st = MUON_OK;
+            if (first) st = clear_status(call);
+            first = false;
+            if (st == MUON_OK) st = reverse_on_chip(g, d, sch, delta, call);
+            if (st != MUON_OK) return st;
+        }
+
         std::vector<StackItem> in, dot, out;
         double read = 0.0;
         for (const Part& p : g.parts) {
             const StackClass& c = g.classes[p.cls];
+            if (c.chip_grad) continue;
             const GradPlanes& q = gp[p.cls];
             const ns_stack_desc& s = d[p.stack];
             StackItem it = base_item(c, p);
@@ -908,6 +972,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             o.step = static_cast<float>(delta[p.cls][0]);
             out.push_back(o);
         }
+        if (in.empty()) continue;
         StackPassArgs args = {};
         args.eps = sch.eps;
         args.status = first ? call.status : nullptr;
@@ -976,7 +1041,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                 }
             }
         }
-        st = launch_chain(classes, ops, 3 * static_cast<int>(nc), flops, args.tickets, call);
+        st = launch_chain(classes, ops, 3 * static_cast<int>(order.size()), flops, args.tickets, call);
         if (st != MUON_OK) return st;
         dot = out;
         st = launch_pass(StackPass::kDot, dot, args, MUON_KERNEL_SCALE, 0.0, call);

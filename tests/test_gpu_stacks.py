@@ -663,3 +663,54 @@ def test_optimizers_carry_their_state_in_fp32():
     for t in twin.param_groups[0]["params"]:
         t.grad = blocks(200, 2, 24, 40, BF)
     twin.step()
+
+
+@pytest.mark.parametrize("shape", [(5, 128, 256), (3, 128, 1024), (2, 120, 2048), (2, 128, 2049), (40, 96, 641), (16, 64, 768),
+                                   (9, 7, 500), (200, 24, 40), (1, 128, 128)], ids=str)
+@pytest.mark.parametrize("dtype,pad", [(HF, 0), (FP, 3), (BF, 8)])
+@pytest.mark.parametrize("coeffs,tol", [(ref.KJ, lambda t: 2 * ref.tol_kj(t)), (ref.STABLE, ref.tol_stable)],
+                         ids=["kj", "stable"])
+def test_gradient_of_short_sides(shape, dtype, pad, coeffs, tol):
+    """Wide blocks whose short side is at most 128, of every cluster size, on either side of the longest slab; arrays
+    with and without whole 16-byte rows.  Tolerances as above."""
+    count = shape[0]
+    x, dy = blocks(210, *shape, dtype, std=0.5), blocks(211, *shape, FP, std=1e-2)
+    dy = dy.to(dtype)
+    leaf, buf = padded(*shape, pad, dtype)
+    leaf.copy_(x)
+    dyv, _ = padded(*shape, pad, dtype)
+    dyv.copy_(dy)
+    dx, out = padded(*shape, pad, dtype)
+    sch = mb.Schedule.fixed(T, coeffs)
+    y = torch.empty_like(x)
+    stacks, grads = [mb.Stack(leaf, y)], [mb.Stack(dyv, dx)]
+    saved = mb.workspace(mb.ns_stacks_saved_size(stacks, sch))
+    run(stacks, sch, saved=saved)
+    ws = mb.workspace(mb.ns_stacks_backward_workspace_size(grads, sch))
+    mb.ns_orthogonalize_stacks_backward(grads, sch, saved, ws)
+    assert mb.device_status(ws) == mb.MUON_OK
+    for b in sorted({0, 1 % count, count // 2, count - 1}):
+        assert ref.rel(dx[b], ref.ns_grad(x[b], dy[b], [coeffs] * T)) <= tol(dtype), b
+    if pad:
+        assert bool((out[:, :, shape[2]:] == 7.0).all())
+
+
+def test_gradient_of_short_sides_at_any_magnitude():
+    """Gradients from 1e-30 to 1e30, a zero gradient, and one that is not finite, side by side."""
+    x = blocks(212, 5, 40, 300, FP, std=0.5)
+    dy = blocks(213, 5, 40, 300, FP, std=1.0)
+    dy[0] *= 1e-30
+    dy[1] *= 1e30
+    dy[2] = 0
+    dy[3, 39, 299] = float("inf")
+    sch = mb.Schedule.fixed(T)
+    dx = torch.empty_like(x)
+    stacks, grads = [mb.Stack(x, torch.empty_like(x))], [mb.Stack(dy, dx)]
+    saved = mb.workspace(mb.ns_stacks_saved_size(stacks, sch))
+    run(stacks, sch, saved=saved)
+    ws = mb.workspace(mb.ns_stacks_backward_workspace_size(grads, sch))
+    mb.ns_orthogonalize_stacks_backward(grads, sch, saved, ws)
+    assert mb.device_status(ws) == mb.MUON_ERR_NONFINITE
+    assert bool((dx[2] == 0).all()) and bool(torch.isnan(dx[3]).any())
+    for b in (0, 1, 4):
+        assert ref.rel(dx[b], ref.ns_grad(x[b], dy[b], [ref.KJ] * T)) <= 2 * ref.tol_kj(FP), b
