@@ -577,20 +577,20 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     // What the reverse pass reads, kept as it lies in shared memory (thread 0): X^_t from every CTA, A_t and
     // B~_t from the first.
     const bool keep = k.saved != 0;
-    const int keep_z = keep ? it.at + static_cast<int>(b) : 0;
+    const int keep_z = keep ? it.at + static_cast<int>(b) : 0, r_true = min(k.rows, k.cols), s_true = max(k.rows, k.cols);
     auto keep_x = [&](int t) {
         for (int j = 0; j < nchunk; ++j) {
             const int x = slab.first(j);
-            if (x >= k.cols) break;
-            for (int y = 0; y < k.rows; y += 64)
+            if (x >= s_true) break;
+            for (int y = 0; y < r_true; y += 64)
                 tma_store_3d(&k.x, smem_u32(panels) + j * PANEL + y * 128, x, y, t * k.saved + keep_z);
         }
         bulk_commit();
     };
     auto keep_square = [&](const CUtensorMap* m, const uint8_t* src, int t) {
         if (rank != 0) return;
-        for (int x = 0; x < k.rows; x += 64)
-            for (int y = 0; y < k.rows; y += 64)
+        for (int x = 0; x < r_true; x += 64)
+            for (int y = 0; y < r_true; y += 64)
                 tma_store_3d(m, smem_u32(src) + (x >> 6) * PANEL + y * 128, x, y, t * k.saved + keep_z);
         bulk_commit();
     };
@@ -879,6 +879,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const long long b = blk - it.block0;
     const int kept = it.at + static_cast<int>(b);
     const int q = warp & 3, cg = warp >> 2, row = 32 * q + lane;
+    const bool tall = k.rows > k.cols;
 
     if (tid == 0) {
         for (uint64_t* x : {&bar_s, &bar_p, &bar_apply, &bar_rows, &bar_all, &bar_ab, &bar_x}) mbar_init(x, 1);
@@ -897,7 +898,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
-    const Slab slab = {k.rows, k.cols, rank, C, nchunk, false, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
     const bool tma_in = (it.vec & 1) != 0, tma_out = (it.vec & 4) != 0;
 
     auto load_x = [&](int t) {     // thread 0
@@ -958,7 +959,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
     } else {
         const Momentum mo = {1.f, 0.f, false, false};
-        ss = slab_in_any<false>(slab, it, b, mo);
+        ss = tall ? slab_in_any<true>(slab, it, b, mo) : slab_in_any<false>(slab, it, b, mo);
     }
     tmem_st_wait();
     double sum = cluster_sum(ss);
@@ -1213,7 +1214,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
         if (tid == 0) bulk_wait_read<0>();
     } else {
-        slab_out_any<false>(slab, it, b, 1.f);
+        if (tall) slab_out_any<true>(slab, it, b, 1.f);
+        else slab_out_any<false>(slab, it, b, 1.f);
     }
     tc_fence_before();
     __syncthreads();

@@ -161,7 +161,7 @@ struct SmallStackIter {
     float pb, pc;         // B~ = pb * A + pc * A^2
 };
 struct alignas(64) SmallStackClass {
-    CUtensorMap x, a, b;  // saved planes of wide blocks: X^_t, A_t and B~_t in slot t of `saved` blocks
+    CUtensorMap x, a, b;  // saved planes: X^_t (turned so that it is wide), A_t, B~_t in slot t of `saved` blocks
     float* info;          // kStackInfo floats per saved block
     int saved;            // 0: nothing is kept
     float f0;             // X_0 = f0 * X^_0
@@ -173,7 +173,7 @@ struct alignas(64) SmallStackClass {
     const float* gscale;
     unsigned* status;
 };
-// The reverse pass of wide blocks whose iterates were kept, on chip as well: G is the gradient of the output, W
+// The reverse pass of blocks whose iterates were kept, on chip as well: G is the gradient of the output, W
 // receives that of the input (decay = 0, step = 1).
 constexpr int kSmallGradSlab = 256;      // columns of a CTA's slab at most
 struct SmallGradIter {

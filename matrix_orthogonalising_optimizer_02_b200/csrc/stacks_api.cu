@@ -686,15 +686,17 @@ const uint8_t* bytes_at(const void* p, long long blocks, long long stride, int d
 }
 
 // ---------------------------------------------------------------- forward
-// Where iterates are kept for the reverse pass: wide blocks that run on chip keep them from there, with B_t
-// scaled as it is there (a tall block's X^ lies the wrong way for that).
+// Where iterates are kept for the reverse pass: blocks that run on chip keep them from there, X^ turned so that it
+// is wide and B_t scaled as it is there.  A tall block whose reverse pass runs as a chain has to have X^ as it lies,
+// and goes the other way.
 void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
     for (StackClass& c : g.classes) {
         SmallStackClass k;
         std::vector<double> kappas;
-        if (c.tall || !small_class(c.rows, c.cols, c.count, sch, bd, k, &kappas)) continue;
+        const bool both = c.s <= 8 * kSmallGradSlab;
+        if ((c.tall && !both) || !small_class(c.rows, c.cols, c.count, sch, bd, k, &kappas)) continue;
         c.chip = true;
-        c.chip_grad = c.cols <= 8 * kSmallGradSlab;
+        c.chip_grad = both;
         c.gamma = kappas;
     }
 }
@@ -714,6 +716,11 @@ SmallStackItem small_item(const ns_stack_desc& s, int first, int count) {
     small_stack_maps(it, s.rows, s.cols);
     return it;
 }
+template <class K>
+bool kept_maps(K& q, const StackClass& c, int n) {
+    return encode_stack_tmap(&q.x, c.X, std::min(c.rp, c.cp), std::max(c.rp, c.cp), n) &&
+           encode_stack_tmap(&q.a, c.A, c.r8, c.r8, n) && encode_stack_tmap(&q.b, c.B, c.r8, c.r8, n);
+}
 // The on-chip classes of a group whose iterates are kept.
 muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedule& sch, const Bounds& bd, const Call& call) {
     for (size_t k = 0; k < g.classes.size(); ++k) {
@@ -722,9 +729,7 @@ muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedul
         SmallStackClass q;
         if (!small_class(c.rows, c.cols, c.count, sch, bd, q)) return MUON_ERR_INVALID_ARG;
         const int n = sch.n_iters * c.count;
-        if (!encode_stack_tmap(&q.x, c.X, c.rp, c.cp, n) || !encode_stack_tmap(&q.a, c.A, c.r8, c.r8, n) ||
-            !encode_stack_tmap(&q.b, c.B, c.r8, c.r8, n))
-            return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        if (!kept_maps(q, c, n)) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
         q.info = c.info;
         q.saved = c.count;
         q.status = call.status;
@@ -749,9 +754,7 @@ muon_status reverse_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_sche
         const int T = sch.n_iters, n = T * c.count;
         SmallGradClass q;
         std::memset(&q, 0, sizeof(q));
-        if (!encode_stack_tmap(&q.x, c.X, c.rp, c.cp, n) || !encode_stack_tmap(&q.a, c.A, c.r8, c.r8, n) ||
-            !encode_stack_tmap(&q.b, c.B, c.r8, c.r8, n))
-            return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
+        if (!kept_maps(q, c, n)) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
         for (int t = 0; t < T; ++t) {
             const double inv_tau = t == 0 ? 1.0 : 1.0 / c.tau[t], p = 2.0 * c.gamma[t] * inv_tau;   // t = 0: f0 comes from info
             SmallGradIter& f = q.it[t];
@@ -770,10 +773,10 @@ muon_status reverse_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_sche
         q.eps = sch.eps;
         q.status = call.status;
         // as in small_class
-        const int pieces = (c.cols + 63) / 64;
+        const int pieces = (c.s + 63) / 64;
         int C = 1;
-        while (C * kSmallGradSlab < c.cols) C *= 2;
-        while (c.cols > 256 && 2 * C <= 8 && 2 * C <= pieces && c.count <= stack_small_resident(2 * C)) C *= 2;
+        while (C * kSmallGradSlab < c.s) C *= 2;
+        while (c.s > 256 && 2 * C <= 8 && 2 * C <= pieces && c.count <= stack_small_resident(2 * C)) C *= 2;
         q.cluster = C;
         q.slab = (pieces + C - 1) / C * 64;
         std::vector<SmallStackItem> items;

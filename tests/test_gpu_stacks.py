@@ -666,12 +666,13 @@ def test_optimizers_carry_their_state_in_fp32():
 
 
 @pytest.mark.parametrize("shape", [(5, 128, 256), (3, 128, 1024), (2, 120, 2048), (2, 128, 2049), (40, 96, 641), (16, 64, 768),
-                                   (9, 7, 500), (200, 24, 40), (1, 128, 128)], ids=str)
+                                   (9, 7, 500), (200, 24, 40), (1, 128, 128), (6, 2048, 64), (2, 2049, 100), (20, 641, 96),
+                                   (4, 300, 7), (3, 777, 128)], ids=str)
 @pytest.mark.parametrize("dtype,pad", [(HF, 0), (FP, 3), (BF, 8)])
 @pytest.mark.parametrize("coeffs,tol", [(ref.KJ, lambda t: 2 * ref.tol_kj(t)), (ref.STABLE, ref.tol_stable)],
                          ids=["kj", "stable"])
 def test_gradient_of_short_sides(shape, dtype, pad, coeffs, tol):
-    """Wide blocks whose short side is at most 128, of every cluster size, on either side of the longest slab; arrays
+    """Blocks whose short side is at most 128, of every cluster size, on either side of the longest slab; arrays
     with and without whole 16-byte rows.  Tolerances as above."""
     count = shape[0]
     x, dy = blocks(210, *shape, dtype, std=0.5), blocks(211, *shape, FP, std=1e-2)
