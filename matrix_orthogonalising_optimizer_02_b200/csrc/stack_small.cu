@@ -32,7 +32,7 @@
 // 16 bytes, no finer, so rows of a broken number of 16-byte pieces are among them.)
 //
 // Where the reverse pass is to follow, the panels of X^_t and the matrices A_t and B~_t leave by TMA as they lie in
-// shared memory, behind the products that read them (16 blocks of 96 x 641: 55 us without, 63 with).
+// shared memory, behind the products that read them (16 blocks of 96 x 641: 55 us without, 65 with).
 //
 // Bound: latency of the chain Gram, exchange, A^2, apply (12 blocks of 64 x 768: 50 us for five iterations, the
 // tensor pipe 12% busy).  A cluster of 8 leaves 36 SMs idle (14 run at once); 96 steps of 128 x 4096 are 7 rounds
@@ -832,9 +832,9 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
 // ---------------------------------------------------------------- reverse pass
 // D <- aD + BD + 2PX with S = sym(D X^T), P = bS + c(SA + AS), from the kept X^_t, A_t and B~_t, t falling.
 // The state V = 2^k D stays in TMEM in fp32 (columns 0 ..), the products go to the columns from ACC_G on; X^_t and
-// D^ = fp16(V) lie in panels as above.  S's partial rows are exchanged as the Gram matrix's are; A and B~ come in by
-// TMA over the partial rows when those have been summed, P^ takes S^'s place.  (As a chain of launches' tiles the
-// reverse pass of 16 blocks of 96 x 641 took 160 us.)
+// D^ = fp16(d V) lie in panels as above.  S's partial rows are exchanged as the Gram matrix's are; A and B~ come in by
+// TMA over the partial rows when those have been summed, P^ takes S^'s place.  Bound by latency as the forward pass is:
+// 16 blocks of 96 x 641 take 68 us, 96 of 128 x 1024 219 (as chains of tiles 154 and 499).
 constexpr int ACC_G = 256;
 __host__ __device__ constexpr int grad_smem_bytes(int w) { return 2 * (w / 64) * PANEL + A_BYTES + RED_BYTES + 1024; }
 static_assert(grad_smem_bytes(kSmallGradSlab) + 512 <= 232448, "shared memory above the 227 KB per-CTA limit");
