@@ -271,7 +271,8 @@ typedef struct {
 } adamw_hyper;
 
 /* out[0] <- norm of all gradients together, out[1] <- min(1, max_norm / (norm + 1e-6)) (device
- * floats).  Squares and sums in fp64, in a fixed order: the result does not change from run to run.
+ * floats).  Sums in fp64 (of four squares formed in fp32 for 16-bit gradients, where they are in its
+ * range), in a fixed order: the result does not change from run to run and is within 2^-23.
  * A norm that is not finite is reported in the workspace's device status. */
 MUON_API size_t grad_norm_workspace_size(const adamw_tensor_desc* descs, int n);
 MUON_API muon_status grad_norm_batched(const adamw_tensor_desc* descs, int n, float max_norm, float* out,

@@ -3,8 +3,8 @@
 // Both are HBM-bound: the norm reads each gradient once; AdamW reads W, G, m, v and writes W, m, v
 // once, all arithmetic in fp32 registers.  Descriptors travel as kernel parameters (up to 256 tensors
 // a launch).  A persistent grid walks chunks of 4096 elements, 8 elements a thread at a time.
-// Measured: AdamW on 33e6 bf16 elements 116 us (0.96 of the measured copy rate); the norm of 83e6 45 us (0.57:
-// the conversions to fp64, which keep squares of 1e-20 and 1e30 in range, bind it).
+// Measured: AdamW on 33e6 bf16 elements 116 us (0.96 of the measured copy rate); the norm of 262e6
+// 84 us (0.96).
 #include <cmath>
 
 #include "../../include/muon_b200.h"
@@ -39,6 +39,26 @@ __device__ __forceinline__ int find(const Params<N>& p, long long chunk) {
     return lo;
 }
 
+// Adds the squares of 8 values of 16 bits.  A square is exact in fp32, and sums of four have two roundings on the
+// way, which leaves the norm within 2^-24; where a sum would leave fp32's range it is formed in fp64.  (A conversion
+// to fp64 per value took longer than the reading: 262e6 values 108 us, 84 with one per sum.)
+__device__ __forceinline__ void add_squares8(const uint4& w, int dtype, double& ss) {
+    float x[8];
+    unpack8(w, dtype, x);
+    const uint32_t bits[2] = {w.x | w.y, w.z | w.w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float* v = x + 4 * h;
+        const float s = fmaf(v[1], v[1], v[0] * v[0]) + fmaf(v[3], v[3], v[2] * v[2]);
+        if (s > 1e-25f && s < 1e36f) {
+            ss += static_cast<double>(s);
+        } else if (bits[h] & 0x7fff7fffu) {      // not all zero: rows of an embedding that no token met are
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ss = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), ss);
+        }
+    }
+}
+
 // partials[blockIdx.x] <- sum of squares of this CTA's chunks, in fp64.
 template <int N>
 __global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Params<N> p, double* partials) {
@@ -46,6 +66,15 @@ __global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constan
     for (long long c = blockIdx.x; c < p.chunks; c += gridDim.x) {
         const AdamItem& it = p.item[find(p, c)];
         const long long e0 = (c - it.chunk0) * CHUNK;
+        if (it.g_dtype != MUON_F32 && (it.vec & 1) && e0 + CHUNK <= it.n) {
+            const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(it.G) + e0) + threadIdx.x;
+            uint4 x[GROUPS];
+#pragma unroll
+            for (int q = 0; q < GROUPS; ++q) x[q] = g[q * THREADS];
+#pragma unroll
+            for (int q = 0; q < GROUPS; ++q) add_squares8(x[q], it.g_dtype, ss);
+            continue;
+        }
 #pragma unroll
         for (int q = 0; q < GROUPS; ++q) {
             const long long e = e0 + (q * THREADS + static_cast<int>(threadIdx.x)) * 8;

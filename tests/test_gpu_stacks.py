@@ -715,3 +715,21 @@ def test_gradient_of_short_sides_at_any_magnitude():
     assert bool((dx[2] == 0).all()) and bool(torch.isnan(dx[3]).any())
     for b in (0, 1, 4):
         assert ref.rel(dx[b], ref.ns_grad(x[b], dy[b], [ref.KJ] * T)) <= 2 * ref.tol_kj(FP), b
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+def test_norm_of_long_tensors(dtype):
+    """Whole chunks: runs of zeros, values whose squares leave fp32's range, an infinity."""
+    n = 5 * 4096 + 17
+    g = blocks(220, 1, 1, n, dtype, std=1.0)[0, 0]
+    g[4096:9000] = 0
+    out, ws = torch.empty(2, device="cuda"), mb.workspace(mb.grad_norm_workspace_size([g]))
+    sizes = [1.0, 1e-30, 1e25] if dtype != HF else [1.0, 2.0 ** -20]     # fp16: down to its subnormals
+    for size in sizes:
+        h = (g.double() * size).to(dtype)
+        mb.grad_norm_batched([h], 1.0, out, ws)
+        norm = float(h.double().norm())
+        assert abs(float(out[0]) - norm) <= 2.0 ** -23 * norm, size   # 2^-24 of the sums, 2^-24 of the result
+    h[4] = float("inf")
+    mb.grad_norm_batched([h], 1.0, out, ws)
+    assert float(out[0]) == float("inf") and mb.device_status(ws) == mb.MUON_ERR_NONFINITE
