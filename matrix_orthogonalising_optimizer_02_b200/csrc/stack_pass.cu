@@ -75,6 +75,34 @@ struct Eight {
             plane = plane0 + f0;
         }
     }
+    // Where all eight are there for 16-byte accesses, fetch() only starts the loads and take() waits for them, so that
+    // several groups' are under way together; otherwise take() does it all.
+    struct Raw { uint4 a, b; };
+    __device__ __forceinline__ bool whole() const { return VEC && n == 8; }
+    __device__ __forceinline__ void fetch(const void* p, int dtype, long long base, int ld, Raw& r) const {
+        if (!whole()) return;
+        const size_t e = base + static_cast<long long>(i[0]) * ld + j[0];
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + e * (dtype == MUON_F32 ? 4 : 2));
+        r.a = q[0];
+        if (dtype == MUON_F32) r.b = q[1];
+    }
+    __device__ __forceinline__ void take(const Raw& r, const void* p, int dtype, long long base, int ld, float (&x)[8]) const {
+        if (!whole()) return get(p, dtype, base, ld, x);
+        if (dtype == MUON_F32) {
+            const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
+        } else {
+            unpack8(r.a, dtype, x);
+        }
+    }
+    __device__ __forceinline__ void fetch_plane(const __half* p, Raw& r) const {
+        if (VEC) r.a = *reinterpret_cast<const uint4*>(p + plane);
+    }
+    __device__ __forceinline__ void take_plane(const Raw& r, const __half* p, float (&x)[8]) const {
+        if (VEC) unpack8(r.a, MUON_F16, x);
+        else get_plane(p, x);
+    }
     __device__ __forceinline__ bool any() const {
         if constexpr (VEC) return n > 0;
         else return in != 0;
@@ -139,64 +167,81 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
     const size_t plane0 = static_cast<size_t>(b) * rp * cp;
     const long long gb = b * it.g_stride, mb = b * it.m_stride, wb = b * it.w_stride;
     double ss = 0.0;
-    for (int q = 0; q < it.per; ++q) {
-        const Eight<VEC> at(it, plane0, c, q);
-        if (!at.padded) continue;
-        if (PASS == StackPass::kNorm) {
-            if (!at.any()) continue;
-            float x[8];
-            at.get(it.G, it.g_dtype, gb, it.g_ld, x);
+    constexpr int U = VEC ? 2 : 1;     // groups whose loads are under way together
+    using At = Eight<VEC>;
+    constexpr bool norm = PASS == StackPass::kNorm, pack = PASS == StackPass::kPack || PASS == StackPass::kPackGrad;
+    // The momentum pass has updated M when the planes are made.
+    const bool from_g = norm || it.M == nullptr || a.nesterov, from_m = it.M != nullptr;
+    for (int q0 = 0; q0 < it.per; q0 += U) {
+        const At at[2] = {At(it, plane0, c, q0), At(it, plane0, c, q0 + U - 1)};
+        typename At::Raw r0[U], r1[U], r2[U];
+        bool on[U];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= gs;
-            if (it.M != nullptr) {
-                float m[8];
-                at.get(it.M, MUON_F32, mb, it.m_ld, m);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    m[e] = fmaf(a.beta, m[e], x[e]);
-                    x[e] = a.nesterov ? fmaf(a.beta, m[e], x[e]) : m[e];
-                }
-                at.put(it.M, MUON_F32, mb, it.m_ld, m);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
-        } else if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad) {
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (at.any()) {
-                if (it.M == nullptr || a.nesterov) {
-                    at.get(it.G, it.g_dtype, gb, it.g_ld, x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= gs;
-                }
-                if (it.M != nullptr) {   // the momentum pass has updated M
-                    float m[8];
-                    at.get(it.M, MUON_F32, mb, it.m_ld, m);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = a.nesterov ? fmaf(a.beta, m[e], x[e]) : m[e];
+        for (int u = 0; u < U; ++u) {
+            on[u] = q0 + u < it.per && at[u].any();
+            if (!on[u]) continue;
+            if (norm || pack) {
+                if (from_g) at[u].fetch(it.G, it.g_dtype, gb, it.g_ld, r0[u]);
+                if (from_m) at[u].fetch(it.M, MUON_F32, mb, it.m_ld, r1[u]);
+            } else {
+                at[u].fetch_plane(it.hi, r0[u]);
+                if (PASS == StackPass::kUpdate) at[u].fetch(it.W, it.w_dtype, wb, it.w_ld, r1[u]);
+                if (PASS == StackPass::kDot || PASS == StackPass::kGradOut) {
+                    at[u].fetch_plane(it.lo, r1[u]);
+                    at[u].fetch_plane(it.hi2, r2[u]);
                 }
             }
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= up;
-            at.put_plane(it.hi, x);
-            at.put_plane(it.lo, x);
-        } else {
-            if (!at.any()) continue;
+        for (int u = 0; u < U; ++u) {
+            if (norm || pack) {
+                if (!on[u] && (norm || q0 + u >= it.per || !at[u].padded)) continue;   // padding is written too
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (on[u]) {
+                    if (from_g) {
+                        at[u].take(r0[u], it.G, it.g_dtype, gb, it.g_ld, x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] *= gs;
+                    }
+                    if (from_m) {
+                        float m[8];
+                        at[u].take(r1[u], it.M, MUON_F32, mb, it.m_ld, m);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            if (norm) m[e] = fmaf(a.beta, m[e], x[e]);
+                            x[e] = a.nesterov ? fmaf(a.beta, m[e], x[e]) : m[e];
+                        }
+                        if (norm) at[u].put(it.M, MUON_F32, mb, it.m_ld, m);
+                    }
+                }
+                if (norm) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= up;
+                    at[u].put_plane(it.hi, x);
+                    at[u].put_plane(it.lo, x);
+                }
+                continue;
+            }
+            if (!on[u]) continue;
             float x[8];
-            at.get_plane(it.hi, x);
+            at[u].take_plane(r0[u], it.hi, x);
             if (PASS == StackPass::kOut) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] *= it.step;
-                at.put(it.W, it.w_dtype, wb, it.w_ld, x);
+                at[u].put(it.W, it.w_dtype, wb, it.w_ld, x);
             } else if (PASS == StackPass::kUpdate) {
                 float w[8];
-                at.get(it.W, it.w_dtype, wb, it.w_ld, w);
+                at[u].take(r1[u], it.W, it.w_dtype, wb, it.w_ld, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = fmaf(it.step, x[e], it.decay * w[e]);
-                at.put(it.W, it.w_dtype, wb, it.w_ld, w);
+                at[u].put(it.W, it.w_dtype, wb, it.w_ld, w);
             } else {
                 float y[8], z[8];
-                at.get_plane(it.lo, y);
-                at.get_plane(it.hi2, z);
+                at[u].take_plane(r1[u], it.lo, y);
+                at[u].take_plane(r2[u], it.hi2, z);
                 if (PASS == StackPass::kDot) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -204,7 +249,7 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = fmaf(od, x[e] + y[e], ox * z[e]);
-                    at.put(it.W, it.w_dtype, wb, it.w_ld, x);
+                    at[u].put(it.W, it.w_dtype, wb, it.w_ld, x);
                 }
             }
         }
