@@ -258,7 +258,7 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
 }
 
 template <StackPass PASS, int N>
-__global__ void __launch_bounds__(kStackThreads)
+__global__ void __launch_bounds__(kStackThreads, 4)
 stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
     int lo = 0, hi = p.n - 1;
     const int chunk = static_cast<int>(blockIdx.x);
