@@ -116,7 +116,7 @@ __device__ __forceinline__ void put_panel16(uint8_t* panels, int row, int c, con
 // ---------------------------------------------------------------- a slab in and out
 struct Slab {
     int rows, cols, rank, cluster, nchunk;
-    bool tall;
+    bool tall, two;        // two: a packed cluster has a second block
     uint8_t* buf;          // all of the shared memory that the iterations use, 1024-byte aligned
     int bytes;
     uint32_t t_lane;       // TMEM address of this warp's lanes
@@ -149,30 +149,40 @@ __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-// One array's part of a chunk: two boxes of 64 x 128 (64-column halves of a tall block's rows) or one of 128 x 64
+// Packed: rows 64 .. of X are the next block's.  One array's part of a chunk: two boxes of 64 x 128 (64-column halves of a tall block's rows) or one of 128 x 64
 // for 16-bit elements, twice as many for fp32.  A box's row has 128 bytes: 64 or 32 elements.
+template <bool PACK>
 struct Boxes {
     const CUtensorMap* map;
     int dtype, es, block;
     __device__ __forceinline__ int bytes() const { return BOX * es / 2; }
-    // Calls f(byte offset in the buffer, x, y) for every box of the chunk at column c.
+    // Calls f(byte offset in the buffer, x, y, block) for every box of the chunk at column c.
     template <class F>
     __device__ __forceinline__ void each(const Slab& s, int c, F f) const {
         const int per = 128 / es;
         if (!s.tall) {
-            for (int h = 0; h < es / 2; ++h) f(h * BOX, c + h * per, 0);
+            for (int h = 0; h < es / 2; ++h) {
+                f(h * BOX, c + h * per, 0, block);
+                if (PACK) f(h * BOX + BOX / 2, c + h * per, 0, block + 1);
+            }
         } else {
-            for (int h = 0; h < es; ++h) f(h * (BOX / 2), h * per, c);
+            for (int h = 0; h < es; ++h) {
+                const int i = h * per;
+                f(h * (BOX / 2), PACK ? i & 63 : i, c, PACK ? block + (i >> 6) : block);
+            }
         }
     }
+    __device__ __forceinline__ bool there(const Slab& s, int x, int y, int z) const {
+        return x < s.cols && y < s.rows && (!PACK || z == block || s.two);
+    }
     __device__ __forceinline__ void load(const Slab& s, int c, uint32_t buf, uint32_t bar) const {
-        each(s, c, [&](int o, int x, int y) { tma_load_3d(buf + o, map, bar, x, y, block); });
+        each(s, c, [&](int o, int x, int y, int z) { tma_load_3d(buf + o, map, bar, x, y, z); });   // zeros where none
     }
     __device__ __forceinline__ void prefetch(const Slab& s, int c) const {
-        each(s, c, [&](int, int x, int y) { if (x < s.cols && y < s.rows) tma_prefetch_3d(map, x, y, block); });
+        each(s, c, [&](int, int x, int y, int z) { if (there(s, x, y, z)) tma_prefetch_3d(map, x, y, z); });
     }
     __device__ __forceinline__ void store(const Slab& s, int c, uint32_t buf) const {
-        each(s, c, [&](int o, int x, int y) { if (x < s.cols && y < s.rows) tma_store_3d(map, buf + o, x, y, block); });
+        each(s, c, [&](int o, int x, int y, int z) { if (there(s, x, y, z)) tma_store_3d(map, buf + o, x, y, z); });
     }
     // This thread's 16 elements (X's row `row`, columns 16 cg ...) in a buffer: piece h (0, 1) of 8 for wide
     // blocks, element h (0..15) for tall ones.
@@ -227,9 +237,9 @@ struct Boxes {
 };
 
 // Chunk buffers that TMA fills in turn; thread 0 issues.  `turns`: the phases of the mbarriers, as bits.
-template <int N>
+template <int N, bool PACK>
 struct Ring {
-    Boxes a[N];
+    Boxes<PACK> a[N];
     int n, size, bufs;
     __device__ __forceinline__ void shape(const Slab& s) {
         size = 0;
@@ -292,11 +302,12 @@ __device__ __forceinline__ float sum_squares(const float (&u)[16]) {
 
 // The element-wise walk of a chunk: element (a, h) of a thread, A x H = 16 of them, a warp along the caller's
 // rows.  Offsets are a base and two steps.
-template <bool TALL>
+template <bool TALL, bool PACK>
 struct Walk {
     static constexpr int A = TALL ? 4 : 8, H = 16 / A;
     int row, col;              // the caller's, of element (0, 0)
     int rows, cols;
+    bool two;
     long long at;              // its place in an array with row pitch ld
     int staged;                // its place in the staging buffer
     __device__ __forceinline__ Walk(const Slab& s, int ch, int ld) {
@@ -305,19 +316,28 @@ struct Walk {
         col = lane + (TALL ? 0 : s.first(ch));
         rows = s.rows;
         cols = s.cols;
+        two = s.two;
         at = static_cast<long long>(row) * ld + col;
         staged = TALL ? lane * STG_PITCH + warp : warp * STG_PITCH + lane;
     }
-    __device__ __forceinline__ bool ok(int a, int h) const { return row + 16 * a < rows && col + 32 * h < cols; }
+    // Whether element (a, h) is the second block's, and its place from that of (0, 0).
+    static __device__ __forceinline__ constexpr bool second(int a, int h) { return PACK && (TALL ? h >= 2 : a >= 4); }
+    static __device__ __forceinline__ long long step(int a, int h, long long ld16, long long stride) {
+        if (!PACK) return a * ld16 + 32 * h;
+        return (TALL ? a * ld16 + 32 * (h & 1) : (a & 3) * ld16 + 32 * h) + (second(a, h) ? stride : 0ll);
+    }
+    __device__ __forceinline__ bool ok(int a, int h) const {
+        return row + 16 * (PACK && !TALL ? a & 3 : a) < rows && col + 32 * (PACK && TALL ? h & 1 : h) < cols && (!second(a, h) || two);
+    }
     __device__ __forceinline__ int place(int a, int h) const {
         return staged + (TALL ? 32 * h * STG_PITCH + 16 * a : 16 * a * STG_PITCH + 32 * h);
     }
 };
 
 // Out of line: their registers and code are not the iterations'.
-template <bool TALL>
+template <bool TALL, bool PACK>
 __device__ __noinline__ double slab_in_any(const Slab s, const SmallStackItem& item, long long b, const Momentum mo) {
-    using W = Walk<TALL>;
+    using W = Walk<TALL, PACK>;
     const int g_dtype = item.g_dtype, warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
     const uint8_t* g0 = static_cast<const uint8_t*>(item.G) + b * item.g_stride * (g_dtype == MUON_F32 ? 4 : 2);
     float* m0 = item.M + b * item.m_stride;
@@ -332,13 +352,13 @@ __device__ __noinline__ double slab_in_any(const Slab s, const SmallStackItem& i
 #pragma unroll
             for (int a = 0; a < W::A; ++a)
 #pragma unroll
-                for (int h = 0; h < W::H; ++h) u[a * W::H + h] = g.ok(a, h) ? widen(p[a * g16 + 32 * h]) : 0.f;
+                for (int h = 0; h < W::H; ++h) u[a * W::H + h] = g.ok(a, h) ? widen(p[W::step(a, h, g16, item.g_stride)]) : 0.f;
         });
         if (mo.on) {
 #pragma unroll
             for (int a = 0; a < W::A; ++a)
 #pragma unroll
-                for (int h = 0; h < W::H; ++h) m[a * W::H + h] = k.ok(a, h) ? m0[k.at + a * m16 + 32 * h] : 0.f;
+                for (int h = 0; h < W::H; ++h) m[a * W::H + h] = k.ok(a, h) ? m0[k.at + W::step(a, h, m16, item.m_stride)] : 0.f;
         }
     };
     fetch(0);
@@ -353,7 +373,7 @@ __device__ __noinline__ double slab_in_any(const Slab s, const SmallStackItem& i
 #pragma unroll
             for (int h = 0; h < W::H; ++h) {
                 buf[k.place(a, h)] = u[a * W::H + h];
-                if (mo.on && k.ok(a, h)) m0[k.at + a * m16 + 32 * h] = m[a * W::H + h];
+                if (mo.on && k.ok(a, h)) m0[k.at + W::step(a, h, m16, item.m_stride)] = m[a * W::H + h];
             }
         if (ch + 1 < s.nchunk) fetch(ch + 1);      // on its way while this chunk goes to TMEM
         __syncthreads();
@@ -364,9 +384,9 @@ __device__ __noinline__ double slab_in_any(const Slab s, const SmallStackItem& i
     }
     return ss;
 }
-template <bool TALL>
+template <bool TALL, bool PACK>
 __device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& item, long long b, float out) {
-    using W = Walk<TALL>;
+    using W = Walk<TALL, PACK>;
     const int w_dtype = item.w_dtype, warp = threadIdx.x >> 5, row = 32 * (warp & 3) + (threadIdx.x & 31), cg = warp >> 2;
     uint8_t* w0 = static_cast<uint8_t*>(item.W) + b * item.w_stride * (w_dtype == MUON_F32 ? 4 : 2);
     const int w_ld = item.w_ld;
@@ -384,7 +404,7 @@ __device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& it
             for (int a = 0; a < W::A; ++a)
 #pragma unroll
                 for (int h = 0; h < W::H; ++h)
-                    if (k.ok(a, h)) x[a * W::H + h] = p[a * w16 + 32 * h];
+                    if (k.ok(a, h)) x[a * W::H + h] = p[W::step(a, h, w16, item.w_stride)];
         };
         fetch(0);
 #pragma unroll 1
@@ -402,7 +422,8 @@ __device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& it
 #pragma unroll
                 for (int h = 0; h < W::H; ++h) {
                     const float v = buf[k.place(a, h)];
-                    if (k.ok(a, h)) narrow(p[a * w16 + 32 * h], update ? fmaf(step, v, decay * widen(x[a * W::H + h])) : step * v);
+                    if (k.ok(a, h))
+                        narrow(p[W::step(a, h, w16, item.w_stride)], update ? fmaf(step, v, decay * widen(x[a * W::H + h])) : step * v);
                 }
             if (ch + 1 < s.nchunk) fetch(ch + 1);
         }
@@ -418,14 +439,17 @@ struct SmallParams {
 constexpr int kFewItems = 5;
 static_assert(sizeof(SmallParams<kFewItems>) <= 4096, "the small form's parameters launch faster");
 
-template <int N>
+// PACK: two blocks with a short side of at most 64 share a cluster.  Their Gram matrices are the diagonal quarters of
+// the 128 x 128 product; the others are set to zero, and with them those of B~, so that neither block sees the other
+// (192 steps of 64 x 1024: 2 rounds of clusters instead of 3).
+template <int N, bool PACK>
 __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParams<N> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t bar_gram, bar_square, bar_apply[2], bar_rows, bar_a, bar_ring[kRing];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double red_norm[THREADS / 32];
-    __shared__ double parts[16];
+    __shared__ double parts[PACK ? 2 : 1][16];
 
     const SmallStackClass& k = p.k;
     const int C = k.cluster, w = k.slab;
@@ -443,10 +467,11 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         if (p.item[mid].block0 <= blk) lo = mid; else hi = mid - 1;
     }
     const SmallStackItem& it = p.item[lo];
-    const long long b = blk - it.block0;
+    const long long b = (PACK ? 2 : 1) * static_cast<long long>(blk - it.block0);
     const bool tall = k.rows > k.cols;
     const int q = warp & 3, cg = warp >> 2;        // TMEM lane quarter, column group
     const int row = 32 * q + lane;                 // this thread's row of X
+    const int half = PACK ? q >> 1 : 0;            // its block of the two
     const int nchunk = w >> 6;
     const float gs = k.gscale != nullptr ? __ldg(k.gscale) : 1.f;
     const bool mom = it.M != nullptr;
@@ -469,16 +494,17 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
 
-    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, panels, (w >> 6) * PANEL + FIXED_BYTES, t_lane, bar_ring, abort, status};
+    const bool two = PACK && b + 1 < it.count;
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, panels, (w >> 6) * PANEL + FIXED_BYTES, t_lane, bar_ring, abort, status};
     const Momentum mo = {gs, k.beta, mom, k.nesterov != 0};
     const bool tma_in = (it.vec & 1) && (!mom || (it.vec & 2)), tma_out = (it.vec & 4) != 0, update = it.decay != 0.f;
-    const Boxes boxes_w = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+    const Boxes<PACK> boxes_w = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
     uint32_t turns = 0;
 
     // ---------------------------------------------------------------- momentum, norm, U -> TMEM
     double ss = 0.0;
     if (tma_in) {
-        Ring<2> ring;
+        Ring<2, PACK> ring;
         ring.a[0] = {&it.map_g, it.g_dtype, it.g_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
         ring.a[1] = {&it.map_m, MUON_F32, 4, static_cast<int>(b)};
         ring.n = mom ? 2 : 1;
@@ -515,7 +541,19 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         if (tid == 0) bulk_wait_read<0>();
         __syncthreads();       // the buffers are free
     } else {
-        ss = tall ? slab_in_any<true>(slab, it, b, mo) : slab_in_any<false>(slab, it, b, mo);
+        ss = tall ? slab_in_any<true, PACK>(slab, it, b, mo) : slab_in_any<false, PACK>(slab, it, b, mo);
+        if (PACK) {            // a thread of that walk has elements of both blocks
+            tmem_st_wait();
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+            ss = 0.0;
+            for (int c = cg * 16; c < w; c += 64) {
+                float z[16];
+                tmem_ld_x16(t_lane + c, z);
+                ss += static_cast<double>(sum_squares(z));
+            }
+        }
     }
     tmem_st_wait();
     double sum = 0.0;
@@ -535,20 +573,26 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         __syncthreads();
         cluster_arrive();      // every CTA of the cluster runs, and is past its last read of `parts`
         cluster_wait();
-        if (tid < C) {
+        if (tid < (PACK ? 2 * C : C)) {
+            const int to = tid & (C - 1), of = tid / C;
             double s = 0.0;
-            for (int i = 0; i < THREADS / 32; ++i) s += red_norm[i];
-            st_cluster_f64(mapa_shared(smem_u32(&parts[rank]), tid), s);
+            for (int i = 0; i < THREADS / 32; ++i)
+                if (!PACK || ((i & 3) >> 1) == of) s += red_norm[i];
+            st_cluster_f64(mapa_shared(smem_u32(&parts[of][rank]), to), s);
         }
         cluster_arrive();
         cluster_wait();
-        sum = 0.0;
-        for (int i = 0; i < C; ++i) sum += parts[i];
-        if (sum > 1e-25 && sum < 1e36) break;      // the same in every CTA of the cluster
+        double sums[2] = {0.0, 0.0};
+#pragma unroll
+        for (int of = 0; of < (PACK ? 2 : 1); ++of)
+            for (int i = 0; i < C; ++i) sums[of] += parts[of][i];
+        sum = PACK && half ? sums[1] : sums[0];
+        // the same in every thread of the cluster
+        if (sums[0] > 1e-25 && sums[0] < 1e36 && (!two || (sums[1] > 1e-25 && sums[1] < 1e36))) break;
     }
     const double norm = sqrt(sum);
     const bool fin = isfinite(norm);
-    if (tid == 0 && rank == 0 && !fin) atomicOr(status, kDevErrNonfinite);
+    if (lane == 0 && (warp == 0 || (PACK && warp == 2)) && rank == 0 && !fin) atomicOr(status, kDevErrNonfinite);
     {
         // Z_0 = U * 2^e * zf, so that neither factor leaves fp32's range
         int ex = 0;
@@ -563,7 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             float z[16];
             tmem_ld_x16(t_lane + c, z);
 #pragma unroll
-            for (int h = 0; h < 16; ++h) z[h] = (z[h] * up) * zf;
+            for (int h = 0; h < 16; ++h) z[h] = PACK && !fin ? 0.f : (z[h] * up) * zf;   // packed: not into the other block
             tmem_st_x16(t_lane + c, z);
             put_panel16(panels, row, c, z, zs);
         }
@@ -582,22 +626,26 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         for (int j = 0; j < nchunk; ++j) {
             const int x = slab.first(j);
             if (x >= s_true) break;
-            for (int y = 0; y < r_true; y += 64)
-                tma_store_3d(&k.x, smem_u32(panels) + j * PANEL + y * 128, x, y, t * k.saved + keep_z);
+            for (int y = 0; y < (PACK ? two ? 128 : 64 : r_true); y += 64)
+                tma_store_3d(&k.x, smem_u32(panels) + j * PANEL + y * 128, x, PACK ? 0 : y, t * k.saved + keep_z + (PACK ? y >> 6 : 0));
         }
         bulk_commit();
     };
     auto keep_square = [&](const CUtensorMap* m, const uint8_t* src, int t) {
         if (rank != 0) return;
+        if (PACK) {
+            for (int of = 0; of < (two ? 2 : 1); ++of)
+                tma_store_3d(m, smem_u32(src) + of * (PANEL + 64 * 128), 0, 0, t * k.saved + keep_z + of);
+        } else
         for (int x = 0; x < r_true; x += 64)
             for (int y = 0; y < r_true; y += 64)
                 tma_store_3d(m, smem_u32(src) + (x >> 6) * PANEL + y * 128, x, y, t * k.saved + keep_z);
         bulk_commit();
     };
-    if (keep && tid == 0) {
-        keep_x(0);
-        if (rank == 0) {
-            float* info = k.info + static_cast<size_t>(keep_z) * kStackInfo;
+    if (keep && tid == 0) keep_x(0);
+    if (keep && lane == 0) {
+        if (rank == 0 && (warp == 0 || (two && warp == 2))) {
+            float* info = k.info + static_cast<size_t>(keep_z + half) * kStackInfo;
             info[0] = !fin ? NAN : norm > 0.0 ? k.f0 : 0.f;
             info[1] = 1.f;
             info[2] = static_cast<float>(1.0 / (norm + static_cast<double>(k.eps)));
@@ -676,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    v[e] *= f.ga;
+                    v[e] = PACK && (pc >> 3) != (ar >> 6) ? 0.f : v[e] * f.ga;
                     if (8 * pc + e == ar) v[e] -= f.diag;
                 }
                 const uint4 x = pack8(MUON_F16, v);
@@ -694,7 +742,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    v[e] = __uint_as_float(r[8 * s + e]) * f.ga;
+                    v[e] = PACK && (cg >> 1) != (row >> 6) ? 0.f : __uint_as_float(r[8 * s + e]) * f.ga;
                     if (32 * cg + 8 * s + e == row) v[e] -= f.diag;
                 }
                 *reinterpret_cast<uint4*>(Am + pn * PANEL + row * 128 + (((ps + s) ^ (row & 7)) << 4)) = pack8(MUON_F16, v);
@@ -779,10 +827,17 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
 
     // ---------------------------------------------------------------- result
     // Peers' last stores into this CTA are the last rows of A, which it has waited for.
+    if (PACK && !fin) {
+        const float nan[16] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
+        for (int c = cg * 16; c < w; c += 64) tmem_st_x16(t_lane + c, nan);
+        tmem_st_wait();
+    }
+    tc_fence_before();
     __syncthreads();           // every warp is past the last reads of A and B~
+    tc_fence_after();
     if (tma_out) {
         const float step = it.step * k.out, decay = it.decay;
-        Ring<1> ring;
+        Ring<1, PACK> ring;
         ring.a[0] = boxes_w;
         ring.n = 1;
         ring.shape(slab);
@@ -818,8 +873,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         }
         if (tid == 0) bulk_wait_read<0>();
     } else {
-        if (tall) slab_out_any<true>(slab, it, b, k.out);
-        else slab_out_any<false>(slab, it, b, k.out);
+        if (tall) slab_out_any<true, PACK>(slab, it, b, k.out);
+        else slab_out_any<false, PACK>(slab, it, b, k.out);
     }
     tc_fence_before();
     __syncthreads();
@@ -898,7 +953,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
-    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, false, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
     const bool tma_in = (it.vec & 1) != 0, tma_out = (it.vec & 4) != 0;
 
     auto load_x = [&](int t) {     // thread 0
@@ -941,7 +996,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     uint32_t turns = 0;
     double ss = 0.0;
     if (tma_in) {
-        Ring<1> ring;
+        Ring<1, false> ring;
         ring.a[0] = {&it.map_g, it.g_dtype, it.g_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
         ring.n = 1;
         ring.shape(slab);
@@ -959,7 +1014,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
     } else {
         const Momentum mo = {1.f, 0.f, false, false};
-        ss = tall ? slab_in_any<true>(slab, it, b, mo) : slab_in_any<false>(slab, it, b, mo);
+        ss = tall ? slab_in_any<true, false>(slab, it, b, mo) : slab_in_any<false, false>(slab, it, b, mo);
     }
     tmem_st_wait();
     double sum = cluster_sum(ss);
@@ -1193,7 +1248,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     tmem_st_wait();
     __syncthreads();
     if (tma_out) {
-        const Boxes boxes = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+        const Boxes<false> boxes = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
         const int size = boxes.bytes(), bufs = min(nchunk, slab.bytes / size);
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
@@ -1214,8 +1269,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
         if (tid == 0) bulk_wait_read<0>();
     } else {
-        if (tall) slab_out_any<true>(slab, it, b, 1.f);
-        else slab_out_any<false>(slab, it, b, 1.f);
+        if (tall) slab_out_any<true, false>(slab, it, b, 1.f);
+        else slab_out_any<false, false>(slab, it, b, 1.f);
     }
     tc_fence_before();
     __syncthreads();
@@ -1225,7 +1280,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     }
 }
 
-template <class P, class K, int N>
+template <class P, class K, int N, int PER>     // PER: blocks to a cluster
 cudaError_t launch(void (*kernel)(P), int most_smem, int smem, const SmallStackItem* items, int n, const K& k, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> ready[kMaxDevices];
@@ -1246,7 +1301,7 @@ cudaError_t launch(void (*kernel)(P), int most_smem, int smem, const SmallStackI
         for (int i = 0; i < p.n; ++i) {
             p.item[i] = items[i0 + i];
             p.item[i].block0 = blocks;
-            blocks += items[i0 + i].count;
+            blocks += (items[i0 + i].count + PER - 1) / PER;
         }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(k.cluster) * blocks, 1, 1);
@@ -1267,14 +1322,14 @@ cudaError_t launch(void (*kernel)(P), int most_smem, int smem, const SmallStackI
     return cudaSuccess;
 }
 
-template <int N>
+template <int N, bool PACK>
 cudaError_t run_step(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
-    return launch<SmallParams<N>, SmallStackClass, N>(stack_small_kernel<N>, smem_bytes(kSmallStackSlab), smem_bytes(k.slab), items, n,
-                                                      k, stream);
+    return launch<SmallParams<N>, SmallStackClass, N, PACK ? 2 : 1>(stack_small_kernel<N, PACK>, smem_bytes(kSmallStackSlab),
+                                                                    smem_bytes(k.slab), items, n, k, stream);
 }
 template <int N>
 cudaError_t run_grad(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream) {
-    return launch<SmallGradParams<N>, SmallGradClass, N>(stack_small_grad_kernel<N>, grad_smem_bytes(kSmallGradSlab),
+    return launch<SmallGradParams<N>, SmallGradClass, N, 1>(stack_small_grad_kernel<N>, grad_smem_bytes(kSmallGradSlab),
                                                          grad_smem_bytes(k.slab), items, n, k, stream);
 }
 
@@ -1291,7 +1346,7 @@ int stack_small_resident(int cluster) {
     }
     int n = of[dev][k].load();
     if (n == 0) {
-        const auto kernel = stack_small_kernel<kFewItems>;
+        const auto kernel = stack_small_kernel<kFewItems, false>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(cluster) * 148, 1, 1);
         cfg.blockDim = dim3(THREADS, 1, 1);
@@ -1314,7 +1369,9 @@ int stack_small_resident(int cluster) {
 }
 
 cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream) {
-    return n <= kFewItems ? run_step<kFewItems>(items, n, k, stream) : run_step<kSmallStackItems>(items, n, k, stream);
+    if (k.pack)
+        return n <= kFewItems ? run_step<kFewItems, true>(items, n, k, stream) : run_step<kSmallStackItems, true>(items, n, k, stream);
+    return n <= kFewItems ? run_step<kFewItems, false>(items, n, k, stream) : run_step<kSmallStackItems, false>(items, n, k, stream);
 }
 
 cudaError_t stack_small_grad_launch(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream) {

@@ -167,6 +167,7 @@ struct alignas(64) SmallStackClass {
     float f0;             // X_0 = f0 * X^_0
     SmallStackIter it[32];
     int rows, cols, cluster, slab, iters;   // slab: a multiple of 64, cluster * slab >= long side
+    int pack;             // 1: two blocks of an item (short side <= 64) to a cluster, in rows 0 .. and 64 ..
     float unit, out;      // Z_0 = unit * X_0; X_T = out * Z
     float beta, eps;
     int nesterov;
@@ -192,8 +193,8 @@ struct alignas(64) SmallGradClass {
     unsigned* status;
 };
 cudaError_t stack_small_grad_launch(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream);
-// Fills the item's maps and `vec` from its arrays.
-void small_stack_maps(SmallStackItem& it, int rows, int cols);
+// Fills the item's maps and `vec` from its arrays; pack as in the class.
+void small_stack_maps(SmallStackItem& it, int rows, int cols, bool pack);
 // Clusters of 1, 2, 4 or 8 CTAs that run at once on the current device (they do not fill it: 14 of 8, not 18).
 int stack_small_resident(int cluster);
 cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallStackClass& k, cudaStream_t stream);

@@ -158,7 +158,8 @@ StackClass make_class(int rows, int cols, const muon_ns_schedule& sch, const Bou
 // The scales of a class whose blocks run in one cluster each (stack_small.cu), or false where they do not:
 // a long side above 8 slabs, or a schedule whose product of coefficients a leaves the range in which the
 // state's unit keeps X^ and B~ inside fp16.
-bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, const Bounds& bd, SmallStackClass& k,
+// pairs: clusters where two blocks of a stack share one.
+bool small_class(int rows, int cols, int blocks, int pairs, const muon_ns_schedule& sch, const Bounds& bd, SmallStackClass& k,
                  std::vector<double>* kappas = nullptr) {
     const int r = std::min(rows, cols), s = std::max(rows, cols);
     if (r > kSmallStackSide || s > 8 * kSmallStackSlab) return false;
@@ -201,6 +202,9 @@ bool small_class(int rows, int cols, int blocks, const muon_ns_schedule& sch, co
     const int pieces = (s + 63) / 64;
     int C = 1;
     while (C * kSmallStackSlab < s) C *= 2;
+    // Where not all run at once, two blocks of up to 64 rows (or columns) share a cluster.
+    k.pack = r <= 64 && blocks > stack_small_resident(C);
+    if (k.pack) blocks = pairs;
     while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && blocks <= stack_small_resident(2 * C)) C *= 2;
     k.cluster = C;
     k.slab = (pieces + C - 1) / C * 64;
@@ -240,11 +244,14 @@ std::vector<SmallSet> find_small(std::vector<Shape>& shapes, const muon_ns_sched
             }
         for (auto& n : no) known = known || (n.first == rows && n.second == cols);
         if (known) continue;
-        long long blocks = 0;
+        long long blocks = 0, pairs = 0;
         for (const Shape& s : shapes)
-            if (s.rows == rows && s.cols == cols) blocks += s.count;
+            if (s.rows == rows && s.cols == cols) {
+                blocks += s.count;
+                pairs += (s.count + 1) / 2;
+            }
         SmallSet s;
-        if (small_class(rows, cols, static_cast<int>(blocks), sch, bd, s.k)) {
+        if (small_class(rows, cols, static_cast<int>(blocks), static_cast<int>(pairs), sch, bd, s.k)) {
             s.stacks.push_back(static_cast<int>(i));
             shapes[i].small = true;
             sets.push_back(s);
@@ -694,13 +701,13 @@ void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
         SmallStackClass k;
         std::vector<double> kappas;
         const bool both = c.s <= 8 * kSmallGradSlab;
-        if ((c.tall && !both) || !small_class(c.rows, c.cols, c.count, sch, bd, k, &kappas)) continue;
+        if ((c.tall && !both) || !small_class(c.rows, c.cols, c.count, c.count, sch, bd, k, &kappas)) continue;
         c.chip = true;
         c.chip_grad = both;
         c.gamma = kappas;
     }
 }
-SmallStackItem small_item(const ns_stack_desc& s, int first, int count) {
+SmallStackItem small_item(const ns_stack_desc& s, int first, int count, bool pack) {
     SmallStackItem it;
     std::memset(&it, 0, sizeof(it));
     it.G = bytes_at(s.X, first, s.x_stride, s.x_dtype);
@@ -713,7 +720,7 @@ SmallStackItem small_item(const ns_stack_desc& s, int first, int count) {
     it.w_dtype = s.y_dtype;
     it.count = count;
     it.step = 1.f;
-    small_stack_maps(it, s.rows, s.cols);
+    small_stack_maps(it, s.rows, s.cols, pack);
     return it;
 }
 template <class K>
@@ -727,7 +734,10 @@ muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedul
         const StackClass& c = g.classes[k];
         if (!c.chip) continue;
         SmallStackClass q;
-        if (!small_class(c.rows, c.cols, c.count, sch, bd, q)) return MUON_ERR_INVALID_ARG;
+        int pairs = 0;
+        for (const Part& p : g.parts)
+            if (p.cls == static_cast<int>(k)) pairs += (p.count + 1) / 2;
+        if (!small_class(c.rows, c.cols, c.count, pairs, sch, bd, q)) return MUON_ERR_INVALID_ARG;
         const int n = sch.n_iters * c.count;
         if (!kept_maps(q, c, n)) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
         q.info = c.info;
@@ -736,7 +746,7 @@ muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedul
         std::vector<SmallStackItem> items;
         for (const Part& p : g.parts) {
             if (p.cls != static_cast<int>(k)) continue;
-            items.push_back(small_item(d[p.stack], p.first, p.count));
+            items.push_back(small_item(d[p.stack], p.first, p.count, q.pack != 0));
             items.back().at = p.at;
         }
         const muon_status st = launch_small(items, q, small_flops(q, c.count), call);
@@ -782,7 +792,7 @@ muon_status reverse_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_sche
         std::vector<SmallStackItem> items;
         for (const Part& p : g.parts) {
             if (p.cls != static_cast<int>(k)) continue;
-            items.push_back(small_item(d[p.stack], p.first, p.count));
+            items.push_back(small_item(d[p.stack], p.first, p.count, false));
             items.back().at = p.at;
         }
         const double flops = static_cast<double>(c.count) * T * (6.0 * c.r * c.r * c.s + 2.0 * c.r * c.r * c.r);
@@ -809,7 +819,7 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
         std::vector<SmallStackItem> items;
         double blocks = 0.0;
         for (int i : set.stacks) {
-            items.push_back(small_item(d[i], 0, d[i].count));
+            items.push_back(small_item(d[i], 0, d[i].count, set.k.pack != 0));
             blocks += d[i].count;
         }
         set.k.status = call.status;
@@ -1088,7 +1098,7 @@ muon_status step(const muon_stack_desc* d, const std::vector<Shape>& shapes, std
             it.count = s.count;
             it.decay = static_cast<float>(1.0 - static_cast<double>(hp.lr) * hp.weight_decay);
             it.step = static_cast<float>(-static_cast<double>(hp.lr) * shape_scale(s.rows, s.cols, hp.scale_mode));
-            small_stack_maps(it, s.rows, s.cols);
+            small_stack_maps(it, s.rows, s.cols, set.k.pack != 0);
             items.push_back(it);
             blocks += s.count;
         }
@@ -1231,7 +1241,7 @@ bool encode_stack_tmap(CUtensorMap* out, const void* base, int rows, int cols, i
                       static_cast<long long>(rows) * cols, 64);
 }
 
-void small_stack_maps(SmallStackItem& it, int rows, int cols) {
+void small_stack_maps(SmallStackItem& it, int rows, int cols, bool pack) {
     it.vec = 0;
     auto one = [&](CUtensorMap& m, int bit, const void* p, int dtype, int ld, long long stride) {
         if (p == nullptr) return;
@@ -1246,7 +1256,7 @@ void small_stack_maps(SmallStackItem& it, int rows, int cols) {
                                          : dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         // what the encoder refuses goes element by element
-        if (encode_map(&m, p, type, static_cast<int>(elem_size(dtype)), rows, cols, it.count, l, t, rows > cols ? 64 : 128))
+        if (encode_map(&m, p, type, static_cast<int>(elem_size(dtype)), rows, cols, it.count, l, t, rows > cols || pack ? 64 : 128))
             it.vec |= bit;
     };
     one(it.map_g, 1, it.G, it.g_dtype, it.g_ld, it.g_stride);

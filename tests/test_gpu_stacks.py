@@ -733,3 +733,64 @@ def test_norm_of_long_tensors(dtype):
     h[4] = float("inf")
     mb.grad_norm_batched([h], 1.0, out, ws)
     assert float(out[0]) == float("inf") and mb.device_status(ws) == mb.MUON_ERR_NONFINITE
+
+
+@pytest.mark.parametrize("shape", [(151, 64, 320), (151, 320, 64), (149, 33, 65), (149, 65, 33), (79, 64, 1024), (75, 1000, 61),
+                                   (201, 1, 5), (160, 64, 64)], ids=str)
+@pytest.mark.parametrize("x_dtype,y_dtype,pad", [(BF, BF, 0), (FP, HF, 8), (HF, FP, 3)])
+def test_more_short_blocks_than_run_at_once(shape, x_dtype, y_dtype, pad):
+    """Two to a cluster, an odd number of them, neighbours of every kind: with a zero block, one that is not finite
+    and sizes far apart.  What the padding holds stays."""
+    n = shape[0]
+    x, _ = padded(*shape, pad, x_dtype)
+    x.copy_(blocks(230, *shape, x_dtype))
+    x[2] = 0
+    x[5, -1, -1] = float("nan")
+    x[6] *= 64
+    x[9, 0, 0] = float("inf")
+    y, buf = padded(*shape, pad, y_dtype)
+    ws = run([mb.Stack(x, y)], mb.Schedule.fixed(T, ref.STABLE))
+    assert mb.device_status(ws) == mb.MUON_ERR_NONFINITE
+    assert bool(torch.isnan(y[5]).all()) and bool(torch.isnan(y[9]).all()) and bool((y[2] == 0).all())
+    ok = [b for b in list(range(12)) + [n // 2, n - 2, n - 1] if b not in (2, 5, 9)]
+    for b in ok:
+        want = ref.ns(x[b], [ref.STABLE] * T)
+        most = ref.tol_vector([ref.STABLE] * T, y_dtype) if min(shape[1:]) == 1 else ref.tol_stable(y_dtype)
+        assert ref.rel(y[b], want) <= most, b
+    assert int(torch.isnan(y.float()).flatten(1).any(dim=1).sum()) == 2
+    if pad:
+        assert bool((buf[:, :, shape[2]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("shape,counts", [((64, 1024), (50, 33)), ((60, 333), (101, 1, 90)), ((300, 24), (160,))], ids=str)
+def test_steps_and_gradients_of_more_short_blocks_than_run_at_once(shape, counts):
+    """Several stacks of one shape, whose last blocks stay alone."""
+    sch = mb.Schedule.fixed(T)
+    w = [blocks(240 + i, c, *shape, BF, std=0.1) for i, c in enumerate(counts)]
+    g = [blocks(250 + i, c, *shape, BF) for i, c in enumerate(counts)]
+    m = [blocks(260 + i, c, *shape, FP) for i, c in enumerate(counts)]
+    old = [(a.clone(), b.clone()) for a, b in zip(w, m)]
+    hp = mb.hyper(0.02, 0.95, 0.1, True, "moonlight", sch)
+    st = [mb.MuonStack(a, b, c) for a, b, c in zip(w, g, m)]
+    ws = mb.workspace(mb.muon_stacks_workspace_size(st, hp))
+    mb.muon_step_stacks(st, hp, ws)
+    assert mb.device_status(ws) == mb.MUON_OK
+    step = 0.02 * ref.scale(*shape, "moonlight")
+    for i, c in enumerate(counts):
+        for b in sorted({0, c // 2, c - 1}):
+            ww, mm, o = ref.muon(old[i][0][b], g[i][b], old[i][1][b], 0.02, 0.95, 0.1, True, "moonlight", [ref.KJ] * T)
+            assert ref.rel(m[i][b], mm) <= 2 * 2.0 ** -23
+            bound = step * ref.tol_kj(FP) * o.norm() + (ref.half_step(BF) + 2.0 ** -23) * ww.norm() + 1e-12
+            assert float((w[i][b].double() - ww).norm()) <= float(bound), (i, b)
+    # iterates kept two to a cluster, read one to a cluster
+    ys, dx = [torch.empty_like(a) for a in m], [torch.empty_like(a) for a in m]
+    dy = [blocks(270 + i, c, *shape, FP, std=1.0) for i, c in enumerate(counts)]
+    stacks, grads = [mb.Stack(a, b) for a, b in zip(m, ys)], [mb.Stack(a, b) for a, b in zip(dy, dx)]
+    saved = mb.workspace(mb.ns_stacks_saved_size(stacks, sch))
+    run(stacks, sch, saved=saved)
+    ws = mb.workspace(mb.ns_stacks_backward_workspace_size(grads, sch))
+    mb.ns_orthogonalize_stacks_backward(grads, sch, saved, ws)
+    for i, c in enumerate(counts):
+        for b in sorted({0, c // 2, c - 1}):
+            assert ref.rel(ys[i][b], ref.ns(m[i][b], [ref.KJ] * T)) <= ref.tol_kj(FP), (i, b)
+            assert ref.rel(dx[i][b], ref.ns_grad(m[i][b], dy[i][b], [ref.KJ] * T)) <= 2 * ref.tol_kj(FP), (i, b)
