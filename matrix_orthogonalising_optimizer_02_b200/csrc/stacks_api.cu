@@ -200,12 +200,17 @@ bool small_class(int rows, int cols, int blocks, int pairs, const muon_ns_schedu
     // with 4 CTAs each, 98 with 8, of which two do not start before others end; 12 blocks: 57 and 53).  Up to 256
     // columns one CTA is faster than several that have to exchange their sums.
     const int pieces = (s + 63) / 64;
-    int C = 1;
-    while (C * kSmallStackSlab < s) C *= 2;
-    // Where not all run at once, two blocks of up to 64 rows (or columns) share a cluster.
-    k.pack = r <= 64 && blocks > stack_small_resident(C);
-    if (k.pack) blocks = pairs;
-    while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && blocks <= stack_small_resident(2 * C)) C *= 2;
+    int least = 1;
+    while (least * kSmallStackSlab < s) least *= 2;
+    auto widest = [&](int clusters) {
+        int C = least;
+        while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && clusters <= stack_small_resident(2 * C)) C *= 2;
+        return C;
+    };
+    // Two blocks of up to 64 rows (or columns) share a cluster where not all run at once, or where it can be wider then.
+    int C = widest(blocks);
+    k.pack = r <= 64 && (blocks > stack_small_resident(C) || widest(pairs) > C);
+    if (k.pack) C = widest(pairs);
     k.cluster = C;
     k.slab = (pieces + C - 1) / C * 64;
     return true;
