@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             float z[16];
             tmem_ld_x16(t_lane + c, z);
 #pragma unroll
-            for (int h = 0; h < 16; ++h) z[h] = PACK && !fin ? 0.f : (z[h] * up) * zf;   // packed: not into the other block
+            for (int h = 0; h < 16; ++h) z[h] = fin ? (z[h] * up) * zf : 0.f;   // nothing of it into another block
             tmem_st_x16(t_lane + c, z);
             put_panel16(panels, row, c, z, zs);
         }
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
 
     // ---------------------------------------------------------------- result
     // Peers' last stores into this CTA are the last rows of A, which it has waited for.
-    if (PACK && !fin) {
+    if (!fin) {
         const float nan[16] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
         for (int c = cg * 16; c < w; c += 64) tmem_st_x16(t_lane + c, nan);
         tmem_st_wait();
@@ -904,14 +904,14 @@ struct SmallGradParams {
 };
 static_assert(sizeof(SmallGradParams<kFewItems>) <= 4096, "the small form's parameters launch faster");
 
-template <int N>
+template <int N, bool PACK>
 __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __grid_constant__ SmallGradParams<N> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t bar_s, bar_p, bar_apply, bar_rows, bar_all, bar_ab, bar_x, bar_ring[kRing];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double red_sum[THREADS / 32];
-    __shared__ double parts[16];
+    __shared__ double parts[PACK ? 2 : 1][16];
 
     const SmallGradClass& k = p.k;
     const int C = k.cluster, w = k.slab, nchunk = w >> 6;
@@ -931,10 +931,11 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         if (p.item[mid].block0 <= blk) lo = mid; else hi = mid - 1;
     }
     const SmallStackItem& it = p.item[lo];
-    const long long b = blk - it.block0;
+    const long long b = (PACK ? 2 : 1) * static_cast<long long>(blk - it.block0);
     const int kept = it.at + static_cast<int>(b);
     const int q = warp & 3, cg = warp >> 2, row = 32 * q + lane;
-    const bool tall = k.rows > k.cols;
+    const int half = PACK ? q >> 1 : 0;            // this thread's block of the two
+    const bool tall = k.rows > k.cols, two = PACK && b + 1 < it.count;
 
     if (tid == 0) {
         for (uint64_t* x : {&bar_s, &bar_p, &bar_apply, &bar_rows, &bar_all, &bar_ab, &bar_x}) mbar_init(x, 1);
@@ -953,25 +954,33 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
-    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, false, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
     const bool tma_in = (it.vec & 1) != 0, tma_out = (it.vec & 4) != 0;
 
     auto load_x = [&](int t) {     // thread 0
-        mbar_arrive_expect_tx(&bar_x, static_cast<uint32_t>(nchunk * PANEL));
+        const int ys = PACK && !two ? 64 : 128;
+        mbar_arrive_expect_tx(&bar_x, static_cast<uint32_t>(nchunk * ys * 128));
         for (int j = 0; j < nchunk; ++j)
-            for (int y = 0; y < 128; y += 64)
-                tma_load_3d(smem_u32(Xp) + j * PANEL + y * 128, &k.x, smem_u32(&bar_x), slab.first(j), y, t * k.saved + kept);
+            for (int y = 0; y < ys; y += 64)
+                tma_load_3d(smem_u32(Xp) + j * PANEL + y * 128, &k.x, smem_u32(&bar_x), slab.first(j), PACK ? 0 : y,
+                            t * k.saved + kept + (PACK ? y >> 6 : 0));
     };
     auto load_ab = [&](int t) {    // thread 0
         mbar_arrive_expect_tx(&bar_ab, 2 * A_BYTES);
         for (int x = 0; x < 128; x += 64)
             for (int y = 0; y < 128; y += 64) {
+                // packed: the blocks' matrices on the diagonal, zeros (from beyond the matrix) beside them and where
+                // there is no second block
                 const uint32_t at = (x >> 6) * PANEL + y * 128;
-                tma_load_3d(smem_u32(Am) + at, &k.a, smem_u32(&bar_ab), x, y, t * k.saved + kept);
-                tma_load_3d(smem_u32(Bm) + at, &k.b, smem_u32(&bar_ab), x, y, t * k.saved + kept);
+                const bool zeros = PACK && (x != y || (x > 0 && !two));
+                const int mx = PACK ? zeros ? 64 : 0 : x, my = PACK ? 0 : y;
+                const int z = t * k.saved + kept + (PACK && x > 0 && y > 0 && two ? 1 : 0);
+                tma_load_3d(smem_u32(Am) + at, &k.a, smem_u32(&bar_ab), mx, my, z);
+                tma_load_3d(smem_u32(Bm) + at, &k.b, smem_u32(&bar_ab), mx, my, z);
             }
     };
-    // The cluster's sum, in rank order, in every thread of every CTA.
+    // The cluster's sums of the two blocks (packed: by rows), in rank order, in every thread of every CTA.
+    double sums[2] = {0.0, 0.0};
     auto cluster_sum = [&](double v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -979,24 +988,32 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         __syncthreads();
         cluster_arrive();      // every CTA of the cluster runs, and is past its last read of `parts`
         cluster_wait();
-        if (tid < C) {
+        if (tid < (PACK ? 2 * C : C)) {
+            const int to = tid & (C - 1), of = tid / C;
             double s = 0.0;
-            for (int i = 0; i < THREADS / 32; ++i) s += red_sum[i];
-            st_cluster_f64(mapa_shared(smem_u32(&parts[rank]), tid), s);
+            for (int i = 0; i < THREADS / 32; ++i)
+                if (!PACK || ((i & 3) >> 1) == of) s += red_sum[i];
+            st_cluster_f64(mapa_shared(smem_u32(&parts[of][rank]), to), s);
         }
         cluster_arrive();
         cluster_wait();
-        double s = 0.0;
-        for (int i = 0; i < C; ++i) s += parts[i];
-        return s;
+#pragma unroll
+        for (int of = 0; of < (PACK ? 2 : 1); ++of) {
+            sums[of] = 0.0;
+            for (int i = 0; i < C; ++i) sums[of] += parts[of][i];
+        }
+        return PACK && half ? sums[1] : sums[0];
     };
 
     // ---------------------------------------------------------------- gradient of the output -> TMEM, its norm
+    if (PACK && !two)      // X^ of a block that is not there
+        for (int i = tid; i < nchunk * 512; i += THREADS)
+            *reinterpret_cast<uint4*>(Xp + (i >> 9) * PANEL + 64 * 128 + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
     if (tid == 0) load_x(k.iters - 1);
     uint32_t turns = 0;
     double ss = 0.0;
     if (tma_in) {
-        Ring<1, false> ring;
+        Ring<1, PACK> ring;
         ring.a[0] = {&it.map_g, it.g_dtype, it.g_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
         ring.n = 1;
         ring.shape(slab);
@@ -1014,11 +1031,20 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
     } else {
         const Momentum mo = {1.f, 0.f, false, false};
-        ss = tall ? slab_in_any<true, false>(slab, it, b, mo) : slab_in_any<false, false>(slab, it, b, mo);
+        ss = tall ? slab_in_any<true, PACK>(slab, it, b, mo) : slab_in_any<false, PACK>(slab, it, b, mo);
+        if (PACK) {            // a thread of that walk has elements of both blocks
+            tmem_st_wait();
+            ss = 0.0;
+            for (int c = cg * 16; c < w; c += 64) {
+                float z[16];
+                tmem_ld_x16(t_lane + c, z);
+                ss += static_cast<double>(sum_squares(z));
+            }
+        }
     }
     tmem_st_wait();
     double sum = cluster_sum(ss);
-    if (!(sum > 1e-25 && sum < 1e36)) {     // squares outside fp32's range: once more in fp64 (all CTAs alike)
+    if (!(sums[0] > 1e-25 && sums[0] < 1e36 && (!two || (sums[1] > 1e-25 && sums[1] < 1e36)))) {     // squares outside fp32's range: once more in fp64 (all CTAs alike)
         ss = 0.0;
         for (int c = cg * 16; c < w; c += 64) {
             float z[16];
@@ -1029,20 +1055,27 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         sum = cluster_sum(ss);
     }
     const double norm = sqrt(sum);
-    const bool fin = isfinite(norm);
-    if (tid == 0 && rank == 0 && !fin) atomicOr(status, kDevErrNonfinite);
+    if (lane == 0 && (warp == 0 || (PACK && warp == 2)) && rank == 0 && !isfinite(norm)) atomicOr(status, kDevErrNonfinite);
+    // The factors f0 of the blocks.  One that is not finite, or whose gradient is not, goes on with zeros, so that
+    // nothing of it gets into another, and ends as NaN.
+    float f0s[2] = {k.info[static_cast<size_t>(kept) * kStackInfo], 0.f};
+    if (two) f0s[1] = k.info[static_cast<size_t>(kept + 1) * kStackInfo];
+    const float* info = k.info + static_cast<size_t>(kept + (half && two ? 1 : 0)) * kStackInfo;
+    const bool fin = isfinite(norm) && isfinite(half ? f0s[1] : f0s[0]);
+#pragma unroll
+    for (float& f : f0s)
+        if (!isfinite(f)) f = 0.f;
+    const float f0 = half ? f0s[1] : f0s[0];
     int ex = 0;
     if (fin && norm > 0.0) ex = max(-126, min(126, -(ilogb(norm) + 1)));
     const float up = __int_as_float((ex + 127) << 23);
-    const float* info = k.info + static_cast<size_t>(kept) * kStackInfo;
-    const float f0 = info[0];
     {
         const float d = k.it[k.iters - 1].d;
         for (int c = cg * 16; c < w; c += 64) {
             float z[16];
             tmem_ld_x16(t_lane + c, z);
 #pragma unroll
-            for (int h = 0; h < 16; ++h) z[h] *= up;
+            for (int h = 0; h < 16; ++h) z[h] = fin ? z[h] * up : 0.f;
             tmem_st_x16(t_lane + c, z);
             put_panel16(Dp, row, c, z, d);
         }
@@ -1091,7 +1124,6 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         tmem_ld_32x32b_x32(t_lane + ACC_G + 32 * cg, r);
         tmem_ld_wait();
         tc_fence_before();
-        const float fs = f.s * f0t;
         if (C > 1) {
             // as the Gram matrix's rows
             cluster_wait();        // every CTA's buffers are free
@@ -1117,7 +1149,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= fs;
+                for (int e = 0; e < 8; ++e) v[e] = PACK && (pc >> 3) != (ar >> 6) ? 0.f : v[e] * f.s * (t == 0 ? f0s[PACK ? ar >> 6 : 0] : 1.f);
                 const uint4 x = pack8(MUON_F16, v);
                 const uint32_t off = (pc >> 3) * PANEL + ar * 128 + (((pc & 7) ^ (ar & 7)) << 4);
                 for (int j = 0; j < C; ++j) {
@@ -1137,7 +1169,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
             for (int s = 0; s < 4; ++s) {
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * s + e]) * fs;
+                for (int e = 0; e < 8; ++e) v[e] = PACK && (cg >> 1) != (row >> 6) ? 0.f : __uint_as_float(r[8 * s + e]) * f.s * f0t;
                 *reinterpret_cast<uint4*>(Sm + pn * PANEL + row * 128 + (((ps + s) ^ (row & 7)) << 4)) = pack8(MUON_F16, v);
             }
         }
@@ -1235,8 +1267,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     }
     dot = cluster_sum(dot);
     const double n = info[3], eps = static_cast<double>(k.eps), sd = 1.0 / static_cast<double>(up);
-    const double corr = n > 0.0 ? dot * sd * f0 * (n + eps) / n : (isnan(f0) ? static_cast<double>(f0) : 0.0);
-    const float od = static_cast<float>(sd / (n + eps)), ox = static_cast<float>(-corr * f0 / (n + eps));
+    const double corr = n > 0.0 ? dot * sd * f0 * (n + eps) / n : 0.0;
+    const float od = fin ? static_cast<float>(sd / (n + eps)) : NAN, ox = static_cast<float>(-corr * f0 / (n + eps));
     for (int c = cg * 16; c < w; c += 64) {
         float z[16], x[16];
         tmem_ld_x16(t_lane + c, z);
@@ -1248,7 +1280,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     tmem_st_wait();
     __syncthreads();
     if (tma_out) {
-        const Boxes<false> boxes = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
+        const Boxes<PACK> boxes = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
         const int size = boxes.bytes(), bufs = min(nchunk, slab.bytes / size);
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
@@ -1269,8 +1301,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
         if (tid == 0) bulk_wait_read<0>();
     } else {
-        if (tall) slab_out_any<true, false>(slab, it, b, 1.f);
-        else slab_out_any<false, false>(slab, it, b, 1.f);
+        if (tall) slab_out_any<true, PACK>(slab, it, b, 1.f);
+        else slab_out_any<false, PACK>(slab, it, b, 1.f);
     }
     tc_fence_before();
     __syncthreads();
@@ -1327,10 +1359,11 @@ cudaError_t run_step(const SmallStackItem* items, int n, const SmallStackClass& 
     return launch<SmallParams<N>, SmallStackClass, N, PACK ? 2 : 1>(stack_small_kernel<N, PACK>, smem_bytes(kSmallStackSlab),
                                                                     smem_bytes(k.slab), items, n, k, stream);
 }
-template <int N>
+template <int N, bool PACK>
 cudaError_t run_grad(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream) {
-    return launch<SmallGradParams<N>, SmallGradClass, N, 1>(stack_small_grad_kernel<N>, grad_smem_bytes(kSmallGradSlab),
-                                                         grad_smem_bytes(k.slab), items, n, k, stream);
+    return launch<SmallGradParams<N>, SmallGradClass, N, PACK ? 2 : 1>(stack_small_grad_kernel<N, PACK>,
+                                                                       grad_smem_bytes(kSmallGradSlab), grad_smem_bytes(k.slab),
+                                                                       items, n, k, stream);
 }
 
 }  // namespace
@@ -1375,7 +1408,9 @@ cudaError_t stack_small_launch(const SmallStackItem* items, int n, const SmallSt
 }
 
 cudaError_t stack_small_grad_launch(const SmallStackItem* items, int n, const SmallGradClass& k, cudaStream_t stream) {
-    return n <= kFewItems ? run_grad<kFewItems>(items, n, k, stream) : run_grad<kSmallStackItems>(items, n, k, stream);
+    if (k.pack)
+        return n <= kFewItems ? run_grad<kFewItems, true>(items, n, k, stream) : run_grad<kSmallStackItems, true>(items, n, k, stream);
+    return n <= kFewItems ? run_grad<kFewItems, false>(items, n, k, stream) : run_grad<kSmallStackItems, false>(items, n, k, stream);
 }
 
 }  // namespace muon

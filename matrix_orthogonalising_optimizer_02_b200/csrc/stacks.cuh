@@ -189,6 +189,7 @@ struct alignas(64) SmallGradClass {
     int saved;
     SmallGradIter it[32];
     int rows, cols, cluster, slab, iters;
+    int pack;             // as above
     float eps;
     unsigned* status;
 };

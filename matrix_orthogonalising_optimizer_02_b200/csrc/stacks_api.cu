@@ -155,10 +155,31 @@ StackClass make_class(int rows, int cols, const muon_ns_schedule& sch, const Bou
 }
 
 // ---------------------------------------------------------------- classes that run on chip
+// Clusters of the on-chip kernels.  As few CTAs as hold the block; more while all blocks' clusters still run at once
+// (16 blocks of 96 x 641: 55 us with 4 CTAs each, 98 with 8, of which two do not start before others end; 12 blocks: 57
+// and 53).  Up to 256 columns one CTA is faster than several that have to exchange their sums.  Two blocks of up to 64
+// rows (or columns) share a cluster where not all run at once (96 of 64 x 2048: 242 us apart, 173 together), or where
+// the cluster can be wider then (37 of 64 x 1024: 70 and 55).  pairs: clusters where two blocks of a stack share one.
+template <class K>
+void set_clusters(K& k, int r, int s, int blocks, int pairs, int most_slab) {
+    const int pieces = (s + 63) / 64;
+    int least = 1;
+    while (least * most_slab < s) least *= 2;
+    auto widest = [&](int clusters) {
+        int C = least;
+        while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && clusters <= stack_small_resident(2 * C)) C *= 2;
+        return C;
+    };
+    int C = widest(blocks);
+    k.pack = r <= 64 && (blocks > stack_small_resident(C) || widest(pairs) > C);
+    if (k.pack) C = widest(pairs);
+    k.cluster = C;
+    k.slab = (pieces + C - 1) / C * 64;
+}
+
 // The scales of a class whose blocks run in one cluster each (stack_small.cu), or false where they do not:
 // a long side above 8 slabs, or a schedule whose product of coefficients a leaves the range in which the
 // state's unit keeps X^ and B~ inside fp16.
-// pairs: clusters where two blocks of a stack share one.
 bool small_class(int rows, int cols, int blocks, int pairs, const muon_ns_schedule& sch, const Bounds& bd, SmallStackClass& k,
                  std::vector<double>* kappas = nullptr) {
     const int r = std::min(rows, cols), s = std::max(rows, cols);
@@ -196,23 +217,7 @@ bool small_class(int rows, int cols, int blocks, int pairs, const muon_ns_schedu
     k.out = static_cast<float>(pa / unit);
     k.eps = sch.eps;
     k.f0 = static_cast<float>(1.0 / tau0);
-    // As few CTAs as hold the block; more while all blocks' clusters still run at once (16 blocks of 96 x 641: 57 us
-    // with 4 CTAs each, 98 with 8, of which two do not start before others end; 12 blocks: 57 and 53).  Up to 256
-    // columns one CTA is faster than several that have to exchange their sums.
-    const int pieces = (s + 63) / 64;
-    int least = 1;
-    while (least * kSmallStackSlab < s) least *= 2;
-    auto widest = [&](int clusters) {
-        int C = least;
-        while (s > 256 && 2 * C <= 8 && 2 * C <= pieces && clusters <= stack_small_resident(2 * C)) C *= 2;
-        return C;
-    };
-    // Two blocks of up to 64 rows (or columns) share a cluster where not all run at once, or where it can be wider then.
-    int C = widest(blocks);
-    k.pack = r <= 64 && (blocks > stack_small_resident(C) || widest(pairs) > C);
-    if (k.pack) C = widest(pairs);
-    k.cluster = C;
-    k.slab = (pieces + C - 1) / C * 64;
+    set_clusters(k, r, s, blocks, pairs, kSmallStackSlab);
     return true;
 }
 
@@ -712,6 +717,12 @@ void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
         c.gamma = kappas;
     }
 }
+int pairs_of(const Group& g, int cls) {
+    int pairs = 0;
+    for (const Part& p : g.parts)
+        if (p.cls == cls) pairs += (p.count + 1) / 2;
+    return pairs;
+}
 SmallStackItem small_item(const ns_stack_desc& s, int first, int count, bool pack) {
     SmallStackItem it;
     std::memset(&it, 0, sizeof(it));
@@ -739,10 +750,7 @@ muon_status keep_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_schedul
         const StackClass& c = g.classes[k];
         if (!c.chip) continue;
         SmallStackClass q;
-        int pairs = 0;
-        for (const Part& p : g.parts)
-            if (p.cls == static_cast<int>(k)) pairs += (p.count + 1) / 2;
-        if (!small_class(c.rows, c.cols, c.count, pairs, sch, bd, q)) return MUON_ERR_INVALID_ARG;
+        if (!small_class(c.rows, c.cols, c.count, pairs_of(g, static_cast<int>(k)), sch, bd, q)) return MUON_ERR_INVALID_ARG;
         const int n = sch.n_iters * c.count;
         if (!kept_maps(q, c, n)) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
         q.info = c.info;
@@ -787,17 +795,11 @@ muon_status reverse_on_chip(Group& g, const ns_stack_desc* d, const muon_ns_sche
         q.iters = T;
         q.eps = sch.eps;
         q.status = call.status;
-        // as in small_class
-        const int pieces = (c.s + 63) / 64;
-        int C = 1;
-        while (C * kSmallGradSlab < c.s) C *= 2;
-        while (c.s > 256 && 2 * C <= 8 && 2 * C <= pieces && c.count <= stack_small_resident(2 * C)) C *= 2;
-        q.cluster = C;
-        q.slab = (pieces + C - 1) / C * 64;
+        set_clusters(q, c.r, c.s, c.count, pairs_of(g, static_cast<int>(k)), kSmallGradSlab);
         std::vector<SmallStackItem> items;
         for (const Part& p : g.parts) {
             if (p.cls != static_cast<int>(k)) continue;
-            items.push_back(small_item(d[p.stack], p.first, p.count, false));
+            items.push_back(small_item(d[p.stack], p.first, p.count, q.pack != 0));
             items.back().at = p.at;
         }
         const double flops = static_cast<double>(c.count) * T * (6.0 * c.r * c.r * c.s + 2.0 * c.r * c.r * c.r);

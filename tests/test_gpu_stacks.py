@@ -794,3 +794,31 @@ def test_steps_and_gradients_of_more_short_blocks_than_run_at_once(shape, counts
         for b in sorted({0, c // 2, c - 1}):
             assert ref.rel(ys[i][b], ref.ns(m[i][b], [ref.KJ] * T)) <= ref.tol_kj(FP), (i, b)
             assert ref.rel(dx[i][b], ref.ns_grad(m[i][b], dy[i][b], [ref.KJ] * T)) <= 2 * ref.tol_kj(FP), (i, b)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(161, 64, 100), (41, 60, 1500), (77, 640, 33), (3, 90, 400)])
+def test_gradient_of_short_blocks_beside_bad_ones(n, rows, cols):
+    """An input, or a gradient, that is not finite makes its own block's gradient NaN and no other's."""
+    x = blocks(280, n, rows, cols, FP, std=0.5)
+    dy = blocks(281, n, rows, cols, FP, std=1.0)
+    x[0, 3, 3] = float("nan")
+    dy[n - 2, 1, 1] = float("inf")
+    if n > 8:
+        dy[4] = 0
+        x[7] = 0
+    sch = mb.Schedule.fixed(T, ref.STABLE)
+    dx = torch.empty_like(x)
+    stacks, grads = [mb.Stack(x, torch.empty_like(x))], [mb.Stack(dy, dx)]
+    saved = mb.workspace(mb.ns_stacks_saved_size(stacks, sch))
+    run(stacks, sch, saved=saved)
+    ws = mb.workspace(mb.ns_stacks_backward_workspace_size(grads, sch))
+    mb.ns_orthogonalize_stacks_backward(grads, sch, saved, ws)
+    assert mb.device_status(ws) == mb.MUON_ERR_NONFINITE
+    assert bool(torch.isnan(dx[0]).all()) and bool(torch.isnan(dx[n - 2]).all())
+    assert int(torch.isnan(dx).flatten(1).any(dim=1).sum()) == 2
+    for b in [b for b in list(range(12)) + [n - 3, n - 1] if b < n and b not in (0, n - 2)]:
+        want = ref.ns_grad(x[b], dy[b], [ref.STABLE] * T)
+        if n > 8 and b == 4:
+            assert bool((dx[b] == 0).all())
+        else:
+            assert ref.rel(dx[b], want) <= ref.tol_stable(FP), b
