@@ -441,7 +441,7 @@ static_assert(sizeof(SmallParams<kFewItems>) <= 4096, "the small form's paramete
 
 // PACK: two blocks with a short side of at most 64 share a cluster.  Their Gram matrices are the diagonal quarters of
 // the 128 x 128 product; the others are set to zero, and with them those of B~, so that neither block sees the other
-// (192 steps of 64 x 1024: 2 rounds of clusters instead of 3).
+// (192 steps of 64 x 1024: 2 rounds of clusters instead of 3, 230 and 169 us).
 template <int N, bool PACK>
 __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParams<N> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
