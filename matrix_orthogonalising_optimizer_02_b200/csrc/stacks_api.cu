@@ -313,6 +313,20 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
     if (groups.back().parts.empty()) groups.pop_back();
     return groups;
 }
+// Where iterates are kept for the reverse pass: blocks that run on chip keep them from there, X^ turned so that it
+// is wide and B_t scaled as it is there.  A tall block whose reverse pass runs as a chain has to have X^ as it lies,
+// and goes the other way.
+void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
+    for (StackClass& c : g.classes) {
+        SmallStackClass k;
+        std::vector<double> kappas;
+        const bool both = c.s <= 8 * kSmallGradSlab;
+        if ((c.tall && !both) || !small_class(c.rows, c.cols, c.count, c.count, sch, bd, k, &kappas)) continue;
+        c.chip = true;
+        c.chip_grad = both;
+        c.gamma = kappas;
+    }
+}
 
 // Pointers of a group's planes; `sv` takes what the reverse pass reads.  Returns the workspace used.  The
 // workspace begins with the chain's tile counters.
@@ -324,13 +338,16 @@ size_t layout_forward(Group& g, int T, bool saving, Arena& ws, Arena& sv) {
         c.per = stack_per(c.rp, c.cp, c.count);
         c.chunks = stack_chunks(c.rp, c.cp, c.per);
         c.info = static_cast<float*>(take(keep, static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
-        c.partials = static_cast<double*>(take(ws, static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
-        c.done = static_cast<int*>(take(ws, static_cast<size_t>(c.count) * sizeof(int)));
+        if (!c.chip) {
+            c.partials = static_cast<double*>(take(ws, static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
+            c.done = static_cast<int*>(take(ws, static_cast<size_t>(c.count) * sizeof(int)));
+        }
         c.x_slots = saving ? T : 2;
         c.a_slots = saving ? T : 1;
         c.X = static_cast<__half*>(take(keep, c.x_slots * c.plane()));
         c.A = static_cast<__half*>(take(keep, c.a_slots * c.square()));
         c.B = static_cast<__half*>(take(keep, c.a_slots * c.square()));
+        if (c.chip) continue;
         c.L = static_cast<__half*>(take(ws, 2 * c.plane()));
         if (saving) c.last = static_cast<__half*>(take(ws, c.plane()));
         else c.last = c.X != nullptr ? c.X + (T & 1) * (c.plane() / sizeof(__half)) : nullptr;
@@ -499,6 +516,7 @@ muon_status run_iterations(Group& g, const muon_ns_schedule& sch, const std::vec
     const std::vector<int> order = class_order(g, false);
     std::vector<ChainClass> classes(g.classes.size());
     for (size_t k = 0; k < classes.size(); ++k) {
+        if (g.classes[k].chip) continue;
         if (!chain_class(classes[k], g.classes[k]))
             return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
         if (direct[k].p != nullptr)
@@ -637,6 +655,7 @@ size_t forward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& s
     for (Group& g : make_groups(shapes, sch, bd, saving ? SIZE_MAX : kGroupBytes)) {
         Arena ws, sv;
         sv.used = kept;
+        if (saving) mark_chip(g, sch, bd);
         most = std::max(most, layout_forward(g, sch.n_iters, saving, ws, sv));
         kept = align_up(sv.used, kAlign);
     }
@@ -659,7 +678,11 @@ std::vector<GradPlanes> layout_backward(const Group& g, Arena& ws) {
     auto take = [&](size_t bytes) { return ws.at(ws.take(bytes)); };
     take(kStackTickets * sizeof(int));
     for (const StackClass& c : g.classes) {
-        GradPlanes p;
+        GradPlanes p = {};
+        if (c.chip_grad) {
+            out.push_back(p);
+            continue;
+        }
         p.info = static_cast<float*>(take(static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
         p.partials = static_cast<double*>(take(static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
         p.done = static_cast<int*>(take(static_cast<size_t>(c.count) * sizeof(int)));
@@ -675,6 +698,7 @@ size_t backward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& 
     size_t most = 0;
     for (Group& g : make_groups(shapes, sch, bd, SIZE_MAX)) {
         Arena ws, fw, sv;
+        mark_chip(g, sch, bd);
         layout_forward(g, sch.n_iters, true, fw, sv);
         layout_backward(g, ws);
         most = std::max(most, align_up(ws.used, kAlign));
@@ -703,20 +727,6 @@ const uint8_t* bytes_at(const void* p, long long blocks, long long stride, int d
 }
 
 // ---------------------------------------------------------------- forward
-// Where iterates are kept for the reverse pass: blocks that run on chip keep them from there, X^ turned so that it
-// is wide and B_t scaled as it is there.  A tall block whose reverse pass runs as a chain has to have X^ as it lies,
-// and goes the other way.
-void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
-    for (StackClass& c : g.classes) {
-        SmallStackClass k;
-        std::vector<double> kappas;
-        const bool both = c.s <= 8 * kSmallGradSlab;
-        if ((c.tall && !both) || !small_class(c.rows, c.cols, c.count, c.count, sch, bd, k, &kappas)) continue;
-        c.chip = true;
-        c.chip_grad = both;
-        c.gamma = kappas;
-    }
-}
 int pairs_of(const Group& g, int cls) {
     int pairs = 0;
     for (const Part& p : g.parts)
@@ -838,9 +848,9 @@ muon_status orthogonalize(const ns_stack_desc* d, const std::vector<Shape>& shap
         ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
         sv.base = static_cast<uint8_t*>(saved);
         sv.used = kept;
+        if (saving) mark_chip(g, sch, bd);
         layout_forward(g, T, saving, ws, sv);
         kept = align_up(sv.used, kAlign);
-        if (saving) mark_chip(g, sch, bd);
         bool any_chip = false;
         for (const StackClass& c : g.classes) any_chip = any_chip || c.chip;
         if (any_chip) {
@@ -920,8 +930,8 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
         ws.base = static_cast<uint8_t*>(workspace) + kHeaderBytes;
         sv.base = static_cast<uint8_t*>(const_cast<void*>(saved));
         sv.used = kept;
-        layout_forward(g, T, true, fw, sv);   // the saved planes' places
         mark_chip(g, sch, bd);
+        layout_forward(g, T, true, fw, sv);   // the saved planes' places
         kept = align_up(sv.used, kAlign);
         std::vector<GradPlanes> gp = layout_backward(g, ws);
         const std::vector<int> order = class_order(g, true);
@@ -1008,6 +1018,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             const StackClass& c = g.classes[k];
             const GradPlanes& q = gp[k];
             ChainClass& o = classes[k];
+            if (c.chip_grad) continue;
             const long long pl = static_cast<long long>(c.rp) * c.cp, sq = static_cast<long long>(c.r8) * c.r8;
             const bool ok = chain_class(o, c) && encode_stack_tmap(&o.map[kMapD], q.D, c.rp, c.cp, 2 * c.count) &&
                             encode_stack_tmap(&o.map[kMapS], q.S, c.r8, c.r8, c.count) &&

@@ -223,3 +223,13 @@ def test_front_ends_refuse():
         ms.orthogonalize(torch.zeros(4, 4), steps=3, coeffs=[ref.KJ] * 2)
     with pytest.raises(ValueError):   # host tensors
         ms.orthogonalize(torch.zeros(4, 4))
+
+
+def test_blocks_on_chip_need_no_planes():
+    """Where the iterations and the reverse pass run on chip, the workspaces hold no planes; the kept iterates do."""
+    s, lib = mb.Schedule.fixed(5), mb.load()
+    d = _ns(count=96, rows=64, cols=2048, x_ld=2048, y_ld=2048, x_stride=64 * 2048, y_stride=64 * 2048)
+    assert lib.ns_stacks_workspace_size(d, 1, ctypes.byref(s.c), 0) < 4096
+    assert lib.ns_stacks_workspace_size(d, 1, ctypes.byref(s.c), 1) < 4096
+    assert lib.ns_stacks_backward_workspace_size(d, 1, ctypes.byref(s.c)) < 4096
+    assert lib.ns_stacks_saved_size(d, 1, ctypes.byref(s.c)) >= 5 * 2 * 96 * 64 * 2048
