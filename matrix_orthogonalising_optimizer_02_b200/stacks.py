@@ -2,6 +2,8 @@
 views that cut a fused parameter into its blocks."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import binding as mb
@@ -28,6 +30,14 @@ def _unit_last(t):
     at least a row), else a dense copy."""
     ok = (t.shape[-1] == 1 or t.stride(-1) == 1) and (t.shape[-2] == 1 or t.stride(-2) >= t.shape[-1])
     return t if ok else t.contiguous()
+
+
+@functools.lru_cache(maxsize=64)
+def _schedule(coeffs: tuple, steps: int, eps: float):
+    per_step = coeffs if isinstance(coeffs[0], tuple) else (coeffs,) * steps
+    if len(per_step) != steps:
+        raise ValueError(f"{len(per_step)} coefficient triples for {steps} steps")
+    return mb.Schedule(per_step, eps=eps)
 
 
 class _Orthogonalize(torch.autograd.Function):
@@ -62,11 +72,8 @@ def orthogonalize(x, steps: int = 5, coeffs=KJ_COEFFS, eps: float = 1e-7, dtype=
     parametrisation that needs orthonormal blocks takes converging ones, such as (1.875, -1.25, 0.375).
     The iterates run on the tensor cores in fp16 with scales of their own (see ns_orthogonalize_stacks
     in the C header for the accuracy)."""
-    coeffs = list(coeffs)
-    per_step = [tuple(coeffs)] * steps if not isinstance(coeffs[0], (tuple, list)) else coeffs
-    if len(per_step) != steps:
-        raise ValueError(f"{len(per_step)} coefficient triples for {steps} steps")
-    schedule, dtype = mb.Schedule(per_step, eps=eps), dtype if dtype is not None else x.dtype
+    coeffs = tuple(tuple(map(float, c)) if isinstance(c, (tuple, list)) else float(c) for c in coeffs)
+    schedule, dtype = _schedule(coeffs, steps, eps), dtype if dtype is not None else x.dtype
     if torch.is_grad_enabled() and x.requires_grad:
         return _Orthogonalize.apply(x, schedule, dtype)
     y = torch.empty(x.shape, dtype=dtype, device=x.device)
