@@ -113,6 +113,45 @@ __device__ __forceinline__ void put_panel16(uint8_t* panels, int row, int c, con
     }
 }
 
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------- giving up
+// What thread 0 has armed on the CTA's mbarriers (copies of its own, peers' stores): a bit per barrier that was armed at
+// least once, and the parity of the phase armed last.  After a wait of the CTA has run out (kWaitLimitNs) nothing more is
+// armed, copied in or multiplied, the cluster barriers are still met, and before the CTA leaves it waits (with a limit)
+// for what is under way: a late copy or a peer's store must not find its memory given to another CTA.
+struct Flight {
+    uint32_t used = 0, parity = ~0u;
+    __device__ __forceinline__ void arm(int bar) {
+        used |= 1u << bar;
+        parity ^= 1u << bar;
+    }
+};
+__device__ __forceinline__ bool lands(uint64_t* bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    bool landed = false;
+    while (!(landed = mbar_try_wait(bar, parity)) && global_ns() - t0 < 100000000ull) {
+    }
+    return landed;
+}
+// Thread 0 at the end of a CTA that has given up: `bars` as counted by `fly`, `drain` a barrier without a phase so far.
+// The products, and the signals that wait for them, end before `drain`'s.
+__device__ __noinline__ void drain_flight(uint64_t* bars, int n, uint64_t* drain, const Flight fly, unsigned* status) {
+    tc_commit(drain);
+    bool landed = lands(drain, 0);
+    for (int i = 0; i < n; ++i)
+        if (fly.used >> i & 1u) landed = lands(&bars[i], fly.parity >> i & 1u) && landed;
+    bulk_wait_read<0>();       // stores' reads of this CTA's memory
+    // stores of peers that came after this CTA had armed its last: no barrier counts them, a millisecond is a thousand times theirs
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
+    if (!landed) atomicOr(status, kDevErrUndrained);
+}
+
 // ---------------------------------------------------------------- a slab in and out
 struct Slab {
     int rows, cols, rank, cluster, nchunk;
@@ -120,7 +159,7 @@ struct Slab {
     uint8_t* buf;          // all of the shared memory that the iterations use, 1024-byte aligned
     int bytes;
     uint32_t t_lane;       // TMEM address of this warp's lanes
-    uint64_t* bars;        // kRing mbarriers
+    uint64_t* bars;        // kRing mbarriers, the first of those that a Flight counts
     volatile int* abort;
     unsigned* status;
     __device__ __forceinline__ int first(int ch) const { return (ch * cluster + rank) * 64; }   // first column of a chunk
@@ -142,11 +181,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z)
                  : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // Packed: rows 64 .. of X are the next block's.  One array's part of a chunk: two boxes of 64 x 128 (64-column halves of a tall block's rows) or one of 128 x 64
@@ -249,8 +283,10 @@ struct Ring {
         bufs = min(min(kRing, s.bytes / size), s.nchunk);
     }
     __device__ __forceinline__ uint8_t* buf(const Slab& s, int ch) const { return s.buf + (ch % bufs) * size; }
-    __device__ __forceinline__ void fill(const Slab& s, int ch) const {
+    __device__ __forceinline__ void fill(const Slab& s, int ch, Flight& fly) const {
+        if (*s.abort) return;
         const uint32_t bar = smem_u32(s.bars + ch % bufs);
+        fly.arm(ch % bufs);
         mbar_arrive_expect_tx(s.bars + ch % bufs, size);
         uint32_t dst = smem_u32(buf(s, ch));
 #pragma unroll
@@ -268,12 +304,12 @@ struct Ring {
     }
     // After the barrier that ends chunk ch, with its store (if any) committed: fills a buffer whose chunk is done.
     // With several buffers that is the one before, whose store has had a chunk's time.
-    __device__ __forceinline__ void refill(const Slab& s, int ch) const {
+    __device__ __forceinline__ void refill(const Slab& s, int ch, Flight& fly) const {
         const int back = bufs > 1 ? ch - 1 : ch;
         if (back < 0 || back + bufs >= s.nchunk) return;
         if (bufs > 1) bulk_wait_read<1>();
         else bulk_wait_read<0>();
-        fill(s, back + bufs);
+        fill(s, back + bufs, fly);
     }
 };
 
@@ -445,12 +481,15 @@ static_assert(sizeof(SmallParams<kFewItems>) <= 4096, "the small form's paramete
 template <int N, bool PACK>
 __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_constant__ SmallParams<N> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t bar_gram, bar_square, bar_apply[2], bar_rows, bar_a, bar_ring[kRing];
+    __shared__ uint64_t bar_fly[kRing + 2], bar_gram, bar_square, bar_apply[2], bar_drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double red_norm[THREADS / 32];
     __shared__ double parts[PACK ? 2 : 1][16];
 
+    constexpr int kRows = kRing, kA = kRing + 1;   // places in bar_fly, after the ring
+    uint64_t &bar_rows = bar_fly[kRows], &bar_a = bar_fly[kA];
+    Flight fly;
     const SmallStackClass& k = p.k;
     const int C = k.cluster, w = k.slab;
     uint8_t* panels = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -477,8 +516,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     const bool mom = it.M != nullptr;
 
     if (tid == 0) {
-        for (uint64_t* x : {&bar_gram, &bar_square, &bar_apply[0], &bar_apply[1], &bar_rows, &bar_a}) mbar_init(x, 1);
-        for (uint64_t& x : bar_ring) mbar_init(&x, 1);
+        for (uint64_t* x : {&bar_gram, &bar_square, &bar_apply[0], &bar_apply[1], &bar_drain}) mbar_init(x, 1);
+        for (uint64_t& x : bar_fly) mbar_init(&x, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -495,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     unsigned* status = k.status;
 
     const bool two = PACK && b + 1 < it.count;
-    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, panels, (w >> 6) * PANEL + FIXED_BYTES, t_lane, bar_ring, abort, status};
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, panels, (w >> 6) * PANEL + FIXED_BYTES, t_lane, bar_fly, abort, status};
     const Momentum mo = {gs, k.beta, mom, k.nesterov != 0};
     const bool tma_in = (it.vec & 1) && (!mom || (it.vec & 2)), tma_out = (it.vec & 4) != 0, update = it.decay != 0.f;
     const Boxes<PACK> boxes_w = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
@@ -510,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         ring.n = mom ? 2 : 1;
         ring.shape(slab);
         if (tid == 0) {
-            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch);
+            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch, fly);
             if (tma_out && update)      // on its way to L2 while the block iterates
                 for (int ch = 0; ch < nchunk; ++ch) boxes_w.prefetch(slab, slab.first(ch));
         }
@@ -535,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                     ring.a[1].store(slab, slab.first(ch), smem_u32(buf_m));
                     bulk_commit();
                 }
-                ring.refill(slab, ch);
+                ring.refill(slab, ch, fly);
             }
         }
         if (tid == 0) bulk_wait_read<0>();
@@ -673,8 +712,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             tc_fence_before();
             __syncthreads();
         }
-        if (tid == 0) {
+        if (tid == 0 && !*abort) {
             if (C > 1) {
+                fly.arm(kRows);
+                fly.arm(kA);
                 mbar_arrive_expect_tx(&bar_rows, RED_BYTES);
                 mbar_arrive_expect_tx(&bar_a, A_BYTES);
             }
@@ -750,7 +791,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         }
         fence_async_proxy();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !*abort) {
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
@@ -782,7 +823,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         fence_async_proxy();
         tc_fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !*abort) {
             if (keep) keep_square(&k.b, Bm, t);
             tc_fence_after();
             for (int n0 = 0; n0 < w; n0 += 256) {
@@ -808,7 +849,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                 if (tid == 0) bulk_wait_read<0>();
                 __syncthreads();
             }
-            if (!last && n0 + 256 >= w && C > 1) cluster_arrive();   // this CTA's A, B~ and partial rows are done with
+            // This CTA's A, B~ and partial rows are done with (and, after the last iteration, its stores into its peers)
+            if (n0 + 256 >= w && C > 1) cluster_arrive();
             const int nq = min(256, w - n0) >> 2;
             if (!last)
                 for (int c = n0 + cg * nq; c < n0 + (cg + 1) * nq; c += 16) {
@@ -826,7 +868,6 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     }
 
     // ---------------------------------------------------------------- result
-    // Peers' last stores into this CTA are the last rows of A, which it has waited for.
     if (!fin) {
         const float nan[16] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
         for (int c = cg * 16; c < w; c += 64) tmem_st_x16(t_lane + c, nan);
@@ -842,7 +883,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         ring.n = 1;
         ring.shape(slab);
         if (update && tid == 0)
-            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch);
+            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch, fly);
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
             uint8_t* buf = ring.buf(slab, ch);
@@ -868,7 +909,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             if (tid == 0) {
                 boxes_w.store(slab, slab.first(ch), smem_u32(buf));
                 bulk_commit();
-                if (update) ring.refill(slab, ch);
+                if (update) ring.refill(slab, ch, fly);
             }
         }
         if (tid == 0) bulk_wait_read<0>();
@@ -876,6 +917,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         if (tall) slab_out_any<true, PACK>(slab, it, b, k.out);
         else slab_out_any<false, PACK>(slab, it, b, k.out);
     }
+    if (C > 1) cluster_wait();     // no peer sends any more: one that has given up on its waits is as far as this
+    if (tid == 0 && *abort) drain_flight(bar_fly, kRing + 2, &bar_drain, fly, status);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -907,12 +950,15 @@ static_assert(sizeof(SmallGradParams<kFewItems>) <= 4096, "the small form's para
 template <int N, bool PACK>
 __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __grid_constant__ SmallGradParams<N> p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t bar_s, bar_p, bar_apply, bar_rows, bar_all, bar_ab, bar_x, bar_ring[kRing];
+    __shared__ uint64_t bar_fly[kRing + 4], bar_s, bar_p, bar_apply, bar_drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ double red_sum[THREADS / 32];
     __shared__ double parts[PACK ? 2 : 1][16];
 
+    constexpr int kRows = kRing, kAll = kRing + 1, kAB = kRing + 2, kX = kRing + 3;   // places in bar_fly, after the ring
+    uint64_t &bar_rows = bar_fly[kRows], &bar_all = bar_fly[kAll], &bar_ab = bar_fly[kAB], &bar_x = bar_fly[kX];
+    Flight fly;
     const SmallGradClass& k = p.k;
     const int C = k.cluster, w = k.slab, nchunk = w >> 6;
     uint8_t* Xp = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -938,8 +984,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const bool tall = k.rows > k.cols, two = PACK && b + 1 < it.count;
 
     if (tid == 0) {
-        for (uint64_t* x : {&bar_s, &bar_p, &bar_apply, &bar_rows, &bar_all, &bar_ab, &bar_x}) mbar_init(x, 1);
-        for (uint64_t& x : bar_ring) mbar_init(&x, 1);
+        for (uint64_t* x : {&bar_s, &bar_p, &bar_apply, &bar_drain}) mbar_init(x, 1);
+        for (uint64_t& x : bar_fly) mbar_init(&x, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -954,11 +1000,13 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     volatile int* abort = &abort_flag;
     unsigned* status = k.status;
-    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_ring, abort, status};
+    const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, Dp, nchunk * PANEL + A_BYTES + RED_BYTES, t_lane, bar_fly, abort, status};
     const bool tma_in = (it.vec & 1) != 0, tma_out = (it.vec & 4) != 0;
 
     auto load_x = [&](int t) {     // thread 0
+        if (*abort) return;
         const int ys = PACK && !two ? 64 : 128;
+        fly.arm(kX);
         mbar_arrive_expect_tx(&bar_x, static_cast<uint32_t>(nchunk * ys * 128));
         for (int j = 0; j < nchunk; ++j)
             for (int y = 0; y < ys; y += 64)
@@ -966,6 +1014,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                             t * k.saved + kept + (PACK ? y >> 6 : 0));
     };
     auto load_ab = [&](int t) {    // thread 0
+        if (*abort) return;
+        fly.arm(kAB);
         mbar_arrive_expect_tx(&bar_ab, 2 * A_BYTES);
         for (int x = 0; x < 128; x += 64)
             for (int y = 0; y < 128; y += 64) {
@@ -1018,7 +1068,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         ring.n = 1;
         ring.shape(slab);
         if (tid == 0)
-            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch);
+            for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch, fly);
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
             ring.wait(slab, ch, turns);
@@ -1027,7 +1077,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
             ss += static_cast<double>(sum_squares(u));
             tmem_st_x16(t_lane + ch * 64 + cg * 16, u);
             __syncthreads();
-            if (tid == 0) ring.refill(slab, ch);
+            if (tid == 0) ring.refill(slab, ch, fly);
         }
     } else {
         const Momentum mo = {1.f, 0.f, false, false};
@@ -1097,8 +1147,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         const SmallGradIter& f = k.it[t];
         const uint32_t phase = i & 1;
         const float f0t = t == 0 ? f0 : 1.f;       // X_0 = f0 X^_0
-        if (tid == 0) {
+        if (tid == 0 && !*abort) {
             if (C > 1) {
+                fly.arm(kRows);
+                fly.arm(kAll);
                 mbar_arrive_expect_tx(&bar_rows, RED_BYTES);
                 mbar_arrive_expect_tx(&bar_all, A_BYTES);
             } else {
@@ -1175,7 +1227,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
         fence_async_proxy();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !*abort) {
             mbar_wait(&bar_ab, phase, abort, status);
             tc_fence_after();
 #pragma unroll
@@ -1205,7 +1257,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         fence_async_proxy();
         tc_fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !*abort) {
             tc_fence_after();
             const uint32_t id = idesc_f16_f32(128, w, 0, 1);
             for (int g = 0; g < 2; ++g)
@@ -1304,6 +1356,9 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         if (tall) slab_out_any<true, PACK>(slab, it, b, 1.f);
         else slab_out_any<false, PACK>(slab, it, b, 1.f);
     }
+    // Peers' last stores into this CTA lie before the cluster barriers of the last sum, which also a CTA that has given
+    // up on its waits meets.
+    if (tid == 0 && *abort) drain_flight(bar_fly, kRing + 4, &bar_drain, fly, status);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
