@@ -5,6 +5,7 @@ from __future__ import annotations
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as mb
 
@@ -63,16 +64,18 @@ class _Orthogonalize(torch.autograd.Function):
 def orthogonalize(x, steps: int = 5, coeffs=KJ_COEFFS, eps: float = 1e-7, dtype=None):
     """Every [rows, cols] block of x ([rows, cols] or [count, rows, cols]; bf16, fp16 or fp32) after
     `steps` Newton-Schulz iterations with `coeffs` ((a, b, c), or a sequence of `steps` of them), in
-    `dtype` (x's own if None).  Differentiable with respect to x, once; without a gradient to come (no
-    grad mode, an input that needs none) no iterates are kept.  Forward and backward can be captured in
-    a CUDA graph; as for any backward pass, no graph of the same leaves made outside the capture may
-    still be alive then.
+    `dtype` (x's own if None).  Differentiable with respect to x, once and in reverse mode (an input
+    with a forward-mode tangent is refused); without a gradient to come (no grad mode, an input that
+    needs none) no iterates are kept.  Forward and backward can be captured in a CUDA graph; as for any
+    backward pass, no graph of the same leaves made outside the capture may still be alive then.
 
     With the optimizer's coefficients the singular values of the result lie near 1 (0.7 to 1.2); a
     parametrisation that needs orthonormal blocks takes converging ones, such as (1.875, -1.25, 0.375).
     The iterates run on the tensor cores in fp16 with scales of their own (see ns_orthogonalize_stacks
     in the C header for the accuracy)."""
     coeffs = tuple(tuple(map(float, c)) if isinstance(c, (tuple, list)) else float(c) for c in coeffs)
+    if forward_ad.unpack_dual(x).tangent is not None:
+        raise NotImplementedError("orthogonalize has no forward-mode derivative")
     schedule, dtype = _schedule(coeffs, steps, eps), dtype if dtype is not None else x.dtype
     if torch.is_grad_enabled() and x.requires_grad:
         return _Orthogonalize.apply(x, schedule, dtype)

@@ -1,0 +1,30 @@
+"""CPU checks of the torch front-ends of the stacked-block operators and AdamW; the library's calls are replaced by
+recorders."""
+import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
+
+from matrix_orthogonalising_optimizer_02_b200 import binding as mb
+from matrix_orthogonalising_optimizer_02_b200 import stacks as ms
+
+
+@pytest.mark.parametrize("requires_grad", [False, True])
+@pytest.mark.parametrize("grad_mode", [False, True])
+def test_orthogonalize_refuses_forward_mode(monkeypatch, requires_grad, grad_mode):
+    """A tangent would be dropped silently: the operator has a reverse derivative alone."""
+    calls = []
+
+    def record(stacks, schedule, keep=False):
+        calls.append(keep)
+        stacks[0].Y.zero_()
+        return torch.zeros(1) if keep else None
+    monkeypatch.setattr(mb, "orthogonalize_alloc", record)
+    x = torch.randn(4, 6, requires_grad=requires_grad)
+    with torch.set_grad_enabled(grad_mode), forward_ad.dual_level():
+        with pytest.raises(NotImplementedError):
+            ms.orthogonalize(forward_ad.make_dual(x, torch.ones(4, 6)))
+        assert not calls
+        y = ms.orthogonalize(x)      # beside a dual level, without a tangent
+    assert calls == [requires_grad and grad_mode] and y.shape == x.shape
+    with pytest.raises(NotImplementedError):
+        torch.func.jvp(ms.orthogonalize, (x.detach(),), (torch.ones(4, 6),))
