@@ -28,6 +28,10 @@ def _check_matrix(p):
         raise ValueError(f"unsupported parameter dtype {p.dtype}")
 
 
+def _capturing() -> bool:
+    return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+
+
 class _Workspaces:
     """One workspace per device, grown to the largest request: the library's calls are
     ordered on the current stream, so successive calls can share it."""
@@ -212,7 +216,8 @@ class StackedMuon(_Fp32State):
 
 class AdamW(_Fp32State):
     """AdamW for what Muon does not take, one grouped call per param group.  Parameters of any shape,
-    dense, bf16, fp16 or fp32; moments in fp32."""
+    dense, bf16, fp16 or fp32; moments in fp32.  The number of the step is a host integer, so step() refuses
+    to be captured in a CUDA graph (binding.adamw_step_batched takes a device step count for that)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01):
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
@@ -223,6 +228,8 @@ class AdamW(_Fp32State):
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):
+        if _capturing():
+            raise RuntimeError("AdamW.step() cannot be captured: every replay would use the captured step's number")
         loss = None
         if closure is not None:
             with torch.enable_grad():

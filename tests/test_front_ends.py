@@ -28,3 +28,22 @@ def test_orthogonalize_refuses_forward_mode(monkeypatch, requires_grad, grad_mod
     assert calls == [requires_grad and grad_mode] and y.shape == x.shape
     with pytest.raises(NotImplementedError):
         torch.func.jvp(ms.orthogonalize, (x.detach(),), (torch.ones(4, 6),))
+
+
+def test_adamw_refuses_a_capture(monkeypatch):
+    """The number of the step is a host integer: a replay would go on with the captured one's corrections."""
+    from matrix_orthogonalising_optimizer_02_b200.optim import AdamW
+    steps = []
+    monkeypatch.setattr(mb, "adamw_step_batched", lambda tensors, hp, step, grad_scale=None: steps.append(step))
+    p = torch.nn.Parameter(torch.ones(8))
+    p.grad = torch.ones(8)
+    opt = AdamW([p])
+    opt.step()
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="captured"):
+        opt.step()
+    assert steps == [1] and opt.state[p]["step"] == 1
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    opt.step()
+    assert steps == [1, 2]
