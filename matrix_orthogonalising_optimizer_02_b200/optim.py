@@ -34,16 +34,20 @@ def _capturing() -> bool:
 
 class _Workspaces:
     """One workspace per device, grown to the largest request: the library's calls are
-    ordered on the current stream, so successive calls can share it."""
+    ordered on the current stream, so successive calls can share it.  A buffer that a CUDA
+    graph was captured with is never given back: its replays go on writing there."""
 
     def __init__(self):
         self.bufs = {}
+        self.captured = []
 
     def get(self, nbytes, device):
         ws = self.bufs.get(device)
         if ws is None or ws.numel() < nbytes:
             ws = mb.workspace(nbytes, device=device)
             self.bufs[device] = ws
+        if _capturing() and not any(ws is c for c in self.captured):
+            self.captured.append(ws)
         return ws
 
 
@@ -171,9 +175,9 @@ class StackedMuon(_Fp32State):
                 self._blocks(p, g)
         self._ws = _Workspaces()
 
-    def __setstate__(self, state):     # copies and pickles carry the state alone
+    def __setstate__(self, state):     # copies and pickles carry the state alone; load_state_dict comes here too
         super().__setstate__(state)
-        self._ws = _Workspaces()
+        self.__dict__.setdefault("_ws", _Workspaces())
 
     @staticmethod
     def _blocks(t, group):

@@ -47,3 +47,60 @@ def test_adamw_refuses_a_capture(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     opt.step()
     assert steps == [1, 2]
+
+
+class _Buffer:
+    """Stands for a workspace tensor."""
+
+    def __init__(self, nbytes):
+        self.nbytes, self.streams = nbytes, []
+
+    def numel(self):
+        return self.nbytes
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+@pytest.fixture
+def fake_cuda(monkeypatch):
+    state = {"capturing": False, "stream": "one"}
+    monkeypatch.setattr(mb, "workspace", lambda nbytes, device=None: _Buffer(nbytes))
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: state["stream"])
+    return state
+
+
+def test_a_workspace_that_a_capture_has_used_stays(fake_cuda):
+    """A graph goes on writing to the workspace it was captured with: growing must not give it back."""
+    import gc
+    import weakref
+
+    from matrix_orthogonalising_optimizer_02_b200.optim import _Workspaces
+    pool = _Workspaces()
+    plain = weakref.ref(pool.get(100, "cuda:0"))
+    pool.get(200, "cuda:0")
+    gc.collect()
+    assert plain() is None                          # never captured: given back
+    fake_cuda["capturing"] = True
+    held = [weakref.ref(pool.get(150, "cuda:0"))]
+    assert held[0]().numel() == 200
+    held.append(weakref.ref(pool.get(300, "cuda:0")))   # grown inside a capture
+    fake_cuda["capturing"] = False
+    last = pool.get(400, "cuda:0")
+    gc.collect()
+    assert all(w() is not None for w in held) and last.numel() == 400
+    assert pool.get(10, "cuda:1").numel() == 10
+
+
+def test_state_dicts_leave_the_workspaces(fake_cuda):
+    """A graph that was captured before a state was loaded still has its workspace."""
+    import copy
+
+    from matrix_orthogonalising_optimizer_02_b200.optim import StackedMuon
+    opt = StackedMuon([torch.nn.Parameter(torch.zeros(4, 6))])
+    ws = opt._ws.get(100, "cuda:0")
+    opt.load_state_dict(copy.deepcopy(opt.state_dict()))
+    assert opt._ws.get(100, "cuda:0") is ws
+    assert copy.deepcopy(opt)._ws.get(100, "cuda:0") is not ws    # a copy has its own
