@@ -35,19 +35,24 @@ def _capturing() -> bool:
 class _Workspaces:
     """One workspace per device, grown to the largest request: the library's calls are
     ordered on the current stream, so successive calls can share it.  A buffer that a CUDA
-    graph was captured with is never given back: its replays go on writing there."""
+    graph was captured with is never given back: its replays go on writing there.  One that
+    another stream than its own has used is given back when that stream is done with it."""
 
     def __init__(self):
         self.bufs = {}
         self.captured = []
 
     def get(self, nbytes, device):
-        ws = self.bufs.get(device)
+        ws, own = self.bufs.get(device, (None, None))
+        stream = torch.cuda.current_stream(device)
         if ws is None or ws.numel() < nbytes:
-            ws = mb.workspace(nbytes, device=device)
-            self.bufs[device] = ws
-        if _capturing() and not any(ws is c for c in self.captured):
-            self.captured.append(ws)
+            ws, own = mb.workspace(nbytes, device=device), stream
+            self.bufs[device] = ws, own
+        if _capturing():
+            if not any(ws is c for c in self.captured):
+                self.captured.append(ws)
+        elif stream != own:
+            ws.record_stream(stream)
         return ws
 
 

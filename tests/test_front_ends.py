@@ -94,6 +94,17 @@ def test_a_workspace_that_a_capture_has_used_stays(fake_cuda):
     assert pool.get(10, "cuda:1").numel() == 10
 
 
+def test_a_workspace_used_on_another_stream_waits_for_it(fake_cuda):
+    """The allocator must not hand a dropped workspace to its own stream while another one still uses it."""
+    from matrix_orthogonalising_optimizer_02_b200.optim import _Workspaces
+    pool = _Workspaces()
+    ws = pool.get(100, "cuda:0")
+    assert pool.get(100, "cuda:0") is ws and ws.streams == []
+    fake_cuda["stream"] = "two"
+    assert pool.get(50, "cuda:0") is ws and ws.streams == ["two"]
+    assert pool.get(200, "cuda:0").streams == []
+
+
 def test_state_dicts_leave_the_workspaces(fake_cuda):
     """A graph that was captured before a state was loaded still has its workspace."""
     import copy
