@@ -156,7 +156,9 @@ class _Fp32State(torch.optim.Optimizer):
         params = [p for g in self.param_groups for p in g["params"]]
         for i, p in zip(saved, params):
             for k, v in state_dict["state"].get(i, {}).items():
-                if torch.is_tensor(v):
+                if k == "step":        # a host integer here; torch.optim.AdamW has it in a tensor
+                    self.state[p][k] = int(v)
+                elif torch.is_tensor(v):
                     self.state[p][k] = v.to(device=p.device, dtype=torch.float32, copy=True)
 
 
@@ -234,6 +236,13 @@ class AdamW(_Fp32State):
             for p in g["params"]:
                 if p.dtype not in (torch.bfloat16, torch.float16, torch.float32):
                     raise ValueError(f"unsupported parameter dtype {p.dtype}")
+
+    def load_state_dict(self, state_dict):
+        """Takes a state of torch.optim.AdamW too, where its rule is this one."""
+        for g in state_dict["param_groups"]:
+            if g.get("amsgrad") or g.get("maximize") or (g["weight_decay"] and not g.get("decoupled_weight_decay", True)):
+                raise ValueError("the state is of another rule than AdamW's (amsgrad, maximize or weight decay in the gradient)")
+        super().load_state_dict(state_dict)
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):

@@ -115,3 +115,43 @@ def test_state_dicts_leave_the_workspaces(fake_cuda):
     opt.load_state_dict(copy.deepcopy(opt.state_dict()))
     assert opt._ws.get(100, "cuda:0") is ws
     assert copy.deepcopy(opt)._ws.get(100, "cuda:0") is not ws    # a copy has its own
+
+
+def test_adamw_goes_on_from_torchs_state(monkeypatch):
+    """torch.optim.AdamW keeps the number of the step in a tensor, one per parameter."""
+    from matrix_orthogonalising_optimizer_02_b200.optim import AdamW
+    shapes = [(3, 5), (7,)]
+    theirs = [torch.nn.Parameter(torch.ones(s, dtype=torch.bfloat16)) for s in shapes]
+    ours = [torch.nn.Parameter(torch.ones(s, dtype=torch.bfloat16)) for s in shapes]
+    a, b = torch.optim.AdamW(theirs, lr=0.5, weight_decay=0.25), AdamW(ours)
+    for _ in range(2):
+        for p in theirs:
+            p.grad = torch.ones_like(p)
+        a.step()
+    b.load_state_dict(a.state_dict())
+    assert b.param_groups[0]["lr"] == 0.5 and b.param_groups[0]["weight_decay"] == 0.25
+    for p, q in zip(theirs, ours):
+        s = b.state[q]
+        assert type(s["step"]) is int and s["step"] == 2
+        assert s["exp_avg"].dtype == s["exp_avg_sq"].dtype == torch.float32
+        assert torch.equal(s["exp_avg"], a.state[p]["exp_avg"].float())
+    calls = []
+    monkeypatch.setattr(mb, "adamw_step_batched", lambda t, hp, step, grad_scale=None: calls.append((len(t), step)))
+    for q in ours:
+        q.grad = torch.ones_like(q)
+    b.step()
+    assert calls == [(2, 3)]                       # one call for both parameters
+    b.load_state_dict(b.state_dict())              # and its own
+    assert b.state[ours[0]]["step"] == 3
+
+
+@pytest.mark.parametrize("change", [dict(amsgrad=True), dict(maximize=True), dict(decoupled_weight_decay=False)], ids=str)
+def test_adamw_refuses_a_state_of_another_rule(change):
+    from matrix_orthogonalising_optimizer_02_b200.optim import AdamW
+    p = torch.nn.Parameter(torch.ones(4))
+    state = torch.optim.AdamW([p]).state_dict()
+    state["param_groups"][0].update(change)
+    opt = AdamW([p], lr=0.125)
+    with pytest.raises(ValueError):
+        opt.load_state_dict(state)
+    assert opt.param_groups[0]["lr"] == 0.125      # left as it was
