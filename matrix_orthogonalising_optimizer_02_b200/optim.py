@@ -262,10 +262,12 @@ class AdamW(_Fp32State):
                     state["step"] = 0
                     state["exp_avg"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
                     state["exp_avg_sq"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
-                state["step"] += 1
-                by_step.setdefault(state["step"], []).append(
-                    mb.AdamWTensor(p.data, p.grad.contiguous(), state["exp_avg"], state["exp_avg_sq"]))
+                states, tensors = by_step.setdefault(state["step"] + 1, ([], []))
+                states.append(state)
+                tensors.append(mb.AdamWTensor(p.data, p.grad.contiguous(), state["exp_avg"], state["exp_avg_sq"]))
             hp = mb.adamw_hyper(group["lr"], *group["betas"], group["eps"], group["weight_decay"])
-            for step, tensors in by_step.items():
+            for step, (states, tensors) in by_step.items():
                 mb.adamw_step_batched(tensors, hp, step, grad_scale=grad_scale)
+                for state in states:       # a refused call has not counted
+                    state["step"] = step
         return loss

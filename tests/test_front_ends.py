@@ -155,3 +155,20 @@ def test_adamw_refuses_a_state_of_another_rule(change):
     with pytest.raises(ValueError):
         opt.load_state_dict(state)
     assert opt.param_groups[0]["lr"] == 0.125      # left as it was
+
+
+def test_a_refused_adamw_step_does_not_count(monkeypatch):
+    from matrix_orthogonalising_optimizer_02_b200.optim import AdamW
+
+    def refuse(*args, **kw):
+        raise ValueError("refused")
+    p = torch.nn.Parameter(torch.ones(4))
+    p.grad = torch.ones(4)
+    opt = AdamW([p])
+    monkeypatch.setattr(mb, "adamw_step_batched", refuse)
+    with pytest.raises(ValueError):
+        opt.step()
+    steps = []
+    monkeypatch.setattr(mb, "adamw_step_batched", lambda t, hp, step, grad_scale=None: steps.append(step))
+    opt.step()
+    assert steps == [1]
