@@ -208,7 +208,7 @@ class StackedMuon(_Fp32State):
         for group in self.param_groups:
             stacks = []
             for p in group["params"]:
-                if p.grad is None:
+                if p.grad is None or p.numel() == 0:     # a rank without experts, say
                     continue
                 state = self.state[p]
                 if "momentum_buffer" not in state:

@@ -172,3 +172,21 @@ def test_a_refused_adamw_step_does_not_count(monkeypatch):
     monkeypatch.setattr(mb, "adamw_step_batched", lambda t, hp, step, grad_scale=None: steps.append(step))
     opt.step()
     assert steps == [1]
+
+
+def test_a_parameter_without_elements_takes_no_step(monkeypatch):
+    """A rank without experts, say: beside others, and alone."""
+    from matrix_orthogonalising_optimizer_02_b200.optim import StackedMuon
+    calls = []
+    monkeypatch.setattr(mb, "muon_stacks_workspace_size", lambda stacks, hp: 256)
+    monkeypatch.setattr(mb, "muon_step_stacks", lambda stacks, hp, ws, grad_scale=None: calls.append([s.W for s in stacks]))
+    monkeypatch.setattr(mb, "workspace", lambda nbytes, device=None: _Buffer(nbytes))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "one")
+    full, none = torch.nn.Parameter(torch.ones(2, 4, 6)), torch.nn.Parameter(torch.ones(0, 4, 6))
+    flat = torch.nn.Parameter(torch.ones(0, 6))
+    for p in (full, none, flat):
+        p.grad = torch.ones_like(p)
+    opt = StackedMuon([{"params": [full, none]}, {"params": [flat], "row_block": 4}])
+    opt.step()
+    assert len(calls) == 1 and [w.shape for w in calls[0]] == [full.shape]
+    opt.load_state_dict(opt.state_dict())
