@@ -432,6 +432,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             ti.b = __shfl_sync(0xffffffffu, ti.b, 0);
             ti.m0 = __shfl_sync(0xffffffffu, ti.m0, 0);
             ti.n0 = __shfl_sync(0xffffffffu, ti.n0, 0);
+            __syncwarp();     // what lane 0 has acquired with the tile (E, the block's info) is every lane's: a shuffle orders nothing
             const ChainOp& P = g.op[ti.op];
             const ChainClass& cl = g.cls[P.cls];
             const Shape z = shape_of(cl, P);

@@ -1,16 +1,17 @@
-"""What the on-chip kernels do when a bounded wait runs out, read from their source: such a run cannot be brought
-about without a broken kernel, and what it must not do (leave while copies or peers' stores are under way) is a fault."""
+"""What the kernels of the stacked blocks owe to the memory model and to a bounded wait that runs out, read from their
+source: such runs cannot be brought about without a broken kernel, and what they must not do (leave while copies or peers'
+stores are under way, read what only another lane has acquired) is a fault or a race."""
 import pathlib
 import re
 
 import pytest
 
-SOURCE = pathlib.Path(__file__).resolve().parents[1] / "matrix_orthogonalising_optimizer_02_b200/csrc/stack_small.cu"
+CSRC = pathlib.Path(__file__).resolve().parents[1] / "matrix_orthogonalising_optimizer_02_b200/csrc"
 
 
-def body(kernel):
+def body(kernel, file="stack_small.cu"):
     """The kernel's source, without comments."""
-    text = re.sub(r"//[^\n]*", "", SOURCE.read_text())
+    text = re.sub(r"//[^\n]*", "", (CSRC / file).read_text())
     at = text.index(f"{kernel}(const __grid_constant__")
     start = text.index("{", at)
     depth = 0
@@ -51,3 +52,11 @@ def test_a_cta_that_gives_up_waits_for_what_is_under_way(kernel):
         before = text[:m.start()]
         guard = max(before.rfind("if (tid == 0 && !*abort) {"), before.rfind("if (*abort) return;"))
         assert guard >= 0 and guard > max(before.rfind("if (tid == 0) {"), before.rfind("__syncthreads();"))
+
+
+def test_every_lane_of_the_epilogue_has_acquired_the_tile():
+    """Lane 0 waits for the tile; the others read what it depends on only behind a barrier of the warp."""
+    text = body("stack_chain_kernel", "stack_chain.cu")
+    after = text[text.index("ti.n0 = __shfl_sync("):]
+    first_read = min(after.index("cl.info["), after.index("prefetch_e(c_beg)"))
+    assert "__syncwarp();" in after[:first_read]
