@@ -219,7 +219,10 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
                     for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(x[e]), static_cast<double>(x[e]), ss);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= up;
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] *= up;
+                        if (PASS == StackPass::kPackGrad) x[e] *= it.step;     // apart: their product may leave fp32's range
+                    }
                     at[u].put_plane(it.hi, x);
                     at[u].put_plane(it.lo, x);
                 }
@@ -248,7 +251,7 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
                         ss = fma(static_cast<double>(x[e]) + static_cast<double>(y[e]), static_cast<double>(z[e]), ss);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = fmaf(od, x[e] + y[e], ox * z[e]);
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(od, (x[e] + y[e]) * up, ox * z[e]);
                     at[u].put(it.W, it.w_dtype, wb, it.w_ld, x);
                 }
             }
@@ -272,8 +275,8 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
     float* info = it.info != nullptr ? it.info + static_cast<size_t>(b) * kStackInfo : nullptr;
     double* partials = it.partials != nullptr ? it.partials + static_cast<size_t>(b) * it.chunks : nullptr;
 
-    float up = 1.f;                            // kPack, kPackGrad: factor of the plane
-    float od = 0.f, ox = 0.f;                  // kGradOut: out = od * D + ox * X
+    float up = 1.f;                            // kPack, kPackGrad: factor of the plane; kGradOut: 1 / step
+    float od = 0.f, ox = 0.f;                  // kGradOut: out = od * up * D + ox * X
     if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad || PASS == StackPass::kGradOut) {
         double s = 0.0;
         for (int i = threadIdx.x; i < it.chunks; i += kStackThreads) s += partials[i];
@@ -283,8 +286,9 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
             // dU = [D_0 - X_0 <D_0, X_0> (N + eps) / N] / (N + eps), D_0 = (hi + lo) / (2^k step)
             const float* gi = it.ginfo + static_cast<size_t>(b) * kStackInfo;
             const double n = info[3], f0 = info[0];
-            const double sd = 1.0 / (static_cast<double>(gi[1]) * it.step);
-            const double corr = n > 0.0 ? s * sd * f0 * (n + eps) / n : (isnan(f0) ? f0 : 0.0);
+            up = 1.f / it.step;                  // a power of two; with 2^-k it would leave fp32's normal range for tiny gradients
+            const double sd = 1.0 / gi[1];
+            const double corr = n > 0.0 ? s * up * sd * f0 * (n + eps) / n : (isnan(f0) ? f0 : 0.0);
             od = static_cast<float>(sd / (n + eps));
             ox = static_cast<float>(-corr * f0 / (n + eps));
         } else {
@@ -304,7 +308,6 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
             }
             if (c == 0 && threadIdx.x == 1) it.done[b] = 0;
             if (blockIdx.x == 0 && threadIdx.x < kStackTickets) p.a.tickets[threadIdx.x] = 0;
-            if (PASS == StackPass::kPackGrad) up *= it.step;
         }
     }
 
