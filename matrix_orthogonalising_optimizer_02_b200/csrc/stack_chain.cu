@@ -441,6 +441,19 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 const float x = cl.info[static_cast<size_t>(ti.b) * kStackInfo];
                 f = P.pow == 1 ? x : x * x;
             }
+            // The scale of the planes that are written, from the norm of those that were read: `room` is that of the
+            // planes over the most that the operation can grow them, so nothing leaves fp16's range, and they lie at most
+            // one operation's slack below it.
+            const bool rescale = (P.flags & kStackRescale) != 0;
+            GradScale* scale = rescale ? cl.scale + static_cast<size_t>(ti.b) * cl.scales + P.t : nullptr;
+            if (rescale) {
+                const unsigned long long sum = __ldcg(&scale[1].sum);
+                const float n = sqrtf(__ull2float_rn(sum)) * 3.0517578125e-05f;      // 2^-15
+                const int e = sum != 0 ? max(-60, min(60, ilogbf(P.room / n))) : 0;
+                f *= __int_as_float((e + 127) << 23);
+                if (ti.m0 + ti.n0 == 0 && rank == 0 && warp == 4 && lane == 0) scale->e = __ldcg(&scale[1].e) + e;
+            }
+            float squares = 0.f;
             const float alpha = P.alpha * f, beta = P.beta * f;
             const int chunks = z.width(ti.n0) / 64;
             const int c_beg = ((warp - 4) >> 2) * chunks, c_end = c_beg + chunks;   // this warp's chunks of 32 columns
@@ -517,6 +530,10 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                         }
                     }
                 }
+                if (rescale) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) squares = fmaf(v[j], v[j], squares);   // zeros outside the block
+                }
                 __syncwarp();               // E's staging is free, and the output's of the chunk before
                 if (c + 1 < c_end) prefetch_e(c + 1);
                 if (!below) {
@@ -564,6 +581,12 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
             cp_async_wait_all();
             tc_fence_before();
             mbar_arrive_cluster(tempty_leader + acc * 8u);
+            if (rescale) {
+                // whole numbers add up to the same sum in any order; rounded up, so that the norm is never too small
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+                if (lane == 0) atomicAdd(&scale->sum, __float2ull_ru(squares * 1073741824.f));
+            }
             // the block's next operation may read what this warp stored, by TMA among other ways
             fence_proxy_global();
             __syncwarp();                       // the release below covers every lane's stores

@@ -275,7 +275,7 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
     float* info = it.info != nullptr ? it.info + static_cast<size_t>(b) * kStackInfo : nullptr;
     double* partials = it.partials != nullptr ? it.partials + static_cast<size_t>(b) * it.chunks : nullptr;
 
-    float up = 1.f;                            // kPack, kPackGrad: factor of the plane; kGradOut: 1 / step
+    float up = 1.f;                            // kPack, kPackGrad: factor of the plane; kGradOut: 2^-e
     float od = 0.f, ox = 0.f;                  // kGradOut: out = od * up * D + ox * X
     if (PASS == StackPass::kPack || PASS == StackPass::kPackGrad || PASS == StackPass::kGradOut) {
         double s = 0.0;
@@ -283,11 +283,12 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
         s = block_sum256(s);
         const double eps = static_cast<double>(p.a.eps);
         if (PASS == StackPass::kGradOut) {
-            // dU = [D_0 - X_0 <D_0, X_0> (N + eps) / N] / (N + eps), D_0 = (hi + lo) / (2^k step)
+            // dU = [D_0 - X_0 <D_0, X_0> (N + eps) / N] / (N + eps), D_0 = (hi + lo) / 2^(k + e)
             const float* gi = it.ginfo + static_cast<size_t>(b) * kStackInfo;
             const double n = info[3], f0 = info[0];
-            up = 1.f / it.step;                  // a power of two; with 2^-k it would leave fp32's normal range for tiny gradients
-            const double sd = 1.0 / gi[1];
+            const int e = it.scale[static_cast<size_t>(b) * (p.a.iters + 1)].e, near = max(-100, min(100, e));
+            up = pow2f(-near);                   // apart: with 2^-k it would leave fp32's normal range for tiny gradients
+            const double sd = ldexp(1.0 / gi[1], near - e);
             const double corr = n > 0.0 ? s * up * sd * f0 * (n + eps) / n : (isnan(f0) ? f0 : 0.0);
             od = static_cast<float>(sd / (n + eps));
             ox = static_cast<float>(-corr * f0 / (n + eps));
@@ -307,6 +308,13 @@ stack_pass_kernel(const __grid_constant__ PassParams<N> p) {
                 if (!fin && p.a.status != nullptr) atomicOr(p.a.status, kDevErrNonfinite);
             }
             if (c == 0 && threadIdx.x == 1) it.done[b] = 0;
+            if (PASS == StackPass::kPackGrad && c == 0 && static_cast<int>(threadIdx.x) <= p.a.iters) {
+                // the planes' norm is step at most
+                const bool last = static_cast<int>(threadIdx.x) == p.a.iters;
+                it.scale[static_cast<size_t>(b) * (p.a.iters + 1) + threadIdx.x] = {
+                    last ? static_cast<unsigned long long>(static_cast<double>(it.step) * it.step * 1073741824.0) : 0ull,
+                    last ? ilogbf(it.step) : 0, 0};
+            }
             if (blockIdx.x == 0 && threadIdx.x < kStackTickets) p.a.tickets[threadIdx.x] = 0;
         }
     }

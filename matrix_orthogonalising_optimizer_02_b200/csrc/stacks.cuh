@@ -26,9 +26,17 @@ constexpr uint32_t kStackBMn = 2u;       // B is contiguous along N (else along 
 constexpr uint32_t kStackSym = 4u;       // symmetric output: upper tiles computed, stored mirrored
 constexpr uint32_t kStackOutBf16 = 8u;   // plane 0 of the output is bf16
 constexpr uint32_t kStackRowMajor = 16u; // tiles swept along the rows of a block first
+constexpr uint32_t kStackRescale = 32u;  // alpha and beta are multiplied by a power of two of the block's own (GradScale)
 
 enum StackPlane { kPlaneX, kPlaneL, kPlaneA, kPlaneB, kPlaneOut, kPlaneD, kPlaneDL, kPlaneS, kPlaneP, kPlanes, kPlaneNone = 255 };
 enum StackMap { kMapX, kMapA, kMapB, kMapD, kMapS, kMapP, kMaps };
+
+// How the planes of a block's gradient D_t are scaled in the reverse pass: they hold D_t * 2^(k + e), and `sum` is the sum
+// of the squares of what they hold, in units of 2^-30.  One per iterate, t = 0 .. iterations.
+struct GradScale {
+    unsigned long long sum;
+    int e, unused;
+};
 
 struct ChainPlane {
     __half* p;
@@ -43,9 +51,12 @@ struct alignas(64) ChainClass {
     int rp, cp, r8;        // padded sides of a block, padded shorter side
     int rows;              // rows that kPlaneOut takes
     int count;
+    int scales;            // GradScales of a block
+    GradScale* scale;      // kStackRescale: of the first block
 };
 struct ChainOp {
     float alpha, beta, diag;
+    float room;            // kStackRescale: what the norm of the planes read may be multiplied up to
     int tile0;             // first tile of the operation in the launch (filled by the launcher)
     int need;              // value of `done` at which a block's operation may start (filled by the caller)
     uint8_t cls, kind;     // kind 0: r8 x r8 over the long side, 1: r8 x r8 over r8, 2: rp x cp over r8
@@ -55,6 +66,7 @@ struct ChainOp {
     uint8_t sa[2], sb[2];  // and their slots
     uint8_t e[2], es[2];   // planes and slots of E
     uint8_t o[2], os[2];   // and of the output
+    uint8_t t;             // kStackRescale: the iterate that is written; t + 1 is read
 };
 constexpr int kChainWarps = 16;          // epilogue warps of a tile: what a finished tile adds to `done`
 constexpr int kChainMaxClasses = 12, kChainMaxOps = 360;
@@ -97,8 +109,9 @@ struct alignas(16) StackItem {
     int chunk0;           // first chunk of this item in the launch
     int g_dtype, w_dtype;
     int vec;              // bit 0: G, bit 1: M, bit 2: W allow 8-element vector accesses
-    float decay, step;    // W <- decay * W + step * X (step kernels); X * step (output)
+    float decay, step;    // W <- decay * W + step * X (step kernels); X * step (output, kPackGrad: a power of two)
     int* done;            // kPack, kPackGrad: per block, set to zero
+    GradScale* scale;     // kPackGrad: per block, set to the planes' scale (last) and to zero; kGradOut: the first is D_0's
 };
 constexpr int kStackMaxItems = 128;
 constexpr int kStackThreads = 256;
@@ -121,7 +134,7 @@ constexpr int kStackTickets = 64;
 enum class StackPass {
     kNorm,      // partials <- sum of U^2 (M updated in place where there is one)
     kPack,      // info <- norms; hi, lo <- U * 2^k
-    kPackGrad,  // info2 <- norms; hi, lo <- G * 2^k * step (G: gradient of the output)
+    kPackGrad,  // info2, scale <- norms; hi, lo <- G * 2^k * step (G: gradient of the output)
     kOut,       // W <- hi * step
     kUpdate,    // W <- decay * W + step * hi
     kDot,       // partials <- sum of (hi + lo) * hi2
@@ -133,6 +146,7 @@ struct StackPassArgs {
     float eps;
     const float* gscale;    // device: factor of G (nullable: 1)
     int* tickets;           // kPack, kPackGrad: kStackTickets ints set to zero
+    int iters;              // kPackGrad, kGradOut
     unsigned* status;       // kNorm: cleared (unless null); kPack, kPackGrad: told of a norm that is not finite
 };
 cudaError_t stack_pass_launch(StackPass pass, StackItem* items, int n, const StackPassArgs& args, cudaStream_t stream);

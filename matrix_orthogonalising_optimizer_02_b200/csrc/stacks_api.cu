@@ -10,9 +10,14 @@
 // planes hold  X_t * tau_t,  A_t * alpha_t,  B_t * gamma_t  with powers of two such that no element
 // can leave fp16's range (an element is at most the spectral norm) and ordinary ones keep all 11
 // bits: tau ~ sqrt(s) (rows of X_t have norm about 1), alpha ~ r / prod a^2 (A's mean diagonal for a
-// flat spectrum).  In the reverse pass the gradient's bound grows by max |p'| per iteration (the
-// operator norm of the derivative of a matrix function of an odd polynomial p), and delta_t keeps
-// D_t and everything formed from it within range under that bound.
+// flat spectrum).  In the reverse pass an iteration can make the gradient max |p'| times as long (the
+// operator norm of the derivative of a matrix function of an odd polynomial p).  The product of these maxima
+// is a bound that no gradient keeps up with: they lie at different singular values, so it grows by 1.9 (a
+// converging schedule) or 5 (the optimizer's) an iteration while the gradient stays about as it is, and planes
+// scaled by it run dry: 0.3 off 64 bits after 32 converging iterations, all zero after 16 of the optimizer's.
+// So a chain's D_t is scaled from the measured norm of D_{t+1} and one iteration's bound (GradScale), block by block.
+// On chip D is held in fp32, and delta_t scales only the rounded copy that is multiplied; there the bound
+// decides whether the block goes that way (kMostGrowth).
 //
 // Shift.  For a converging schedule the Gram matrix is stored as A - l I with l = sigma_t^2, sigma_t the
 // iterates of a flat spectrum (l -> 1): bA + cA^2 = (b + 2cl)(A - lI) + c(A - lI)^2 + (bl + cl^2) I, and the
@@ -37,6 +42,10 @@ constexpr long long kMaxBlocks = 1 << 20;
 constexpr double kTop = 16384.0;               // no plane's element exceeds this (fp16: 65504)
 constexpr double kMaxSigma = 64.0;
 constexpr int kMaxTensors = 65536;
+// Product of the bounds of |p'| up to which the reverse pass runs on chip.  At 2^18.8 (8 of the optimizer's iterations)
+// the scales still cost nothing (128 x 2048 and 96 x 200: the same errors as with measured ones), at 2^19.6 the errors
+// of a converging schedule have doubled.
+constexpr double kMostGrowth = 524288.0;
 // Newton-Schulz planes of one group of blocks; more run group after group in the same space.
 constexpr size_t kGroupBytes = static_cast<size_t>(5) << 30;
 
@@ -52,6 +61,7 @@ struct Bounds {
     std::vector<double> growth;   // max |p_t'| on [0, S_t]
     std::vector<double> bmax;     // max |b l + c l^2| on [0, S_t^2]
     bool converging = true;       // p_t(1) = 1 and |p_t'(1)| <= 1/2 throughout
+    double spread = 1.0;          // product of `growth`
 };
 
 // Largest |f| on [0, top] of a function whose interior extrema are among `at`.
@@ -93,6 +103,7 @@ muon_status check_schedule(const muon_ns_schedule* s, Bounds& out) {
         auto q = [=](double l) { return l * (b + c * l); };
         if (std::fabs(p(1.0) - 1.0) > 1e-3 || std::fabs(dp(1.0)) > 0.5) out.converging = false;
         out.growth.push_back(std::max(0.25, 1.02 * largest(dp, top, inflect, 1)));
+        out.spread *= out.growth.back();
         out.bmax.push_back(std::max(1e-3, largest(q, lam, vertex, 1)));
         const double next = 1.02 * largest(p, top, at, 2) + 0.01;   // room for rounding
         if (!(next <= kMaxSigma)) return MUON_ERR_INVALID_ARG;
@@ -314,13 +325,14 @@ std::vector<Group> make_groups(const std::vector<Shape>& shapes, const muon_ns_s
     return groups;
 }
 // Where iterates are kept for the reverse pass: blocks that run on chip keep them from there, X^ turned so that it
-// is wide and B_t scaled as it is there.  A tall block whose reverse pass runs as a chain has to have X^ as it lies,
+// is wide and B_t scaled as it is there, and their reverse pass runs there too where its slabs hold the block and the
+// schedule's bound lets a fixed scale do.  A tall block whose reverse pass runs as a chain has to have X^ as it lies,
 // and goes the other way.
 void mark_chip(Group& g, const muon_ns_schedule& sch, const Bounds& bd) {
     for (StackClass& c : g.classes) {
         SmallStackClass k;
         std::vector<double> kappas;
-        const bool both = c.s <= 8 * kSmallGradSlab;
+        const bool both = c.s <= 8 * kSmallGradSlab && bd.spread <= kMostGrowth;
         if ((c.tall && !both) || !small_class(c.rows, c.cols, c.count, c.count, sch, bd, k, &kappas)) continue;
         c.chip = true;
         c.chip_grad = both;
@@ -672,8 +684,9 @@ struct GradPlanes {
     float* info;
     double* partials;
     int* done;
+    GradScale* scale;
 };
-std::vector<GradPlanes> layout_backward(const Group& g, Arena& ws) {
+std::vector<GradPlanes> layout_backward(const Group& g, int T, Arena& ws) {
     std::vector<GradPlanes> out;
     auto take = [&](size_t bytes) { return ws.at(ws.take(bytes)); };
     take(kStackTickets * sizeof(int));
@@ -686,6 +699,7 @@ std::vector<GradPlanes> layout_backward(const Group& g, Arena& ws) {
         p.info = static_cast<float*>(take(static_cast<size_t>(c.count) * kStackInfo * sizeof(float)));
         p.partials = static_cast<double*>(take(static_cast<size_t>(c.count) * c.chunks * sizeof(double)));
         p.done = static_cast<int*>(take(static_cast<size_t>(c.count) * sizeof(int)));
+        p.scale = static_cast<GradScale*>(take(static_cast<size_t>(c.count) * (T + 1) * sizeof(GradScale)));
         p.D = static_cast<__half*>(take(2 * c.plane()));
         p.DL = static_cast<__half*>(take(2 * c.plane()));
         p.S = static_cast<__half*>(take(c.square()));
@@ -700,7 +714,7 @@ size_t backward_bytes(const std::vector<Shape>& shapes, const muon_ns_schedule& 
         Arena ws, fw, sv;
         mark_chip(g, sch, bd);
         layout_forward(g, sch.n_iters, true, fw, sv);
-        layout_backward(g, ws);
+        layout_backward(g, sch.n_iters, ws);
         most = std::max(most, align_up(ws.used, kAlign));
     }
     return kHeaderBytes + most;
@@ -933,12 +947,13 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
         mark_chip(g, sch, bd);
         layout_forward(g, T, true, fw, sv);   // the saved planes' places
         kept = align_up(sv.used, kAlign);
-        std::vector<GradPlanes> gp = layout_backward(g, ws);
+        std::vector<GradPlanes> gp = layout_backward(g, T, ws);
         const std::vector<int> order = class_order(g, true);
         const size_t nc = g.classes.size();
 
-        // delta[k][t]: D_t's planes hold D_t * 2^k * delta_t
-        std::vector<std::vector<double>> delta(nc, std::vector<double>(T + 1));
+        // room[k][t]: how far D_t may reach so that nothing formed from it leaves fp16's range; delta[k][t]: a factor
+        // that keeps it there whatever the iterations before have done
+        std::vector<std::vector<double>> delta(nc, std::vector<double>(T + 1)), room = delta;
         for (size_t k = 0; k < nc; ++k) {
             const StackClass& c = g.classes[k];
             double nu = 1.0;   // bound of |D_t| relative to the incoming gradient
@@ -952,7 +967,8 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                                       (std::fabs(c.b[u]) + 2.0 * std::fabs(sch.coeffs[3 * u + 2]) * lam);
                     most = std::max({1.0, bd.sigma[u], pf});
                 }
-                delta[k][t] = pow2_floor(kTop / (nu * most));
+                room[k][t] = kTop / most;
+                delta[k][t] = pow2_floor(room[k][t] / nu);
                 if (t > 0) nu *= bd.growth[t - 1];
             }
         }
@@ -987,9 +1003,11 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             it.hi = q.D + (T & 1) * slot + plane_at(c, p);
             it.lo = q.DL + (T & 1) * slot + plane_at(c, p);
             it.done = q.done + p.at;
+            it.scale = q.scale + static_cast<size_t>(p.at) * (T + 1);
             it.step = static_cast<float>(delta[p.cls][T]);
             in.push_back(it);
             read += static_cast<double>(p.count) * c.rows * c.cols * elem_size(s.x_dtype);
+            o.scale = it.scale;
             o.ginfo = it.info;
             o.hi = q.D + plane_at(c, p);
             o.lo = q.DL + plane_at(c, p);
@@ -999,7 +1017,6 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
             o.w_ld = s.y_ld;
             o.w_dtype = s.y_dtype;
             o.vec = vec_ok(o.W, s.y_dtype, s.y_ld, s.y_stride) ? 4 : 0;
-            o.step = static_cast<float>(delta[p.cls][0]);
             out.push_back(o);
         }
         if (in.empty()) continue;
@@ -1007,6 +1024,7 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
         args.eps = sch.eps;
         args.status = first ? call.status : nullptr;
         args.tickets = tickets_at(workspace);
+        args.iters = T;
         muon_status st = launch_pass(StackPass::kNorm, in, args, MUON_KERNEL_SCALE, read, call);
         if (st != MUON_OK) return st;
         args.status = call.status;
@@ -1025,6 +1043,8 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                             encode_stack_tmap(&o.map[kMapP], q.P, c.r8, c.r8, c.count);
             if (!ok) return cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled of a stack plane");
             o.done = q.done;
+            o.scale = q.scale;
+            o.scales = T + 1;
             o.plane[kPlaneD] = {q.D, pl, c.cp};
             o.plane[kPlaneDL] = {q.DL, pl, c.cp};
             o.plane[kPlaneS] = {q.S, sq, c.r8};
@@ -1062,9 +1082,11 @@ muon_status backward(const ns_stack_desc* d, const std::vector<Shape>& shapes, c
                         op_e(o, 1, kPlaneDL, (t + 1) & 1);
                         op_out(o, 0, kPlaneD, t & 1);
                         op_out(o, 1, kPlaneDL, t & 1);
-                        const double kappa = delta[k][t] / delta[k][t + 1];
-                        o.alpha = static_cast<float>(kappa / c.gamma[t]);
-                        o.beta = static_cast<float>(kappa * a);
+                        o.flags |= kStackRescale;
+                        o.t = static_cast<uint8_t>(t);
+                        o.room = static_cast<float>(room[k][t] / bd.growth[t]);
+                        o.alpha = static_cast<float>(1.0 / c.gamma[t]);
+                        o.beta = static_cast<float>(a);
                         flops += 4.0 * c.count * c.r * c.r * c.s;
                     }
                     if (t == 0 && stage < 2) o.pow = 1;

@@ -1,4 +1,5 @@
-"""The gradient of stacked-block orthogonalisation where its range runs out first.  References in 64 bits."""
+"""The gradient of stacked-block orthogonalisation where its range runs out first: gradients that have nearly died out,
+and schedules of many iterations.  References in 64 bits."""
 import pytest
 import torch
 
@@ -46,3 +47,56 @@ def test_gradients_that_have_nearly_died_out(shape, dtype, size):
     want = ref.ns_grad(x[1], dy[1], coeffs)
     step = 2.0 ** (-150 if dtype == FP else -134) * (shape[1] * shape[2]) ** 0.5
     assert float((dx[1].double() - want).norm()) <= ref.tol_stable(dtype) * float(want.norm()) + step
+
+
+def hybrid(n, last=2):
+    return [ref.KJ] * n + [ref.STABLE] * last
+
+
+# The optimizer's polynomial maps [0.68, 1.2] into itself; its |p'| is 1.55 there in the mean square: each iteration
+# beyond the five of 2 tol_kj multiplies what earlier ones have rounded by 1.7 at most on average.  A converging
+# iteration behind them has 0.23 there, and multiplies by 0.25.
+def tol_long(n, last, dtype):
+    return 2 * ref.tol_kj(dtype) * max(1.0, 1.7 ** (n - 5) * 0.25 ** last)
+
+
+@pytest.mark.parametrize("shape", [(2, 160, 256), (1, 300, 200), (3, 96, 200), (2, 512, 768), (2, 64, 2100), (3, 200, 24)], ids=str)
+@pytest.mark.parametrize("coeffs,tol", [
+    ([ref.STABLE] * 10, ref.tol_stable(FP)), ([ref.STABLE] * 16, ref.tol_stable(FP)), ([ref.STABLE] * 32, ref.tol_stable(FP)),
+    ([(2.0, -1.5, 0.5)] * 32, ref.tol_stable(FP)), (hybrid(8), tol_long(8, 2, FP)), (hybrid(12), tol_long(12, 2, FP)),
+    ([ref.KJ] * 8, tol_long(8, 0, FP)), ([ref.KJ] * 10, tol_long(10, 0, FP))],
+    ids=["stable10", "stable16", "stable32", "other32", "hybrid8", "hybrid12", "kj8", "kj10"])
+def test_gradient_through_many_iterations(shape, coeffs, tol):
+    """The derivative's bound grows by the largest |p'| every iteration, the gradient itself does not: what the planes
+    hold has to follow the gradient.  Both directions are compared."""
+    x, dy = blocks(3, *shape, std=0.5), blocks(4, *shape, std=1e-2)
+    y, dx, status = gradient(x, dy, mb.Schedule(coeffs))
+    assert status == mb.MUON_OK
+    for b in range(shape[0]):
+        assert ref.rel(y[b], ref.ns(x[b], coeffs)) <= tol, b
+        assert ref.rel(dx[b], ref.ns_grad(x[b], dy[b], coeffs)) <= tol, b
+
+
+@pytest.mark.parametrize("shape", [(4, 160, 256), (4, 96, 200)], ids=str)
+def test_blocks_of_one_long_call_are_scaled_apart(shape):
+    """Gradients of 1e-20 and 1e12, one along the smallest direction (which grows by a factor a every iteration), a zero
+    one and one that is not finite, side by side."""
+    coeffs = [ref.STABLE] * 24
+    x, dy = blocks(5, *shape, std=0.5), blocks(6, *shape, std=1.0)
+    u, s, v = torch.linalg.svd(x[1].double(), full_matrices=False)
+    s = torch.logspace(0, -6, s.numel(), device="cuda", dtype=torch.float64)
+    x[1] = ((u * s) @ v).float()
+    dy[1] = torch.outer(u[:, -1], v[-1]).float()
+    dy[0] *= 1e-20
+    dy[2] *= 1e12
+    dy[3, 1, 1] = float("inf")
+    _, dx, status = gradient(x, dy, mb.Schedule(coeffs))
+    assert status == mb.MUON_ERR_NONFINITE
+    assert bool(torch.isnan(dx[3]).any())
+    for b in (0, 2):
+        assert ref.rel(dx[b], ref.ns_grad(x[b], dy[b], coeffs)) <= ref.tol_stable(FP), b
+    assert bool(torch.isfinite(dx[1]).all())
+    dy[0] = 0
+    _, dx, _ = gradient(x, dy, mb.Schedule(coeffs))
+    assert bool((dx[0] == 0).all())
+    assert ref.rel(dx[2], ref.ns_grad(x[2], dy[2], coeffs)) <= ref.tol_stable(FP)
