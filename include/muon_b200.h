@@ -227,7 +227,11 @@ MUON_API muon_status ns_orthogonalize_stacks(const ns_stack_desc* descs, int n, 
  * descs[i].Y receives the gradient with respect to its input (both with strides and dtypes of their
  * own); count, rows, cols, their order and the schedule are those of the call that filled `saved`,
  * which is read and left as it is.  Differentiates the division by (norm + eps) too; for a block of
- * zeros the norm's derivative is taken as zero.  Workspace: ns_stacks_backward_workspace_size. */
+ * zeros the norm's derivative is taken as zero.  Relative to 64 bits it is about 2e-4 off for a
+ * converging schedule of any length, 4e-3 for 5 of the optimizer's iterations, 1e-2 for 8 and 4e-2 for
+ * 12: these multiply every rounding.  A schedule through which less than that would survive is
+ * INVALID_ARG wherever a gradient is concerned (`saved`, and the calls below); it is estimated from
+ * the coefficients alone.  Workspace: ns_stacks_backward_workspace_size. */
 MUON_API size_t ns_stacks_backward_workspace_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch);
 MUON_API muon_status ns_orthogonalize_stacks_backward(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch,
                                                       const void* saved, size_t saved_bytes, void* workspace,

@@ -72,7 +72,8 @@ def orthogonalize(x, steps: int = 5, coeffs=KJ_COEFFS, eps: float = 1e-7, dtype=
     With the optimizer's coefficients the singular values of the result lie near 1 (0.7 to 1.2); a
     parametrisation that needs orthonormal blocks takes converging ones, such as (1.875, -1.25, 0.375).
     The iterates run on the tensor cores in fp16 with scales of their own (see ns_orthogonalize_stacks
-    in the C header for the accuracy)."""
+    in the C header for the accuracy).  Long runs of the optimizer's iterations (more than 13, unless two
+    or three converging ones follow) leave nothing of a gradient and are refused where one is to come."""
     coeffs = tuple(tuple(map(float, c)) if isinstance(c, (tuple, list)) else float(c) for c in coeffs)
     if forward_ad.unpack_dual(x).tangent is not None:
         raise NotImplementedError("orthogonalize has no forward-mode derivative")

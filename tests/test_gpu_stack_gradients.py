@@ -5,6 +5,7 @@ import torch
 
 import stack_reference as ref
 from matrix_orthogonalising_optimizer_02_b200 import binding as mb
+from matrix_orthogonalising_optimizer_02_b200 import stacks as ms
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +101,13 @@ def test_blocks_of_one_long_call_are_scaled_apart(shape):
     _, dx, _ = gradient(x, dy, mb.Schedule(coeffs))
     assert bool((dx[0] == 0).all())
     assert ref.rel(dx[2], ref.ns_grad(x[2], dy[2], coeffs)) <= ref.tol_stable(FP)
+
+
+def test_a_schedule_without_a_gradient_is_refused_where_one_is_to_come():
+    x = blocks(7, 2, 160, 200, std=0.5)
+    with torch.no_grad():
+        assert bool(torch.isfinite(ms.orthogonalize(x, steps=16)).all())
+    with pytest.raises(mb.MuonError):
+        ms.orthogonalize(x.requires_grad_(True), steps=16)
+    (dx,) = torch.autograd.grad(ms.orthogonalize(x, steps=12), x, x.detach())
+    assert bool(torch.isfinite(dx).all())

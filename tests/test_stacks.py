@@ -233,3 +233,23 @@ def test_blocks_on_chip_need_no_planes():
     assert lib.ns_stacks_workspace_size(d, 1, ctypes.byref(s.c), 1) < 4096
     assert lib.ns_stacks_backward_workspace_size(d, 1, ctypes.byref(s.c)) < 4096
     assert lib.ns_stacks_saved_size(d, 1, ctypes.byref(s.c)) >= 5 * 2 * 96 * 64 * 2048
+
+
+@pytest.mark.parametrize("coeffs,taken", [
+    ([ref.KJ] * 5, True), ([ref.KJ] * 12, True), ([ref.KJ] * 8 + [ref.STABLE] * 2, True), ([ref.KJ] * 16 + [ref.STABLE] * 2, True),
+    ([ref.STABLE] * 32, True), ([(2.0, -1.5, 0.5)] * 32, True), ([(1.5, -0.5, 0.0)] * 32, True),
+    ([ref.KJ] * 16, False), ([ref.KJ] * 32, False), ([ref.KJ] * 30 + [ref.STABLE], False)],
+    ids=["kj5", "kj12", "hybrid", "hybrid16", "stable32", "other32", "quadratic32", "kj16", "kj32", "kj30 stable1"])
+def test_schedules_through_which_no_gradient_survives(coeffs, taken):
+    """Roundings that grow from iteration to iteration leave no correct digit in a gradient: such a schedule is refused
+    where one is to come (a forward call without one takes it)."""
+    lib, s = mb.load(), mb.Schedule(coeffs)
+    d = _ns()
+    sch = ctypes.byref(s.c)
+    assert lib.ns_stacks_workspace_size(d, 1, sch, 0) > 0
+    for size in (lib.ns_stacks_workspace_size(d, 1, sch, 1), lib.ns_stacks_saved_size(d, 1, sch),
+                 lib.ns_stacks_backward_workspace_size(d, 1, sch)):
+        assert (size > 0) == taken
+    if not taken:
+        assert _orth(d, sch=s, saved=WS, saved_bytes=1 << 30) == INVALID
+        assert lib.ns_orthogonalize_stacks_backward(d, 1, sch, WS, 1 << 30, WS, 1 << 30, None) == INVALID
