@@ -428,7 +428,7 @@ __device__ __noinline__ void slab_out_any(const Slab s, const SmallStackItem& it
     const int w_ld = item.w_ld;
     const long long w16 = 16ll * w_ld;
     const float decay = item.decay, step = item.step * out;
-    const bool update = decay != 0.f;
+    const bool update = item.M != nullptr;     // a step, also with a decay of zero: what is not finite in W stays so
     by_type(w_dtype, [&](auto t) {
         using E = decltype(t);
         E x[16];
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
     const bool two = PACK && b + 1 < it.count;
     const Slab slab = {k.rows, k.cols, rank, C, nchunk, tall, two, panels, (w >> 6) * PANEL + FIXED_BYTES, t_lane, bar_fly, abort, status};
     const Momentum mo = {gs, k.beta, mom, k.nesterov != 0};
-    const bool tma_in = (it.vec & 1) && (!mom || (it.vec & 2)), tma_out = (it.vec & 4) != 0, update = it.decay != 0.f;
+    const bool tma_in = (it.vec & 1) && (!mom || (it.vec & 2)), tma_out = (it.vec & 4) != 0, update = mom;   // a step
     const Boxes<PACK> boxes_w = {&it.map_w, it.w_dtype, it.w_dtype == MUON_F32 ? 4 : 2, static_cast<int>(b)};
     uint32_t turns = 0;
 

@@ -160,7 +160,7 @@ struct alignas(64) SmallStackItem {
     CUtensorMap map_g, map_m, map_w;   // where `vec` says that TMA moves the array
     const void* G;
     float* M;             // nullable: orthogonalisation alone
-    void* W;              // W <- decay * W + step * X; decay = 0: output only
+    void* W;              // W <- decay * W + step * X; without M: W <- step * X
     long long g_stride, m_stride, w_stride;
     int g_ld, m_ld, w_ld;
     int count, block0;
@@ -189,7 +189,7 @@ struct alignas(64) SmallStackClass {
     unsigned* status;
 };
 // The reverse pass of blocks whose iterates were kept, on chip as well: G is the gradient of the output, W
-// receives that of the input (decay = 0, step = 1).
+// receives that of the input (no M, step = 1).
 constexpr int kSmallGradSlab = 256;      // columns of a CTA's slab at most
 struct SmallGradIter {
     float d;              // D^ = fp16(d * V), V = 2^k dL/dX_{t+1}

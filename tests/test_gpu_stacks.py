@@ -822,3 +822,18 @@ def test_gradient_of_short_blocks_beside_bad_ones(n, rows, cols):
             assert bool((dx[b] == 0).all())
         else:
             assert ref.rel(dx[b], want) <= ref.tol_stable(FP), b
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(64, 200, 0), (64, 201, 0), (200, 64, 3), (257, 130, 0)])
+def test_a_decay_to_zero_keeps_what_is_not_finite(rows, cols, pad):
+    """lr * weight decay = 1 takes every weight to zero before the step, and a NaN or an infinity to NaN, on every path."""
+    st, _ = muon_stack(300, 2, rows, cols, pad)
+    st.W[1, 3, 5], st.W[1, 6, 7] = float("nan"), float("inf")
+    m0 = st.M.clone()
+    hp = mb.hyper(1.0, 0.95, 1.0, True, "naive")
+    mb.muon_step_stacks([st], hp, mb.workspace(mb.muon_stacks_workspace_size([st], hp)))
+    assert bool(torch.isnan(st.W[1, 3, 5])) and bool(torch.isnan(st.W[1, 6, 7]))
+    assert int(torch.isnan(st.W.float()).sum()) == 2
+    f = lambda x: float(torch.tensor(x, dtype=FP))  # noqa: E731
+    want = ref.muon(torch.zeros_like(st.W[0]), st.G[0], m0[0], 1.0, f(0.95), 1.0, True, "naive", [ref.KJ] * T)[0]
+    assert ref.rel(st.W[0], want) <= ref.tol_kj(BF)
