@@ -121,14 +121,19 @@ __device__ __forceinline__ void bulk_wait_read() {
 
 // ---------------------------------------------------------------- giving up
 // What thread 0 has armed on the CTA's mbarriers (copies of its own, peers' stores): a bit per barrier that was armed at
-// least once, and the parity of the phase armed last.  After a wait of the CTA has run out (kWaitLimitNs) nothing more is
-// armed, copied in or multiplied, the cluster barriers are still met, and before the CTA leaves it waits (with a limit)
-// for what is under way: a late copy or a peer's store must not find its memory given to another CTA.
+// least once, and the parity of the phase armed last.  It waits for every phase before it arms the next.  After a wait has
+// run out (kWaitLimitNs) nothing more is armed, copied in or multiplied, the cluster barriers are still met, and before
+// the CTA leaves it waits (with a limit) for what is under way: a late copy or a peer's store must not find its memory
+// given to another CTA.
 struct Flight {
     uint32_t used = 0, parity = ~0u;
+    bool ok = true;                // none of this thread's waits has run out
     __device__ __forceinline__ void arm(int bar) {
         used |= 1u << bar;
         parity ^= 1u << bar;
+    }
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, volatile int* abort, unsigned* status) {
+        ok = mbar_wait(bar, phase, abort, status) && ok;
     }
 };
 __device__ __forceinline__ bool lands(uint64_t* bar, uint32_t parity) {
@@ -284,7 +289,7 @@ struct Ring {
     }
     __device__ __forceinline__ uint8_t* buf(const Slab& s, int ch) const { return s.buf + (ch % bufs) * size; }
     __device__ __forceinline__ void fill(const Slab& s, int ch, Flight& fly) const {
-        if (*s.abort) return;
+        if (!fly.ok) return;
         const uint32_t bar = smem_u32(s.bars + ch % bufs);
         fly.arm(ch % bufs);
         mbar_arrive_expect_tx(s.bars + ch % bufs, size);
@@ -296,9 +301,9 @@ struct Ring {
             dst += a[i].bytes();
         }
     }
-    __device__ __forceinline__ void wait(const Slab& s, int ch, uint32_t& turns) const {
+    __device__ __forceinline__ void wait(const Slab& s, int ch, uint32_t& turns, Flight& fly) const {
         const int b = ch % bufs;
-        mbar_wait(s.bars + b, (turns >> b) & 1u, s.abort, s.status);
+        fly.wait(s.bars + b, (turns >> b) & 1u, s.abort, s.status);
         turns ^= 1u << b;
         __syncwarp();
     }
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         }
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
-            ring.wait(slab, ch, turns);
+            ring.wait(slab, ch, turns, fly);
             uint8_t* buf = ring.buf(slab, ch);
             uint8_t* buf_m = buf + ring.a[0].bytes();
             float u[16], m[16];
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             tc_fence_before();
             __syncthreads();
         }
-        if (tid == 0 && !*abort) {
+        if (tid == 0 && fly.ok) {
             if (C > 1) {
                 fly.arm(kRows);
                 fly.arm(kA);
@@ -729,7 +734,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                 }
             tc_commit(&bar_gram);
         }
-        mbar_wait(&bar_gram, phase, abort, status);
+        fly.wait(&bar_gram, phase, abort, status);
         __syncwarp();
         tc_fence_after();
         uint32_t r[32];
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                 const int seg = 8 * cg + s;
                 st_async_v4(dst + ((seg * rc + (orow ^ (seg & rmask))) << 4), bar, r[4 * s], r[4 * s + 1], r[4 * s + 2], r[4 * s + 3]);
             }
-            mbar_wait(&bar_rows, phase, abort, status);
+            fly.wait(&bar_rows, phase, abort, status);
             __syncwarp();
             // rows rank * rc ... of A: the sum over the cluster in rank order, 8 columns a thread, to every CTA
             for (int g = tid; g < rc * 16; g += THREADS) {
@@ -775,7 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
                     st_async_v4(mapa_shared(a0 + off, to), mapa_shared(smem_u32(&bar_a), to), x.x, x.y, x.z, x.w);
                 }
             }
-            mbar_wait(&bar_a, phase, abort, status);
+            fly.wait(&bar_a, phase, abort, status);
             __syncwarp();
         } else {
 #pragma unroll
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         }
         fence_async_proxy();
         __syncthreads();
-        if (tid == 0 && !*abort) {
+        if (tid == 0 && fly.ok) {
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
@@ -801,7 +806,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             tc_commit(&bar_square);
             if (keep) keep_square(&k.a, Am, t);
         }
-        mbar_wait(&bar_square, phase, abort, status);
+        fly.wait(&bar_square, phase, abort, status);
         __syncwarp();
         tc_fence_after();
         tmem_ld_32x32b_x32(t_lane + ACC + 32 * cg, r);
@@ -823,7 +828,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         fence_async_proxy();
         tc_fence_before();
         __syncthreads();
-        if (tid == 0 && !*abort) {
+        if (tid == 0 && fly.ok) {
             if (keep) keep_square(&k.b, Bm, t);
             tc_fence_after();
             for (int n0 = 0; n0 < w; n0 += 256) {
@@ -842,7 +847,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
         const bool last = t + 1 == k.iters;
         const float zs = k.it[last ? t : t + 1].zs;
         for (int n0 = 0; n0 < w; n0 += 256) {
-            mbar_wait(&bar_apply[n0 >> 8], phase, abort, status);
+            fly.wait(&bar_apply[n0 >> 8], phase, abort, status);
             __syncwarp();
             tc_fence_after();
             if (keep && n0 == 0) {     // nothing is overwritten before it has been kept
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_kernel(const __grid_co
             tmem_ld_x16(t_lane + ch * 64 + cg * 16, z);
             if (update) {
                 float x[16];
-                ring.wait(slab, ch, turns);
+                ring.wait(slab, ch, turns, fly);
                 boxes_w.get(slab, buf, row, cg, x);
 #pragma unroll
                 for (int h = 0; h < 16; ++h) z[h] = fmaf(step, z[h], decay * x[h]);
@@ -1004,7 +1009,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
     const bool tma_in = (it.vec & 1) != 0, tma_out = (it.vec & 4) != 0;
 
     auto load_x = [&](int t) {     // thread 0
-        if (*abort) return;
+        if (!fly.ok) return;
         const int ys = PACK && !two ? 64 : 128;
         fly.arm(kX);
         mbar_arrive_expect_tx(&bar_x, static_cast<uint32_t>(nchunk * ys * 128));
@@ -1014,7 +1019,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                             t * k.saved + kept + (PACK ? y >> 6 : 0));
     };
     auto load_ab = [&](int t) {    // thread 0
-        if (*abort) return;
+        if (!fly.ok) return;
         fly.arm(kAB);
         mbar_arrive_expect_tx(&bar_ab, 2 * A_BYTES);
         for (int x = 0; x < 128; x += 64)
@@ -1071,7 +1076,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
             for (int ch = 0; ch < ring.bufs; ++ch) ring.fill(slab, ch, fly);
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
-            ring.wait(slab, ch, turns);
+            ring.wait(slab, ch, turns, fly);
             float u[16];
             ring.a[0].get(slab, ring.buf(slab, ch), row, cg, u);
             ss += static_cast<double>(sum_squares(u));
@@ -1147,7 +1152,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         const SmallGradIter& f = k.it[t];
         const uint32_t phase = i & 1;
         const float f0t = t == 0 ? f0 : 1.f;       // X_0 = f0 X^_0
-        if (tid == 0 && !*abort) {
+        if (tid == 0 && fly.ok) {
             if (C > 1) {
                 fly.arm(kRows);
                 fly.arm(kAll);
@@ -1156,7 +1161,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
             } else {
                 load_ab(t);
             }
-            mbar_wait(&bar_x, phase, abort, status);
+            fly.wait(&bar_x, phase, abort, status);
             tc_fence_after();
             fence_async_proxy();
             for (int j = 0; j < nchunk; ++j)
@@ -1169,7 +1174,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                 }
             tc_commit(&bar_s);
         }
-        mbar_wait(&bar_s, phase, abort, status);
+        fly.wait(&bar_s, phase, abort, status);
         __syncwarp();
         tc_fence_after();
         uint32_t r[32];
@@ -1186,7 +1191,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                 const int seg = 8 * cg + s;
                 st_async_v4(dst + ((seg * rc + (orow ^ (seg & rmask))) << 4), bar, r[4 * s], r[4 * s + 1], r[4 * s + 2], r[4 * s + 3]);
             }
-            mbar_wait(&bar_rows, phase, abort, status);
+            fly.wait(&bar_rows, phase, abort, status);
             __syncwarp();
             for (int g = tid; g < rc * 16; g += THREADS) {
                 const int rr = g >> 4, pc = g & 15, ar = rank * rc + rr;
@@ -1214,7 +1219,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                 fence_async_proxy();
                 load_ab(t);
             }
-            mbar_wait(&bar_all, phase, abort, status);
+            fly.wait(&bar_all, phase, abort, status);
             __syncwarp();
         } else {
 #pragma unroll
@@ -1227,8 +1232,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         }
         fence_async_proxy();
         __syncthreads();
-        if (tid == 0 && !*abort) {
-            mbar_wait(&bar_ab, phase, abort, status);
+        if (tid == 0 && fly.ok) {
+            fly.wait(&bar_ab, phase, abort, status);
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
@@ -1239,7 +1244,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
             }
             tc_commit(&bar_p);
         }
-        mbar_wait(&bar_p, phase, abort, status);
+        fly.wait(&bar_p, phase, abort, status);
         __syncwarp();
         tc_fence_after();
         tmem_ld_32x32b_x32(t_lane + ACC_G + 128 + 32 * cg, r);
@@ -1257,7 +1262,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         fence_async_proxy();
         tc_fence_before();
         __syncthreads();
-        if (tid == 0 && !*abort) {
+        if (tid == 0 && fly.ok) {
             tc_fence_after();
             const uint32_t id = idesc_f16_f32(128, w, 0, 1);
             for (int g = 0; g < 2; ++g)
@@ -1269,7 +1274,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
                 }
             tc_commit(&bar_apply);
         }
-        mbar_wait(&bar_apply, phase, abort, status);
+        fly.wait(&bar_apply, phase, abort, status);
         __syncwarp();
         tc_fence_after();
         const bool last = t == 0;
@@ -1295,7 +1300,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
 
     // ---------------------------------------------------------------- gradient of the input
     // dU = [D - X_0 <D, X_0> (N + eps) / N] / (N + eps), D = V / 2^k, X_0 = f0 X^_0 (whose panels are still here)
-    mbar_wait(&bar_x, (k.iters - 1) & 1, abort, status);
+    fly.wait(&bar_x, (k.iters - 1) & 1, abort, status);
     __syncwarp();
     auto x_at = [&](int c, float (&x)[16]) {
         const uint8_t* src = Xp + (c >> 6) * PANEL + row * 128;

@@ -48,9 +48,10 @@ def test_a_cta_that_gives_up_waits_for_what_is_under_way(kernel):
     end = text[:text.rindex("tmem_dealloc(")]
     assert "if (tid == 0 && *abort) drain_flight(" in end[end.rindex("slab_out_any"):]
     assert text.count("fly.arm(") == text.count("mbar_arrive_expect_tx(")
+    assert "mbar_wait(" not in text            # through fly.wait() alone
     for m in re.finditer(r"tc_mma_bf16\(|mbar_arrive_expect_tx\(", text):
         before = text[:m.start()]
-        guard = max(before.rfind("if (tid == 0 && !*abort) {"), before.rfind("if (*abort) return;"))
+        guard = max(before.rfind("if (tid == 0 && fly.ok) {"), before.rfind("if (!fly.ok) return;"))
         assert guard >= 0 and guard > max(before.rfind("if (tid == 0) {"), before.rfind("__syncthreads();"))
 
 
