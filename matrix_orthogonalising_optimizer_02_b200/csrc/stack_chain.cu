@@ -224,7 +224,9 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-template <int NC, int NO>
+// RESCALE: operations with kStackRescale are among the launch's (the reverse pass); the others' tiles took 0.1 us longer
+// with the code for them.
+template <int NC, int NO, bool RESCALE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -441,20 +443,15 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 const float x = cl.info[static_cast<size_t>(ti.b) * kStackInfo];
                 f = P.pow == 1 ? x : x * x;
             }
-            // The scale of the planes that are written, from the norm of those that were read: `room` is that of the
-            // planes over the most that the operation can grow them, so nothing leaves fp16's range, and they lie at most
-            // one operation's slack below it.
-            const bool rescale = (P.flags & kStackRescale) != 0;
+            const bool rescale = RESCALE && (P.flags & kStackRescale) != 0;
             GradScale* scale = rescale ? cl.scale + static_cast<size_t>(ti.b) * cl.scales + P.t : nullptr;
+            unsigned long long read_sum = 0;     // of the planes that are read: on its way while the products run
+            int read_e = 0;
             if (rescale) {
-                const unsigned long long sum = __ldcg(&scale[1].sum);
-                const float n = sqrtf(__ull2float_rn(sum)) * 3.0517578125e-05f;      // 2^-15
-                const int e = sum != 0 ? max(-60, min(60, ilogbf(P.room / n))) : 0;
-                f *= __int_as_float((e + 127) << 23);
-                if (ti.m0 + ti.n0 == 0 && rank == 0 && warp == 4 && lane == 0) scale->e = __ldcg(&scale[1].e) + e;
+                read_sum = __ldcg(&scale[1].sum);
+                read_e = __ldcg(&scale[1].e);
             }
-            float squares = 0.f;
-            const float alpha = P.alpha * f, beta = P.beta * f;
+            float alpha = P.alpha * f, beta = P.beta * f, squares = 0.f;
             const int chunks = z.width(ti.n0) / 64;
             const int c_beg = ((warp - 4) >> 2) * chunks, c_end = c_beg + chunks;   // this warp's chunks of 32 columns
             const bool sym = (P.flags & kStackSym) != 0;
@@ -490,6 +487,16 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
                 cp_async_commit();
             };
             prefetch_e(c_beg);
+            if (rescale) {
+                // The scale of the planes that are written, from the norm of those that were read: `room` is that of the
+                // planes over the most that the operation can grow them, so nothing leaves fp16's range, and they lie at
+                // most one operation's slack below it.
+                const float n = sqrtf(__ull2float_rn(read_sum)) * 3.0517578125e-05f;      // 2^-15
+                const int e = read_sum != 0 ? max(-60, min(60, ilogbf(P.room / n))) : 0;
+                alpha *= __int_as_float((e + 127) << 23);
+                beta *= __int_as_float((e + 127) << 23);
+                if (ti.m0 + ti.n0 == 0 && rank == 0 && warp == 4 && lane == 0) scale->e = read_e + e;
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], acc_phase, abort_flag, dev_status))) {
                 cp_async_wait_all();
                 break;
@@ -601,7 +608,7 @@ stack_chain_kernel(const __grid_constant__ ChainParams<NC, NO> g) {
 }
 
 // The launch of one instantiation; its attributes and occupancy are looked up once per device.
-template <int NC, int NO>
+template <int NC, int NO, bool RESCALE>
 cudaError_t launch(const ChainClass* classes, int nc, const ChainOp* ops, int n, int tiles, int* ticket, unsigned* d_status,
                    int num_sms, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
@@ -615,7 +622,7 @@ cudaError_t launch(const ChainClass* classes, int nc, const ChainOp* ops, int n,
     cfg.dynamicSmemBytes = SMEM_TOTAL;
     int max_pairs = max_pairs_of[dev].load();
     if (max_pairs == 0) {
-        e = cudaFuncSetAttribute(stack_chain_kernel<NC, NO>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+        e = cudaFuncSetAttribute(stack_chain_kernel<NC, NO, RESCALE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
         cudaLaunchAttribute attr;
@@ -625,7 +632,7 @@ cudaError_t launch(const ChainClass* classes, int nc, const ChainOp* ops, int n,
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&max_pairs, stack_chain_kernel<NC, NO>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&max_pairs, stack_chain_kernel<NC, NO, RESCALE>, &cfg);
         if (e != cudaSuccess || max_pairs <= 0) {
             cudaGetLastError();
             max_pairs = num_sms / 2;
@@ -643,7 +650,7 @@ cudaError_t launch(const ChainClass* classes, int nc, const ChainOp* ops, int n,
     cfg.stream = stream;
     cfg.attrs = nullptr;
     cfg.numAttrs = 0;
-    e = cudaLaunchKernelEx(&cfg, stack_chain_kernel<NC, NO>, g);
+    e = cudaLaunchKernelEx(&cfg, stack_chain_kernel<NC, NO, RESCALE>, g);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -663,10 +670,12 @@ cudaError_t stack_chain_launch(const ChainClass* classes, int nc, ChainOp* ops, 
     // Parameters of up to 4 KB launch in 4 us, larger ones in 30 to 40 (10 KB): short chains take the small form.
     static_assert(sizeof(ChainParams<2, 30>) <= 4000, "the small form's parameters stay below 4 KB");
     static_assert(sizeof(ChainParams<kChainMaxClasses, kChainMaxOps>) <= 32700, "the limit of a launch's parameters");
-    if (nc <= 2 && n <= 30)
-        return launch<2, 30>(classes, nc, ops, n, static_cast<int>(tiles), ticket, d_status, num_sms, stream);
-    return launch<kChainMaxClasses, kChainMaxOps>(classes, nc, ops, n, static_cast<int>(tiles), ticket, d_status, num_sms,
-                                                  stream);
+    bool rescale = false;
+    for (int i = 0; i < n; ++i) rescale = rescale || (ops[i].flags & kStackRescale) != 0;
+    const bool few = nc <= 2 && n <= 30;
+    const auto run = few ? (rescale ? launch<2, 30, true> : launch<2, 30, false>)
+                         : (rescale ? launch<kChainMaxClasses, kChainMaxOps, true> : launch<kChainMaxClasses, kChainMaxOps, false>);
+    return run(classes, nc, ops, n, static_cast<int>(tiles), ticket, d_status, num_sms, stream);
 }
 
 }  // namespace muon
