@@ -55,12 +55,20 @@ Plan::~Plan() {
 
 namespace {
 thread_local char g_last_error[256] = "";
+thread_local cudaError_t g_pending = cudaSuccess;
 }
 
 muon_status cuda_error(cudaError_t e, const char* where) {
-    std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
+    if (g_pending != cudaSuccess)
+        std::snprintf(g_last_error, sizeof(g_last_error), "%s (an earlier %s was pending on entry): %s (%s)", where,
+                      cudaGetErrorName(g_pending), cudaGetErrorName(e), cudaGetErrorString(e));
+    else
+        std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
     return MUON_ERR_CUDA;
 }
+
+PendingError::PendingError() { g_pending = cudaGetLastError(); }
+PendingError::~PendingError() { g_pending = cudaSuccess; }
 
 muon_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MUON_OK : cuda_error(e, "CUDA call"); }
 

@@ -140,6 +140,12 @@ muon_status from_cuda(cudaError_t e);
 // Records `where` and the CUDA error as the calling thread's last library error (read with
 // muon_last_error) and returns MUON_ERR_CUDA.
 muon_status cuda_error(cudaError_t e, const char* where);
+// Around a call that does not go through run_plan: an error left pending by earlier, unrelated work would be reported by
+// the call's first launch check as its own.  It is cleared, and cuda_error() names it if this call then fails.
+struct PendingError {
+    PendingError();
+    ~PendingError();
+};
 
 template <class F>
 muon_status no_throw(F&& f) noexcept {

@@ -490,6 +490,7 @@ void apply_seg(ChainOp& o, const StackClass& c, int ms, int ss, MapSlot x) {
 }
 
 struct Call {
+    PendingError pending;
     unsigned* status = nullptr;
     cudaStream_t stream = nullptr;
     int sms = 148;
@@ -1237,7 +1238,6 @@ muon_status make_call(Call& call, void* workspace, void* stream) {
     call.status = static_cast<unsigned*>(workspace);
     call.stream = static_cast<cudaStream_t>(stream);
     call.sms = device_sm_count();
-    cudaGetLastError();   // an earlier, unrelated error is not this call's
     return MUON_OK;
 }
 
@@ -1517,8 +1517,8 @@ muon_status adamw_step_batched(const adamw_tensor_desc* descs, int n, const adam
         double bytes = 0.0;
         for (const AdamItem& it : items)
             bytes += static_cast<double>(it.n) * (elem_size(it.g_dtype) + 2.0 * elem_size(it.w_dtype) + 16.0);
+        const PendingError pending;
         const int sms = device_sm_count();
-        cudaGetLastError();
         const cudaError_t e = launch_timed(MUON_KERNEL_ADAMW, bytes, static_cast<cudaStream_t>(stream), [&](cudaStream_t s) {
             return adamw_launch(items.data(), static_cast<int>(items.size()), p, sms, s);
         });

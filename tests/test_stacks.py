@@ -253,3 +253,18 @@ def test_schedules_through_which_no_gradient_survives(coeffs, taken):
     if not taken:
         assert _orth(d, sch=s, saved=WS, saved_bytes=1 << 30) == INVALID
         assert lib.ns_orthogonalize_stacks_backward(d, 1, sch, WS, 1 << 30, WS, 1 << 30, None) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls have to fail: without a device they do before any launch")
+def test_a_failing_call_names_an_error_that_was_pending():
+    """An error of earlier work does not become the call's own, and does not vanish either."""
+    lib, hp = mb.load(), mb.adamw_hyper()
+    hp.step = 1
+    cudart = ctypes.CDLL("libcudart.so.12")
+    calls = [lambda: _orth(_ns(rows=300, cols=400, x_ld=400, y_ld=400, x_stride=1 << 18, y_stride=1 << 18)),
+             lambda: lib.adamw_step_batched(_adam(), 1, ctypes.byref(hp), None, None),
+             lambda: lib.grad_norm_batched(_adam(), 1, ctypes.c_float(1.0), WS, WS, 1 << 30, None)]
+    for call in calls:
+        assert cudart.cudaSetDevice(99) != 0               # an unrelated call fails
+        assert call() == mb.MUON_ERR_CUDA
+        assert b"was pending on entry" in lib.muon_last_error()
