@@ -166,7 +166,8 @@ class StackedMuon(_Fp32State):
     """The Muon step on blocks of parameters: a 3-D parameter [count, rows, cols] is a stack of blocks
     (experts); a 2-D one is a block, or, with the group option ``row_block`` or ``col_block``, a stack
     of blocks of that many rows or columns (heads of a fused QKV weight, the halves of a fused gate/up
-    weight).  Any sizes; bf16, fp16 or fp32 parameters.  One grouped call per param group."""
+    weight).  Any sizes; bf16, fp16 or fp32 parameters.  One grouped call per param group.  step() can be
+    captured in a CUDA graph once every parameter with a gradient has taken a step."""
 
     def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.01, nesterov=True, ns_steps=5,
                  scale_mode="moonlight", coeffs=None, eps=1e-7, row_block=None, col_block=None):
@@ -212,6 +213,9 @@ class StackedMuon(_Fp32State):
                     continue
                 state = self.state[p]
                 if "momentum_buffer" not in state:
+                    if _capturing():
+                        raise RuntimeError("a parameter's first step cannot be captured: every replay would begin with "
+                                           "its momentum at zero")
                     state["momentum_buffer"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
                 stacks.append(mb.MuonStack(*(self._blocks(t, group) for t in
                                              (p.data, p.grad.contiguous(), state["momentum_buffer"]))))

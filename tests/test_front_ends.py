@@ -190,3 +190,26 @@ def test_a_parameter_without_elements_takes_no_step(monkeypatch):
     opt.step()
     assert len(calls) == 1 and [w.shape for w in calls[0]] == [full.shape]
     opt.load_state_dict(opt.state_dict())
+
+
+def test_a_first_step_refuses_a_capture(fake_cuda, monkeypatch):
+    """The momentum would be made inside the graph, and every replay would begin by setting it to zero."""
+    from matrix_orthogonalising_optimizer_02_b200.optim import StackedMuon
+    calls = []
+    monkeypatch.setattr(mb, "muon_stacks_workspace_size", lambda stacks, hp: 256)
+    monkeypatch.setattr(mb, "muon_step_stacks", lambda stacks, hp, ws, grad_scale=None: calls.append(len(stacks)))
+    a, b = torch.nn.Parameter(torch.ones(4, 6)), torch.nn.Parameter(torch.ones(6, 4))
+    opt = StackedMuon([a, b])
+    a.grad = torch.ones_like(a)
+    fake_cuda["capturing"] = True
+    with pytest.raises(RuntimeError, match="captured"):
+        opt.step()
+    assert not calls and not opt.state[a]
+    fake_cuda["capturing"] = False
+    opt.step()
+    fake_cuda["capturing"] = True
+    opt.step()
+    b.grad = torch.ones_like(b)            # its first
+    with pytest.raises(RuntimeError, match="captured"):
+        opt.step()
+    assert calls == [1, 1]
