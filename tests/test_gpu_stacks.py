@@ -837,3 +837,32 @@ def test_a_decay_to_zero_keeps_what_is_not_finite(rows, cols, pad):
     f = lambda x: float(torch.tensor(x, dtype=FP))  # noqa: E731
     want = ref.muon(torch.zeros_like(st.W[0]), st.G[0], m0[0], 1.0, f(0.95), 1.0, True, "naive", [ref.KJ] * T)[0]
     assert ref.rel(st.W[0], want) <= ref.tol_kj(BF)
+
+
+def test_a_captured_step_outlives_its_workspaces_growth():
+    """A parameter meets its first gradient after the capture, and the workspace grows: the graph goes on writing to its own,
+    and to nothing that was allocated since."""
+    a, b = blocks(310, 2, 160, 200, FP, std=0.1), blocks(311, 3, 300, 400, FP, std=0.1)
+    p, q = torch.nn.Parameter(a.clone()), torch.nn.Parameter(b.clone())
+    twin = torch.nn.Parameter(a.clone())
+    opt, other = StackedMuon([p, q], lr=0.02), StackedMuon([twin], lr=0.02)
+    p.grad = blocks(312, 2, 160, 200, FP)
+    twin.grad = p.grad.clone()
+    opt.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    size = opt._ws.get(1, p.device).numel()
+    q.grad = blocks(313, 3, 300, 400, FP)
+    opt.step()
+    assert opt._ws.get(1, p.device).numel() > size
+    junk = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for seed in (314, 315):
+        p.grad.copy_(blocks(seed, 2, 160, 200, FP))
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(bool((j == 7).all()) for j in junk)
+    for g in (312, 312, 314, 315):          # eager, eager beside q, replay, replay
+        twin.grad.copy_(blocks(g, 2, 160, 200, FP))
+        other.step()
+    assert torch.equal(p, twin)
