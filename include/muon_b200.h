@@ -188,12 +188,15 @@ MUON_API muon_status stiefel_cayley_step(float* W, const float* G, int batch, in
  * experts of a mixture, the halves of a fused gate/up weight.  Element (b, i, j) of an array is at
  * p + b * stride + i * ld + j (in elements), so blocks may be strided views.  Any size from 1 x 1
  * to 32768 x 32768, any alignment that is a multiple of the element's size; bf16, fp16 or fp32.
- * Input blocks may overlap (a stride of 0 repeats one); blocks that are written may not.
+ * Input blocks may overlap (a stride of 0 repeats one); blocks that are written may not, nor may
+ * they overlap another stack's input.
  *
  * Arithmetic: the iterates are held as fp16 planes with power-of-two scales derived from the
  * schedule, products accumulate in fp32 on the tensor cores, and the term a * X takes X with a
- * second fp16 plane (22 bits), so that small singular directions keep their accuracy: about 1e-3
- * relative to 64 bits for the fixed 5-step schedule, 2e-4 for a converging one.  The scales are
+ * second fp16 plane (22 bits), so that small singular directions keep their accuracy: 1e-3 to 2e-3
+ * relative to 64 bits for the fixed 5-step schedule, 2e-4 for a converging one.  A schedule long
+ * enough to raise singular values of 1e-3 of the largest to 1 raises the roundings of the others
+ * beside them: up to 2e-2 after 16 converging iterations of such a block.  The scales are
  * safe for schedules whose polynomial keeps [0, 1] within [-64, 64]; others are INVALID_ARG, and so
  * are n_iters = 0, fp32_mode and n_split_iters (ns_orthogonalize has them).  A block with a
  * non-finite norm comes out as NaN and sets the workspace's device status to NONFINITE; the other
@@ -228,8 +231,9 @@ MUON_API muon_status ns_orthogonalize_stacks(const ns_stack_desc* descs, int n, 
  * own); count, rows, cols, their order and the schedule are those of the call that filled `saved`,
  * which is read and left as it is.  Differentiates the division by (norm + eps) too; for a block of
  * zeros the norm's derivative is taken as zero.  Relative to 64 bits it is about 2e-4 off for a
- * converging schedule of any length, 4e-3 for 5 of the optimizer's iterations, 1e-2 for 8 and 4e-2 for
- * 12: these multiply every rounding.  A schedule through which less than that would survive is
+ * converging schedule of any length (up to 6e-2 where that has to raise tiny singular values, as
+ * above), 3e-3 for 5 of the optimizer's iterations, 1e-2 for 8 and 3e-2 for 12: these multiply every
+ * rounding.  A schedule through which less than that would survive is
  * INVALID_ARG wherever a gradient is concerned (`saved`, and the calls below); it is estimated from
  * the coefficients alone.  Workspace: ns_stacks_backward_workspace_size. */
 MUON_API size_t ns_stacks_backward_workspace_size(const ns_stack_desc* descs, int n, const muon_ns_schedule* sch);

@@ -250,6 +250,8 @@ __device__ __forceinline__ double walk(const StackItem& it, const StackPassArgs&
                     for (int e = 0; e < 8; ++e)
                         ss = fma(static_cast<double>(x[e]) + static_cast<double>(y[e]), static_cast<double>(z[e]), ss);
                 } else {
+                    // X_0 as its first plane: the radial term is at most as long as the whole, so 2^-11 of it is
+                    // less than the products have left
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = fmaf(od, (x[e] + y[e]) * up, ox * z[e]);
                     at[u].put(it.W, it.w_dtype, wb, it.w_ld, x);

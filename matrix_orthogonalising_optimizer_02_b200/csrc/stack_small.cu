@@ -1319,7 +1319,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_small_grad_kernel(const __gr
         x_at(c, x);
         float s = 0.f;
 #pragma unroll
-        for (int h = 0; h < 16; ++h) s = fmaf(z[h], x[h], s);
+        for (int h = 0; h < 16; ++h) s = fmaf(z[h], x[h], s);     // 16 products in fp32, their sums in fp64
         dot += static_cast<double>(s);
     }
     dot = cluster_sum(dot);

@@ -116,6 +116,7 @@ struct alignas(16) StackItem {
 constexpr int kStackMaxItems = 128;
 constexpr int kStackThreads = 256;
 constexpr int kStackGroup = 8 * kStackThreads;
+// (148 SMs, as the architecture has: a size query, which may run without a device, and the call must come to the same.)
 // Groups of a CTA: one where that spreads few elements over more SMs (a pass over 2 x 320 x 257 took 13 us with
 // four), four where there is work for all (24 x 512 x 1024: 41 us for the passes, 57 with one), and where a
 // block's CTAs would add up too many partial sums.

@@ -422,10 +422,12 @@ bool chain_class(ChainClass& o, const StackClass& c) {
            encode_stack_tmap(&o.map[kMapB], c.B, c.r8, c.r8, na);
 }
 
-// Tile width of an operation (in 64 columns): the one whose time is least in this model, in us measured on a
-// pair of CTAs: a 64-deep step of the product takes 0.41, 0.29, 0.24 at 256, 128, 64 columns, the epilogue 4.4 (one
-// plane) or 7 (two planes in and out) per 256, and a tile's products overlap the epilogue of the one before.
-// 2 blocks of 320 x 257: 256 columns make 6 tiles and 13 us per operation, 64 columns 22 tiles.
+// Tile width of an operation (in 64 columns): the one whose time is least in this model, in us on a pair of CTAs: a
+// 64-deep step of the product takes 0.41, 0.29, 0.24 at 256, 128, 64 columns, the epilogue 4.4 (one plane) or 7 (two
+// planes in and out) per 256, and a tile's products overlap the epilogue of the one before.  These are a fit to an
+// earlier form of the kernel; its own clock now gives 0.36 and 0.30 for 256 and 64 columns, so narrow tiles are chosen
+// somewhat more often than they should be.  2 blocks of 320 x 257: 256 columns make 6 tiles and 13 us per operation, 64
+// columns 22 tiles.
 int tile_width(const ChainClass& c, ChainOp o, int segments, int pairs) {
     const int kind = o.kind, k = ((kind == 0 ? std::max(c.rp, c.cp) : c.r8) + 63) / 64 * segments;
     const double step[5] = {0.0, 0.24, 0.29, 0.0, 0.41};
