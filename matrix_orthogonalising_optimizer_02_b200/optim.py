@@ -44,7 +44,8 @@ class _Workspaces:
 
     def get(self, nbytes, device):
         ws, own = self.bufs.get(device, (None, None))
-        stream = torch.cuda.current_stream(device)
+        # a host tensor's workspace goes to the call that refuses it
+        stream = torch.cuda.current_stream(device) if torch.device(device).type == "cuda" else None
         if ws is None or ws.numel() < nbytes:
             ws, own = mb.workspace(nbytes, device=device), stream
             self.bufs[device] = ws, own
@@ -244,7 +245,7 @@ class AdamW(_Fp32State):
     def load_state_dict(self, state_dict):
         """Takes a state of torch.optim.AdamW too, where its rule is this one."""
         for g in state_dict["param_groups"]:
-            if g.get("amsgrad") or g.get("maximize") or (g["weight_decay"] and not g.get("decoupled_weight_decay", True)):
+            if g.get("amsgrad") or g.get("maximize") or (g.get("weight_decay") and not g.get("decoupled_weight_decay", True)):
                 raise ValueError("the state is of another rule than AdamW's (amsgrad, maximize or weight decay in the gradient)")
         super().load_state_dict(state_dict)
 

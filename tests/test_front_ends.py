@@ -213,3 +213,12 @@ def test_a_first_step_refuses_a_capture(fake_cuda, monkeypatch):
     with pytest.raises(RuntimeError, match="captured"):
         opt.step()
     assert calls == [1, 1]
+
+
+def test_host_tensors_are_refused_as_such():
+    from matrix_orthogonalising_optimizer_02_b200.optim import AdamW, Muon, MuonCayley, StackedMuon
+    for cls in (AdamW, Muon, MuonCayley, StackedMuon):
+        p = torch.nn.Parameter(torch.ones(16, 8))
+        p.grad = torch.ones_like(p)
+        with pytest.raises(ValueError):
+            cls([p]).step()

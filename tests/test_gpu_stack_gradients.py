@@ -111,3 +111,21 @@ def test_a_schedule_without_a_gradient_is_refused_where_one_is_to_come():
         ms.orthogonalize(x.requires_grad_(True), steps=16)
     (dx,) = torch.autograd.grad(ms.orthogonalize(x, steps=12), x, x.detach())
     assert bool(torch.isfinite(dx).all())
+
+
+def test_gradients_of_many_classes_and_iterations():
+    """More operations than one launch of a chain takes, and more classes; the scales carry over from launch to launch."""
+    coeffs = [ref.STABLE] * 32
+    shapes = [(1 + i % 2, 136 + 8 * i, 300 - 4 * i) for i in range(14)] + [(2, 20 + i, 50) for i in range(3)]
+    xs, dys = [blocks(20 + i, *s, std=0.5) for i, s in enumerate(shapes)], [blocks(60 + i, *s) for i, s in enumerate(shapes)]
+    ys, dxs = [torch.empty_like(x) for x in xs], [torch.empty_like(x) for x in xs]
+    sch = mb.Schedule(coeffs)
+    stacks, grads = [mb.Stack(*p) for p in zip(xs, ys)], [mb.Stack(*p) for p in zip(dys, dxs)]
+    saved = mb.workspace(mb.ns_stacks_saved_size(stacks, sch))
+    mb.ns_orthogonalize_stacks(stacks, sch, mb.workspace(mb.ns_stacks_workspace_size(stacks, sch, True)), saved=saved)
+    back = mb.workspace(mb.ns_stacks_backward_workspace_size(grads, sch))
+    mb.ns_orthogonalize_stacks_backward(grads, sch, saved, back)
+    assert mb.device_status(back) == mb.MUON_OK
+    for i, (x, y, dy, dx) in enumerate(zip(xs, ys, dys, dxs)):
+        assert ref.rel(y[-1], ref.ns(x[-1], coeffs)) <= ref.tol_stable(FP), i
+        assert ref.rel(dx[-1], ref.ns_grad(x[-1], dy[-1], coeffs)) <= ref.tol_stable(FP), i
