@@ -38,7 +38,7 @@
 // operation), gained nothing.
 #include <atomic>
 
-#include "ptx_sm100.cuh"
+#include "ptx_stacks.cuh"
 #include "stacks.cuh"
 
 namespace muon {

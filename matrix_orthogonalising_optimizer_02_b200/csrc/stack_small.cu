@@ -41,6 +41,7 @@
 #include <cmath>
 
 #include "../../include/muon_b200.h"
+#include "ptx_stacks.cuh"
 #include "stacks.cuh"
 #include "typed_io.cuh"
 

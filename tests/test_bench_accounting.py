@@ -75,3 +75,9 @@ def test_recorded_traffic_answers_only_for_the_captured_sources(tmp_path, monkey
         dst.write_bytes(open(os.path.join(bench.ROOT, f), "rb").read())
     monkeypatch.setattr(bench, "ROOT", str(root))
     assert bench.recorded_traffic(4) is None
+
+
+def test_recorded_traffic_belongs_to_the_sources_as_they_are():
+    """The kernel's sources are those of the capture, so the benchmark has its traffic."""
+    assert bench.recorded_traffic(1) == json.load(open(os.path.join(bench.ROOT, "profiles", "tc_gemm_traffic.json")))[
+        "traffic_bytes_per_launch_one_layer"]
